@@ -18,6 +18,13 @@
  *     + the combine (all-to-all back)                   coc_moe_dispatch_grouped_matmul_combine
  *     top-k routing with the gated combine              coc_moe_topk_grouped_matmul_combine
  *
+ * and what stands between and behind those layers in a decode step, every
+ * rank in one call (extension):
+ *   append to a paged 8-bit key/value cache, with
+ *     the position rotation of q and k                  coc_kv_cache_append
+ *   attention over that cache                           coc_kv_cache_attention
+ *   MATMUL_ALL_REDUCE with 4-bit weights                coc_matmul_all_reduce_w4a16
+ *
  * The same page's section 问题分析 ("problem analysis") places them in the
  * Megatron ColumnParallelLinear / RowParallelLinear layers: the matmul is
  * followed by AllReduce without sequence parallelism, by AllGather or
@@ -487,11 +494,135 @@ coc_status_t coc_matmul_all_reduce_noalloc(int R, int64_t m, int64_t n, int64_t 
                                            int chunks, int deterministic, coc_stream_t stream);
 
 /*
+ * Paged key/value cache in 8 bits, one per rank (each rank holds its own
+ * key/value heads).
+ *
+ * k[r], v[r]              pages x kv_heads x page_size x head_dim e4m3 codes
+ *                         (1 byte; 448 is the largest value), packed
+ * k_scale[r], v_scale[r]  pages x kv_heads floats: the value of a code is
+ *                         code * scale of its (page, head); positive, finite
+ * page_size  tokens per page: 16, 32, 64 or 128
+ * head_dim   a multiple of 16, 16 .. 256
+ * R in [1, 8], kv_heads in [1, 1024].  Codes 16-byte, scales 4-byte aligned.
+ *
+ * Sequence s's token at position p is in page block_table[s * table_width +
+ * p / page_size], slot p % page_size.  The ranks share the block table.  No
+ * page belongs to two sequences that a call appends to.  Entries that no
+ * length reaches may hold anything, and so may codes past a length.
+ */
+typedef struct {
+    int R;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+    int64_t pages;
+    void* k[COC_MAX_RANKS];
+    void* v[COC_MAX_RANKS];
+    float* k_scale[COC_MAX_RANKS];
+    float* v_scale[COC_MAX_RANKS];
+} coc_kv_cache_t;
+
+/*
+ * Append the new tokens' keys and values to the cache, rotating q and k by
+ * their positions on the way.
+ *
+ * Sequence s has the new tokens [cu_new[s], cu_new[s+1]) of `tokens` (cu_new
+ * NULL: one each, token s) and holds lens[s] tokens with them, so its new
+ * token i of n is at position p = lens[s] - n + i (p < 0: not appended, its q
+ * is copied).
+ *
+ *   rotation     of the first rot_dim values of a head, pairs (a, b) = values
+ *                (j, j + rot_dim/2), or (2j, 2j+1) if `interleaved`:
+ *                (a cos - b sin, b cos + a sin) with cos, sin [p, j]; fp32,
+ *                every product and sum rounded on its own; cos = sin = NULL:
+ *                no rotation.
+ *   scale        S of a (page, head): the least power of two with
+ *                amax <= 448 S over the page's new values, at least 2^-100; in
+ *                a page that holds earlier tokens not below its scale S0
+ *                before.  A power of two costs e4m3 no precision and changes
+ *                of scale stay exact down to its underflow.
+ *   codes        e4m3(value / S), from the fp32 value, round-to-nearest-even;
+ *                the page's earlier codes c become e4m3(c S0 / S) where S grew.
+ *                NaN stays NaN, infinities become +-448 (neither counts in amax).
+ *   q_out[r]     tokens x q_heads x head_dim, packed: the rotated q, rounded once.
+ *
+ * k[r], v[r]   tokens x kv_heads x head_dim in `dt`; strides {token, head} in
+ *              elements (multiples of 8, the same on every rank), a head's
+ *              values adjacent: slices of a fused QKV output as they are.
+ * q_heads = 0  no q (q, q_strides, q_out unused).
+ * cos, sin     positions x (rot_dim/2) floats, packed.
+ * lens, cu_new, block_table  device int32.
+ * Device arrays that name a page outside the cache or the table, or a position
+ * outside cos/sin: the page's new tokens are left out (q copied), and
+ * coc_sync_status reports COC_ERR_INVALID_ARG.
+ * One kernel on `stream`, no scratch.  Appending the same tokens again leaves
+ * the cache as it is.
+ */
+coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, int64_t seqs,
+                                 const void* const* k, const int64_t* k_strides,
+                                 const void* const* v, const int64_t* v_strides,
+                                 int q_heads, const void* const* q, const int64_t* q_strides, void* const* q_out,
+                                 const int32_t* block_table, int64_t table_width, const int32_t* lens,
+                                 const int32_t* cu_new, const float* cos, const float* sin, int64_t positions,
+                                 int rot_dim, int interleaved, coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds them already).
+ *
+ * Query head h of new token i of n of sequence s reads key/value head
+ * h / (q_heads / kv_heads) and sees the positions j < E = lens[s] - (n-1-i)
+ * with, if window > 0, also j >= E - window or j < sinks:
+ *
+ *   out = sum_j softmax_j(scale q.k_j) v_j     (k, v = code * scale of the page)
+ *
+ * in fp32 with one rounding at the end; a row that sees no key is zero.
+ * Positions that a row does not see take no part in it whatever they hold.
+ *
+ * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append
+ * out[r]  tokens x q_heads x head_dim, packed
+ * window  0: every earlier key; sinks needs a window.
+ * Other arguments as coc_kv_cache_append.  Pages outside the cache, and
+ * positions past the table, are left out, and coc_sync_status reports
+ * COC_ERR_INVALID_ARG.  Results do not depend on what else is in the batch's
+ * memory or on timing: splits of the keys go by the lengths and the GPU only
+ * and are added in a fixed order.
+ */
+coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t tokens, int64_t seqs, int q_heads,
+                                    const void* const* q, const int64_t* q_strides, void* const* out,
+                                    const int32_t* block_table, int64_t table_width, const int32_t* lens,
+                                    const int32_t* cu_new, float scale, int64_t window, int64_t sinks,
+                                    coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * w4A16 MATMUL_ALL_REDUCE for decode-sized m: as coc_matmul_all_reduce_w8a16
+ * with per-group scales, and 4-bit weights.
+ *
+ *   Y = sum_r sum_t X_r[:, t] * (code_r(t, j) - z_r(t, j)) * s_r(t, j);  out[r] = rne(Y) for every r
+ *
+ * summed in fp32, the weight itself never rounded.
+ * x[r]      m x k_shard in `dt`
+ * w[r]      (k_shard/8) x n 32-bit words; bits 4i .. 4i+3 of word (t, j) are
+ *           the code, 0 .. 15, of weight (8t + i, j)
+ * scale[r]  (k_shard/group_size) x n in `dt`
+ * zero      NULL (z = 8) or per rank (k_shard/group_size) x n int8
+ * group_size  a multiple of 32 dividing k_shard;  n % 8 == 0;  m <= 65536 (it
+ *           is built for up to 16 rows; more are taken 16 at a time, reading
+ *           the weights again).  Pointers 16-byte aligned.
+ * m == 0 or n == 0 is a no-op, k_shard == 0 writes zeros.
+ */
+coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, int64_t k_shard,
+                                         const void* const* x, const void* const* w,
+                                         const void* const* scale, const void* const* zero,
+                                         int64_t group_size, void* const* out,
+                                         coc_dtype_t dt, coc_stream_t stream);
+
+/*
  * Waits for `stream`, then returns and clears the device-side status of
  * this library on the current device (the status buffer of the allocating
  * entry points and the static block of coc_matmul_all_reduce_noalloc):
  * COC_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * COC_ERR_INVALID_ARG if a MoE dispatch met an expert id out of range,
+ * COC_ERR_INVALID_ARG if a MoE dispatch met an expert id out of range or a
+ * cache operator a page, length or position outside its table,
  * COC_ERR_CUDA if the stream reports an error, COC_OK otherwise.  It creates
  * no library state and allocates nothing.
  */

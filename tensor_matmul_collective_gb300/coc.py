@@ -30,13 +30,21 @@ EXPORTS = (
     "coc_debug_inject_timeout", "coc_shutdown", "coc_matmul_all_reduce_noalloc",
     "coc_fused_matmul", "coc_matmul_all_reduce_w8a16_ex", "coc_moe_dispatch_grouped_matmul", "coc_moe_capacity",
     "coc_moe_dispatch_grouped_matmul_combine", "coc_moe_topk_grouped_matmul_combine", "coc_debug_alloc_count",
-    "coc_debug_clock_probe", "coc_debug_clock_read",
+    "coc_debug_clock_probe", "coc_debug_clock_read", "coc_kv_cache_append", "coc_kv_cache_attention",
+    "coc_matmul_all_reduce_w4a16",
 )
 
 OP_ALL_REDUCE, OP_REDUCE_SCATTER, OP_ALL_GATHER, OP_ALL_GATHER_V2, OP_WEIGHT_GRAD = range(5)
 _OPS = {"all_reduce": OP_ALL_REDUCE, "reduce_scatter": OP_REDUCE_SCATTER,
         "all_gather": OP_ALL_GATHER, "all_gather_v2": OP_ALL_GATHER_V2}
 W_KN, W_NK = 0, 1
+
+
+class _KVCacheDesc(ctypes.Structure):
+    """coc_kv_cache_t."""
+    _fields_ = [("R", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("pages", ctypes.c_int64), ("k", ctypes.c_void_p * MAX_RANKS), ("v", ctypes.c_void_p * MAX_RANKS),
+                ("k_scale", ctypes.c_void_p * MAX_RANKS), ("v_scale", ctypes.c_void_p * MAX_RANKS)]
 
 
 class CocError(RuntimeError):
@@ -88,6 +96,14 @@ def lib() -> ctypes.CDLL:
             L.coc_fused_matmul.restype = i32
             L.coc_matmul.argtypes = [i32, i64, i64, i64, pp, pp, vp, i32, vp]
             L.coc_matmul.restype = i32
+            L.coc_kv_cache_append.argtypes = [vp, i64, i64, pp, vp, pp, vp, i32, pp, vp, pp, vp, i64, vp, vp, vp, vp, i64,
+                                              i32, i32, i32, vp]
+            L.coc_kv_cache_append.restype = i32
+            L.coc_kv_cache_attention.argtypes = [vp, i64, i64, i32, pp, vp, pp, vp, i64, vp, vp, ctypes.c_float, i64, i64,
+                                                 i32, vp]
+            L.coc_kv_cache_attention.restype = i32
+            L.coc_matmul_all_reduce_w4a16.argtypes = [i32, i64, i64, i64, pp, pp, pp, pp, i64, pp, i32, vp]
+            L.coc_matmul_all_reduce_w4a16.restype = i32
             L.coc_sync_status.argtypes = [vp]
             L.coc_sync_status.restype = i32
             L.coc_status_string.argtypes = [i32]
@@ -465,6 +481,205 @@ def moe_topk_grouped_matmul_combine(xs, idxs, gates, w, experts_per_rank: int, x
                                                      cap, counts.data_ptr(), offsets.data_ptr(), _dtype_code(dt),
                                                      _stream(stream)))
     return y_tok, y, xd, counts, offsets
+
+
+class KVCache:
+    """The ranks' paged key/value caches in 8 bits, as kv_cache_append and kv_cache_attention take them.
+
+    k[r], v[r]: (pages, kv_heads, page_size, head_dim) float8_e4m3fn codes;
+    k_scale[r], v_scale[r]: (pages, kv_heads) float32, the value of a code is
+    code * scale.  The tensors stay the caller's (``empty`` allocates them);
+    the object holds references and their addresses, checked once here."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if not isinstance(k, (list, tuple)) or not 1 <= len(k) <= MAX_RANKS:
+            raise ValueError(f"k must be a list of 1..{MAX_RANKS} tensors, one per rank")
+        if any(len(x) != len(k) for x in (v, k_scale, v_scale)):
+            raise ValueError("k, v, k_scale and v_scale need one tensor per rank")
+        c = k[0]
+        if not isinstance(c, torch.Tensor) or c.dim() != 4:
+            raise ValueError("cache codes must be (pages, kv_heads, page_size, head_dim)")
+        _check_device(c)
+        _check_list(k, "k", c.shape, torch.float8_e4m3fn, c.device)
+        _check_list(v, "v", c.shape, torch.float8_e4m3fn, c.device)
+        _check_list(k_scale, "k_scale", c.shape[:2], torch.float32, c.device)
+        _check_list(v_scale, "v_scale", c.shape[:2], torch.float32, c.device)
+        self.k, self.v, self.k_scale, self.v_scale = list(k), list(v), list(k_scale), list(v_scale)
+        self.R, self.device = len(k), c.device
+        self.pages, self.kv_heads, self.page_size, self.head_dim = c.shape
+        d = _KVCacheDesc(R=self.R, page_size=self.page_size, kv_heads=self.kv_heads, head_dim=self.head_dim, pages=self.pages)
+        for field, ts in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            for r, t in enumerate(ts):
+                getattr(d, field)[r] = t.data_ptr()
+        self._desc = d
+        self._ref = ctypes.addressof(d)
+
+    @classmethod
+    def empty(cls, R: int, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        """A zeroed cache of `pages` pages on every rank."""
+        def codes():
+            return torch.zeros((pages, kv_heads, page_size, head_dim), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+
+        def scales():
+            return torch.zeros((pages, kv_heads), dtype=torch.float32, device=device)
+        return cls([codes() for _ in range(R)], [codes() for _ in range(R)], [scales() for _ in range(R)],
+                   [scales() for _ in range(R)])
+
+
+_I64x2 = ctypes.c_int64 * 2
+
+
+def _check_heads(ts, name, R, tokens, d, dtype, device):
+    """R tensors of tokens x heads x d with the same strides, a head's values
+    adjacent (slices of a fused projection's output pass)."""
+    if not isinstance(ts, (list, tuple)) or len(ts) != R:
+        raise ValueError(f"{name} must be a list of {R} tensors, one per rank")
+    t0 = ts[0]
+    if not isinstance(t0, torch.Tensor):
+        raise TypeError(f"{name}[0] is not a tensor")
+    shape, stride = t0.shape, t0.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != d:
+        raise ValueError(f"{name}[0] has shape {tuple(shape)}, expected ({tokens}, heads, {d})")
+    if stride[2] != 1 and d > 1:
+        raise ValueError(f"{name}: the values of a head must be adjacent")
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+            raise TypeError(f"{name}[{i}] must be a {dtype} tensor")
+        if t.device != device:
+            raise ValueError(f"{name}[{i}] is on {t.device}, expected {device}")
+        if t.shape != shape or t.stride() != stride:
+            raise ValueError(f"{name}[{i}] has another shape or other strides than {name}[0]")
+    return shape[1], _I64x2(stride[0], stride[1])
+
+
+def _check_seqs(cache, tokens, block_table, lens, cu_new):
+    """(sequences, table width) of the arrays that index the cache."""
+    seqs = lens.shape[0] if lens.dim() == 1 else -1
+    if seqs < 0 or block_table.dim() != 2 or block_table.shape[0] != seqs:
+        raise ValueError("lens must be (sequences,) and block_table (sequences, pages per sequence)")
+    for name, t in (("block_table", block_table), ("lens", lens), ("cu_new", cu_new)):
+        if t is not None and (t.dtype is not torch.int32 or t.device != cache.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {cache.device}")
+    if cu_new is None:
+        if tokens != seqs:
+            raise ValueError(f"without cu_new every sequence has one new token: {tokens} tokens, {seqs} sequences")
+    elif cu_new.dim() != 1 or cu_new.shape[0] != seqs + 1:
+        raise ValueError(f"cu_new must have {seqs + 1} entries")
+    return seqs, block_table.shape[1]
+
+
+def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=None, q_outs=None, cu_new=None,
+                    interleaved: bool = False, stream=None):
+    """Append the new tokens' keys and values to the cache, with the position rotation of q and k.
+
+    ks[r], vs[r]: tokens x kv_heads x head_dim (fp16/bf16, token and head
+    strides free); qs[r]: tokens x q_heads x head_dim or None.  Sequence s has
+    the new tokens cu_new[s] .. cu_new[s+1]-1 (cu_new None: one each) and
+    lens[s] tokens in the cache with them; block_table[s, p // page_size] is
+    the page of its position p.  cos, sin: float32 positions x rot_dim/2, or
+    None for no rotation; interleaved pairs values 2j, 2j+1 instead of
+    j, j + rot_dim/2.  Returns the rotated q of every rank (tokens x q_heads x
+    head_dim), None without qs."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    if not isinstance(ks, (list, tuple)) or not ks or not isinstance(ks[0], torch.Tensor) or ks[0].dim() != 3:
+        raise ValueError("ks must be a list of tokens x kv_heads x head_dim tensors, one per rank")
+    k0, R, d, dev = ks[0], cache.R, cache.head_dim, cache.device
+    _check_device(k0)
+    code = _dtype_code(k0.dtype)
+    T = k0.shape[0]
+    hk, kstr = _check_heads(ks, "ks", R, T, d, k0.dtype, dev)
+    hv, vstr = _check_heads(vs, "vs", R, T, d, k0.dtype, dev)
+    if hk != cache.kv_heads or hv != cache.kv_heads:
+        raise ValueError(f"ks and vs must have the cache's {cache.kv_heads} heads")
+    seqs, width = _check_seqs(cache, T, block_table, lens, cu_new)
+    hq, qstr, qp, qop = 0, None, None, None
+    if qs is not None:
+        hq, qstr = _check_heads(qs, "qs", R, T, d, k0.dtype, dev)
+        q_outs = _outs(q_outs, R, (T, hq, d), k0.dtype, dev)
+        qp, qop = _ptrs(qs), _ptrs(q_outs)
+    elif q_outs is not None:
+        raise ValueError("q_outs without qs")
+    cp = sp = None
+    positions = rot = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("cos and sin are two float32 tensors (positions, rot_dim / 2)")
+        _check_list((cos, sin), "cos/sin", cos.shape, torch.float32, dev)
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    _check(lib().coc_kv_cache_append(cache._ref, T, seqs, _ptrs(ks), kstr, _ptrs(vs), vstr, hq, qp, qstr, qop,
+                                     block_table.data_ptr(), width, lens.data_ptr(),
+                                     None if cu_new is None else cu_new.data_ptr(), cp, sp, positions, rot,
+                                     int(bool(interleaved)), code, _stream(stream)))
+    return q_outs
+
+
+def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, window: int = 0, sinks: int = 0, outs=None,
+                       stream=None):
+    """Attention of the new tokens over the cache that holds them already (kv_cache_append).
+
+    qs[r]: tokens x q_heads x head_dim (fp16/bf16, strides free), q_heads a
+    multiple of the cache's heads; lens, block_table, cu_new as in
+    kv_cache_append.  New token i of n sees the first E = lens[s] - (n-1-i)
+    positions; with window > 0 only the last `window` of them and the first
+    `sinks`.  scale defaults to head_dim ** -0.5.  Returns outs, one tokens x
+    q_heads x head_dim tensor per rank; a row that sees no key is zero."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    if not isinstance(qs, (list, tuple)) or not qs or not isinstance(qs[0], torch.Tensor) or qs[0].dim() != 3:
+        raise ValueError("qs must be a list of tokens x q_heads x head_dim tensors, one per rank")
+    q0, R, d, dev = qs[0], cache.R, cache.head_dim, cache.device
+    _check_device(q0)
+    code = _dtype_code(q0.dtype)
+    T = q0.shape[0]
+    hq, qstr = _check_heads(qs, "qs", R, T, d, q0.dtype, dev)
+    seqs, width = _check_seqs(cache, T, block_table, lens, cu_new)
+    outs = _outs(outs, R, (T, hq, d), q0.dtype, dev)
+    _check(lib().coc_kv_cache_attention(cache._ref, T, seqs, hq, _ptrs(qs), qstr, _ptrs(outs), block_table.data_ptr(),
+                                        width, lens.data_ptr(), None if cu_new is None else cu_new.data_ptr(),
+                                        d ** -0.5 if scale is None else float(scale), int(window), int(sinks), code,
+                                        _stream(stream)))
+    return outs
+
+
+def matmul_all_reduce_w4a16(xs, wqs, scales, group_size: int, zeros=None, outs=None, stream=None):
+    """w4A16 MATMUL_ALL_REDUCE at decode-sized m: outs[r] = sum_q xs[q] @ ((code_q - z_q) * s_q) for every r.
+
+    xs[q]: m x k_shard (fp16/bf16); wqs[q]: (k_shard/8) x n int32, eight 4-bit
+    codes along k in a word (w4_pack); scales[q]: (k_shard/group_size) x n in
+    the activations' type; zeros: None (z = 8) or int8 tensors like scales."""
+    R, x0, w0 = _prep(xs, wqs)
+    m, ks = x0.shape
+    n = w0.shape[1]
+    dt, dev = x0.dtype, x0.device
+    code = _dtype_code(dt)
+    if ks % 8 or group_size < 1 or ks % group_size:
+        raise CocError(ERR_SHAPE, "COC_ERR_SHAPE", f"k_shard = {ks} is not a multiple of 8 and of group_size = {group_size}")
+    _check_list(xs, "xs", (m, ks), dt, dev)
+    _check_list(wqs, "wqs", (ks // 8, n), torch.int32, dev)
+    for name, views, want in (("scales", scales, dt), ("zeros", zeros, torch.int8)):
+        if views is None:
+            continue
+        if len(views) != R:
+            raise ValueError(f"need one {name} tensor per rank")
+        _check_list(views, name, (ks // group_size, n), want, dev)
+    outs = _outs(outs, R, (m, n), dt, dev)
+    _check(lib().coc_matmul_all_reduce_w4a16(R, m, n, ks, _ptrs(xs), _ptrs(wqs), _ptrs(scales),
+                                             None if zeros is None else _ptrs(zeros), int(group_size), _ptrs(outs), code,
+                                             _stream(stream)))
+    return outs
+
+
+def w4_pack(codes):
+    """The words matmul_all_reduce_w4a16 takes: codes (k, n), integers 0..15, k a
+    multiple of 8 -> (k/8, n) int32, code (8t + i, j) in bits 4i..4i+3 of word (t, j)."""
+    if codes.dim() != 2 or codes.shape[0] % 8:
+        raise ValueError("codes must be (k, n) with k a multiple of 8")
+    k, n = codes.shape
+    bits = torch.arange(0, 32, 4, device=codes.device, dtype=torch.int64)[None, :, None]
+    words = ((codes.to(torch.int64) & 15).view(k // 8, 8, n) << bits).sum(1)
+    return torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
 
 
 def matmul(xs, ws, out=None, stream=None):

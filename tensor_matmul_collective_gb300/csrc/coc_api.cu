@@ -1501,6 +1501,213 @@ COC_API coc_status_t coc_moe_topk_grouped_matmul_combine(int R, int64_t tokens, 
                     dt, stream);
 }
 
+// ---- the attention block of a decode step: paged 8-bit cache, 4-bit weights ----
+
+// The cache descriptor and the arrays that index it, shared by the two calls.
+static coc_status_t check_kv(const coc_kv_cache_t* c, int64_t tokens, int64_t seqs, const int32_t* table,
+                             int64_t table_width, const int32_t* lens, const int32_t* cu, coc_dtype_t dt) {
+    if (c == nullptr) return fail(COC_ERR_INVALID_ARG, "cache is NULL");
+    if (c->R < 1 || c->R > COC_MAX_RANKS) return fail(COC_ERR_INVALID_ARG, "R = %d outside [1, %d]", c->R, COC_MAX_RANKS);
+    if (dt != COC_FP16 && dt != COC_BF16) return fail(COC_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dt));
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return fail(COC_ERR_SHAPE, "page_size = %d; must be 16, 32, 64 or 128", c->page_size);
+    if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16 != 0)
+        return fail(COC_ERR_SHAPE, "head_dim = %d; must be a multiple of 16 up to 256", c->head_dim);
+    if (c->kv_heads < 1 || c->kv_heads > 1024) return fail(COC_ERR_SHAPE, "kv_heads = %d outside [1, 1024]", c->kv_heads);
+    if (c->pages < 0 || c->pages > kMaxDim) return fail(COC_ERR_SHAPE, "pages = %lld", (long long)c->pages);
+    if (tokens < 0 || tokens > (int64_t(1) << 24)) return fail(COC_ERR_SHAPE, "tokens = %lld outside [0, 2^24]", (long long)tokens);
+    if (seqs < 0 || seqs > (int64_t(1) << 16)) return fail(COC_ERR_SHAPE, "sequences = %lld outside [0, 2^16]", (long long)seqs);
+    if (table_width < 0 || table_width > (int64_t(1) << 24)) return fail(COC_ERR_SHAPE, "table width = %lld", (long long)table_width);
+    if (tokens > 0 && seqs == 0) return fail(COC_ERR_SHAPE, "%lld tokens of no sequence", (long long)tokens);
+    if (cu == nullptr && tokens != seqs)
+        return fail(COC_ERR_SHAPE, "without offsets every sequence has one token: %lld tokens, %lld sequences",
+                    (long long)tokens, (long long)seqs);
+    if (tokens == 0) return COC_OK;
+    if (lens == nullptr || (table == nullptr && table_width > 0)) return fail(COC_ERR_INVALID_ARG, "block table or lens is NULL");
+    if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(cu)) & 3u)
+        return fail(COC_ERR_ALIGN, "block table, lens or offsets not 4-byte aligned");
+    if (c->pages > 0)
+        for (int r = 0; r < c->R; ++r) {
+            if (c->k[r] == nullptr || c->v[r] == nullptr || c->k_scale[r] == nullptr || c->v_scale[r] == nullptr)
+                return fail(COC_ERR_INVALID_ARG, "rank %d of the cache has a NULL buffer", r);
+            if (!aligned16(c->k[r]) || !aligned16(c->v[r])) return fail(COC_ERR_ALIGN, "rank %d's codes are not 16-byte aligned", r);
+            if ((reinterpret_cast<uintptr_t>(c->k_scale[r]) | reinterpret_cast<uintptr_t>(c->v_scale[r])) & 3u)
+                return fail(COC_ERR_ALIGN, "rank %d's scales are not 4-byte aligned", r);
+        }
+    return COC_OK;
+}
+
+// Token and head strides in elements: non-negative, rows on 16-byte boundaries.
+static coc_status_t check_strides(const int64_t* s, const char* name) {
+    if (s == nullptr) return fail(COC_ERR_INVALID_ARG, "%s strides are NULL", name);
+    for (int i = 0; i < 2; ++i) {
+        if (s[i] < 0 || s[i] > kMaxDim) return fail(COC_ERR_SHAPE, "%s stride %lld", name, (long long)s[i]);
+        if (s[i] % 8 != 0) return fail(COC_ERR_ALIGN, "%s stride %lld: rows must start on 16-byte boundaries", name, (long long)s[i]);
+    }
+    return COC_OK;
+}
+
+COC_API coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, int64_t seqs,
+                                         const void* const* k, const int64_t* k_strides, const void* const* v,
+                                         const int64_t* v_strides, int q_heads, const void* const* q,
+                                         const int64_t* q_strides, void* const* q_out, const int32_t* block_table,
+                                         int64_t table_width, const int32_t* lens, const int32_t* cu_new,
+                                         const float* cos, const float* sin, int64_t positions, int rot_dim,
+                                         int interleaved, coc_dtype_t dt, coc_stream_t stream) {
+    coc_status_t st = check_kv(cache, tokens, seqs, block_table, table_width, lens, cu_new, dt);
+    if (st != COC_OK) return st;
+    if (q_heads < 0 || q_heads > 65535) return fail(COC_ERR_SHAPE, "q_heads = %d outside [0, 65535]", q_heads);
+    if ((cos == nullptr) != (sin == nullptr)) return fail(COC_ERR_INVALID_ARG, "cos and sin are given together or not at all");
+    if (cos != nullptr) {
+        if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > cache->head_dim)
+            return fail(COC_ERR_SHAPE, "rot_dim = %d; must be even, in [2, head_dim]", rot_dim);
+        if (positions < 0 || positions > kMaxDim) return fail(COC_ERR_SHAPE, "positions = %lld", (long long)positions);
+        if ((reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) & 3u)
+            return fail(COC_ERR_ALIGN, "cos or sin not 4-byte aligned");
+    }
+    if (tokens == 0) return COC_OK;
+    const int R = cache->R;
+    if ((st = check_ptrs(k, R, true, "k")) != COC_OK || (st = check_ptrs(v, R, true, "v")) != COC_OK) return st;
+    if ((st = check_strides(k_strides, "k")) != COC_OK || (st = check_strides(v_strides, "v")) != COC_OK) return st;
+    if (q_heads > 0) {
+        if ((st = check_ptrs(q, R, true, "q")) != COC_OK || (st = check_ptrs(q_out, R, true, "q_out")) != COC_OK) return st;
+        if ((st = check_strides(q_strides, "q")) != COC_OK) return st;
+    }
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != COC_OK) return st;
+    KvAppendArgs a;
+    std::memset(&a, 0, sizeof a);
+    for (int r = 0; r < R; ++r) {
+        a.ck[r] = static_cast<uint8_t*>(cache->k[r]);
+        a.cv[r] = static_cast<uint8_t*>(cache->v[r]);
+        a.sk[r] = cache->k_scale[r];
+        a.sv[r] = cache->v_scale[r];
+        a.k[r] = static_cast<const uint16_t*>(k[r]);
+        a.v[r] = static_cast<const uint16_t*>(v[r]);
+        if (q_heads > 0) {
+            a.q[r] = static_cast<const uint16_t*>(q[r]);
+            a.q_out[r] = static_cast<uint16_t*>(q_out[r]);
+        }
+    }
+    a.table = block_table;
+    a.lens = lens;
+    a.cu = cu_new;
+    a.cos = cos;
+    a.sin = sin;
+    a.status = ds->status;
+    a.k_token = k_strides[0];
+    a.k_head = k_strides[1];
+    a.v_token = v_strides[0];
+    a.v_head = v_strides[1];
+    if (q_heads > 0) {
+        a.q_token = q_strides[0];
+        a.q_head = q_strides[1];
+    }
+    a.table_width = table_width;
+    a.pages = cache->pages;
+    a.positions = positions;
+    a.R = R;
+    a.seqs = static_cast<int>(seqs);
+    a.tokens = static_cast<int>(tokens);
+    a.heads = cache->kv_heads;
+    a.q_heads = q_heads;
+    a.d = cache->head_dim;
+    a.page = cache->page_size;
+    a.rot = cos != nullptr ? rot_dim : 0;
+    a.interleaved = interleaved != 0;
+    const cudaError_t e = launch_kv_append(a, dt == COC_BF16, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? COC_OK : cuda_fail(e, "KV append launch");
+}
+
+COC_API coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t tokens, int64_t seqs, int q_heads,
+                                            const void* const* q, const int64_t* q_strides, void* const* out,
+                                            const int32_t* block_table, int64_t table_width, const int32_t* lens,
+                                            const int32_t* cu_new, float scale, int64_t window, int64_t sinks,
+                                            coc_dtype_t dt, coc_stream_t stream) {
+    coc_status_t st = check_kv(cache, tokens, seqs, block_table, table_width, lens, cu_new, dt);
+    if (st != COC_OK) return st;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads != 0)
+        return fail(COC_ERR_SHAPE, "q_heads = %d; must be a multiple of the %d key/value heads, up to 65535", q_heads, cache->kv_heads);
+    if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
+        return fail(COC_ERR_INVALID_ARG, "window = %lld, sinks = %lld: neither negative, sinks only with a window",
+                    (long long)window, (long long)sinks);
+    if (tokens == 0) return COC_OK;
+    const int R = cache->R;
+    if ((st = check_ptrs(q, R, true, "q")) != COC_OK || (st = check_ptrs(out, R, true, "out")) != COC_OK) return st;
+    if ((st = check_strides(q_strides, "q")) != COC_OK) return st;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != COC_OK) return st;
+    KvAttnArgs a;
+    std::memset(&a, 0, sizeof a);
+    for (int r = 0; r < R; ++r) {
+        a.ck[r] = static_cast<const uint8_t*>(cache->k[r]);
+        a.cv[r] = static_cast<const uint8_t*>(cache->v[r]);
+        a.sk[r] = cache->k_scale[r];
+        a.sv[r] = cache->v_scale[r];
+        a.q[r] = static_cast<const uint16_t*>(q[r]);
+        a.out[r] = static_cast<uint16_t*>(out[r]);
+    }
+    a.table = block_table;
+    a.lens = lens;
+    a.cu = cu_new;
+    a.status = ds->status;
+    a.q_token = q_strides[0];
+    a.q_head = q_strides[1];
+    a.table_width = table_width;
+    a.pages = cache->pages;
+    a.scale = scale;
+    a.R = R;
+    a.seqs = static_cast<int>(seqs);
+    a.tokens = static_cast<int>(tokens);
+    a.heads = cache->kv_heads;
+    a.q_heads = q_heads;
+    a.d = cache->head_dim;
+    a.page = cache->page_size;
+    a.window = static_cast<int>(std::min<int64_t>(window, kMaxDim));
+    a.sinks = static_cast<int>(std::min<int64_t>(sinks, kMaxDim));
+    const cudaError_t e = launch_kv_attention(a, dt == COC_BF16, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? COC_OK : cuda_fail(e, "KV attention launch");
+}
+
+COC_API coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, int64_t k_shard, const void* const* x,
+                                                 const void* const* w, const void* const* scale,
+                                                 const void* const* zero, int64_t group_size, void* const* out,
+                                                 coc_dtype_t dt, coc_stream_t stream) {
+    coc_status_t st = check_common(R, 1, dt, 0);
+    if (st != COC_OK) return st;
+    if ((st = check_dims(m, n, k_shard)) != COC_OK) return st;
+    if (m > (int64_t(1) << 16)) return fail(COC_ERR_SHAPE, "m = %lld above 2^16", (long long)m);
+    if (group_size < 32 || group_size % 32 != 0 || k_shard % group_size != 0)
+        return fail(COC_ERR_SHAPE, "group_size = %lld; must be a multiple of 32 that divides k_shard = %lld",
+                    (long long)group_size, (long long)k_shard);
+    if (n % 8 != 0) return fail(COC_ERR_ALIGN, "n = %lld: rows of the outputs must span a multiple of 16 bytes", (long long)n);
+    if ((st = check_ptrs(out, R, m > 0 && n > 0, "out")) != COC_OK) return st;
+    const bool needed = m > 0 && n > 0 && k_shard > 0;
+    if ((st = check_ptrs(x, R, needed, "x")) != COC_OK || (st = check_ptrs(w, R, needed, "w")) != COC_OK ||
+        (st = check_ptrs(scale, R, needed, "scale")) != COC_OK)
+        return st;
+    if (zero != nullptr && (st = check_ptrs(zero, R, needed, "zero")) != COC_OK) return st;
+    if (m == 0 || n == 0) return COC_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != COC_OK) return st;
+    W4Args a;
+    std::memset(&a, 0, sizeof a);
+    for (int r = 0; r < R; ++r) {
+        a.x[r] = static_cast<const uint16_t*>(x[r]);
+        a.w[r] = static_cast<const uint32_t*>(w[r]);
+        a.scale[r] = static_cast<const uint16_t*>(scale[r]);
+        a.zero[r] = zero != nullptr ? static_cast<const int8_t*>(zero[r]) : nullptr;
+        a.out[r] = static_cast<uint16_t*>(out[r]);
+    }
+    a.R = R;
+    a.m = static_cast<int>(m);
+    a.n = static_cast<int>(n);
+    a.k = static_cast<int>(k_shard);
+    a.group = static_cast<int>(group_size);
+    const cudaError_t e = launch_w4(a, dt == COC_BF16, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? COC_OK : cuda_fail(e, "w4A16 launch");
+}
+
 // Status words of the current device's library state, read and cleared; all
 // zero (and nothing created) when no allocating call has run on the device.
 static coc_status_t take_library_status(unsigned (&words)[STATUS_WORDS]) {
@@ -1532,6 +1739,9 @@ COC_API coc_status_t coc_sync_status(coc_stream_t stream) {
     if ((st = noalloc_take_status(na_words)) != COC_OK) return st;
     const unsigned* words = lib_words[0] != 0 ? lib_words : na_words;
     if (words[0] != 0) {
+        if ((words[0] & (DEV_ERR_TIMEOUT | DEV_ERR_BAD_PAGE)) == DEV_ERR_BAD_PAGE)
+            return fail(COC_ERR_INVALID_ARG, "KV cache: a page id, a length or a position was outside its table; those "
+                        "tokens were left out%s", words[0] & DEV_ERR_BAD_INDEX ? " (and an expert id outside [0, E))" : "");
         if (words[0] == DEV_ERR_BAD_INDEX)
             return fail(COC_ERR_INVALID_ARG, "MoE dispatch: an expert id was outside [0, E); those tokens were not dispatched");
         return fail(COC_ERR_TIMEOUT, "device wait timed out%s (flags 0x%x, first wait site 0x%x, block %u)",

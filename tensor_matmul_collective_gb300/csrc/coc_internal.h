@@ -29,7 +29,7 @@ enum OpKind : int { OP_AR = 0, OP_RS = 1, OP_AG = 2, OP_W8 = 3, OP_GMM = 4 };
 constexpr int NUM_OPS = 5;
 
 // Device status words (per device, zero when healthy).
-enum : unsigned { DEV_ERR_TIMEOUT = 1u, DEV_ERR_BAD_INDEX = 2u };
+enum : unsigned { DEV_ERR_TIMEOUT = 1u, DEV_ERR_BAD_INDEX = 2u, DEV_ERR_BAD_PAGE = 4u };
 constexpr int STATUS_WORDS = 8;   // [0] error bits, [1] first "where" code, [2] block
 // After the status words, CLOCK_SLOTS clock-probe slots of two uint64 each
 // (SM cycles, ns) accumulated by block 0 of every fused-kernel launch made
@@ -186,6 +186,60 @@ struct MoeCombineArgs {
 cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream);
 cudaError_t launch_moe_permute(const MoePermuteArgs& a, int sm_count, cudaStream_t stream);
 cudaError_t launch_moe_combine(const MoeCombineArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+
+// Paged 8-bit key/value cache (coc_kv_append.cu, coc_kv_attention.cu).  Codes
+// are pages x heads x page x d bytes per rank, scales pages x heads floats.
+// cu: seqs + 1 offsets into the new tokens, NULL for one token a sequence.
+// Strides are in elements.  Pages outside [0, pages) or past the table, and
+// positions past the rotation tables, set DEV_ERR_BAD_PAGE and are left out.
+struct KvAppendArgs {
+    uint8_t* ck[COC_MAX_RANKS];
+    uint8_t* cv[COC_MAX_RANKS];
+    float* sk[COC_MAX_RANKS];
+    float* sv[COC_MAX_RANKS];
+    const uint16_t* q[COC_MAX_RANKS];
+    const uint16_t* k[COC_MAX_RANKS];
+    const uint16_t* v[COC_MAX_RANKS];
+    uint16_t* q_out[COC_MAX_RANKS];      // tokens x q_heads x d, packed
+    const int32_t* table;                // seqs x table_width page ids
+    const int32_t* lens;                 // seqs: tokens in the cache, the new ones included
+    const int32_t* cu;
+    const float* cos;                    // positions x rot / 2; NULL: no rotation
+    const float* sin;
+    unsigned* status;
+    long long q_token, q_head, k_token, k_head, v_token, v_head;
+    long long table_width, pages, positions;
+    int R, seqs, tokens, heads, q_heads, d, page, rot, interleaved;
+};
+struct KvAttnArgs {
+    const uint8_t* ck[COC_MAX_RANKS];
+    const uint8_t* cv[COC_MAX_RANKS];
+    const float* sk[COC_MAX_RANKS];
+    const float* sv[COC_MAX_RANKS];
+    const uint16_t* q[COC_MAX_RANKS];
+    uint16_t* out[COC_MAX_RANKS];        // tokens x q_heads x d, packed
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;
+    unsigned* status;
+    long long q_token, q_head, table_width, pages;
+    float scale;
+    int R, seqs, tokens, heads, q_heads, d, page, window, sinks;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, cudaStream_t stream);
+
+// Row-parallel products with 4-bit weights (coc_w4.cu): w holds 8 codes along
+// k in a word (k / 8 x n words per rank), scales and zero points k / group x n.
+struct W4Args {
+    const uint16_t* x[COC_MAX_RANKS];    // m x k
+    const uint32_t* w[COC_MAX_RANKS];
+    const uint16_t* scale[COC_MAX_RANKS];
+    const int8_t* zero[COC_MAX_RANKS];   // NULL: 8 everywhere
+    uint16_t* out[COC_MAX_RANKS];        // m x n
+    int R, m, n, k, group;
+};
+cudaError_t launch_w4(const W4Args& a, bool bf16, cudaStream_t stream);
 
 // Host-side launch helpers implemented in coc_kernel.cu.  `pair` selects the
 // 2-SM variant (a cluster of two CTAs per 256-row tile; grid = 2 x pairs);

@@ -1,0 +1,56 @@
+// Shared by the paged 8-bit key/value cache kernels (coc_kv_append.cu,
+// coc_kv_attention.cu): the cache as the kernels see it, the lookup of a new
+// token's sequence, and the scale rule.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "coc_internal.h"
+
+namespace coc {
+namespace {
+
+// Largest e4m3 value, and the least exponent a page's scale takes (an all-zero
+// page would otherwise have none; 2^-100 keeps code * scale a normal fp32).
+constexpr float kE4M3Max = 448.f;
+constexpr int kMinScaleExp = -100;
+
+template <bool BF16>
+__device__ __forceinline__ float to_float16bit(uint16_t v) {
+    if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    else return __half2float(__ushort_as_half(v));
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t from_float16bit(float f) {
+    if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
+    else return __half_as_ushort(__float2half_rn(f));
+}
+
+// Least power of two s with amax <= 448 s, at least 2^kMinScaleExp.  amax =
+// 1.f x 2^e gives 2^(e - 8) for 1.f <= 1.75 (448 = 1.75 x 2^8), else 2^(e - 7).
+// A power of two makes x / s and a later change of scale exact up to e4m3's
+// own underflow, and costs no precision: e4m3 is a floating-point type.
+__device__ __forceinline__ float scale_for(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = static_cast<int>(b >> 23) - 127;
+    const int s = e - ((b & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+    return __uint_as_float(static_cast<uint32_t>((s < kMinScaleExp ? kMinScaleExp : s) + 127) << 23);
+}
+
+// First and one-past-last new token of sequence s (cu NULL: one token each).
+// Offsets outside [0, tokens] or descending are clamped, so that no lookup
+// leaves the caller's buffers whatever the device array holds.
+__device__ __forceinline__ void seq_tokens(const int32_t* cu, int s, int tokens, int& begin, int& end) {
+    if (cu == nullptr) {
+        begin = s;
+        end = s + 1;
+        return;
+    }
+    begin = min(max(__ldg(cu + s), 0), tokens);
+    end = min(max(__ldg(cu + s + 1), begin), tokens);
+}
+
+}  // namespace
+}  // namespace coc

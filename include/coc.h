@@ -551,7 +551,7 @@ typedef struct {
  *              values adjacent: slices of a fused QKV output as they are.
  * q_heads = 0  no q (q, q_strides, q_out unused).
  * cos, sin     positions x (rot_dim/2) floats, packed.
- * lens, cu_new, block_table  device int32.
+ * lens, cu_new, block_table  device int32; table_width * page_size <= 2^30.
  * Device arrays that name a page outside the cache or the table, or a position
  * outside cos/sin: the page's new tokens are left out (q copied), and
  * coc_sync_status reports COC_ERR_INVALID_ARG.

@@ -1517,7 +1517,8 @@ static coc_status_t check_kv(const coc_kv_cache_t* c, int64_t tokens, int64_t se
     if (c->pages < 0 || c->pages > kMaxDim) return fail(COC_ERR_SHAPE, "pages = %lld", (long long)c->pages);
     if (tokens < 0 || tokens > (int64_t(1) << 24)) return fail(COC_ERR_SHAPE, "tokens = %lld outside [0, 2^24]", (long long)tokens);
     if (seqs < 0 || seqs > (int64_t(1) << 16)) return fail(COC_ERR_SHAPE, "sequences = %lld outside [0, 2^16]", (long long)seqs);
-    if (table_width < 0 || table_width > (int64_t(1) << 24)) return fail(COC_ERR_SHAPE, "table width = %lld", (long long)table_width);
+    if (table_width < 0 || table_width * c->page_size > (int64_t(1) << 30) || table_width > (int64_t(1) << 30))
+        return fail(COC_ERR_SHAPE, "table width = %lld pages of %d: at most 2^30 positions a sequence", (long long)table_width, c->page_size);
     if (tokens > 0 && seqs == 0) return fail(COC_ERR_SHAPE, "%lld tokens of no sequence", (long long)tokens);
     if (cu == nullptr && tokens != seqs)
         return fail(COC_ERR_SHAPE, "without offsets every sequence has one token: %lld tokens, %lld sequences",
@@ -1665,8 +1666,16 @@ COC_API coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t
     a.page = cache->page_size;
     a.window = static_cast<int>(std::min<int64_t>(window, kMaxDim));
     a.sinks = static_cast<int>(std::min<int64_t>(sinks, kMaxDim));
-    const cudaError_t e = launch_kv_attention(a, dt == COC_BF16, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? COC_OK : cuda_fail(e, "KV attention launch");
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+    int grid = 0;
+    size_t bytes = 0;
+    cudaError_t e = kv_attention_plan(a, dt == COC_BF16, ds->sm_count, &grid, &bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "KV attention plan");
+    Scratch sc;
+    if ((st = scratch_acquire(ds, str, bytes, &sc)) != COC_OK) return st;
+    a.scratch = sc.ptr;
+    if ((e = launch_kv_attention(a, dt == COC_BF16, grid, str)) != cudaSuccess) st = cuda_fail(e, "KV attention launch");
+    return scratch_release(str, sc, st);
 }
 
 COC_API coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, int64_t k_shard, const void* const* x,

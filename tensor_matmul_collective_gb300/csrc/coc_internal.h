@@ -222,12 +222,14 @@ struct KvAttnArgs {
     const int32_t* lens;
     const int32_t* cu;
     unsigned* status;
+    void* scratch;                       // kv_attention_plan's bytes
     long long q_token, q_head, table_width, pages;
     float scale;
     int R, seqs, tokens, heads, q_heads, d, page, window, sinks;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
-cudaError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t kv_attention_plan(const KvAttnArgs& a, bool bf16, int sm_count, int* grid, size_t* scratch);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, int grid, cudaStream_t stream);
 
 // Row-parallel products with 4-bit weights (coc_w4.cu): w holds 8 codes along
 // k in a word (k / 8 x n words per rank), scales and zero points k / group x n.

@@ -240,8 +240,9 @@ struct W4Args {
     const int8_t* zero[COC_MAX_RANKS];   // NULL: 8 everywhere
     uint16_t* out[COC_MAX_RANKS];        // m x n
     int R, m, n, k, group;
+    int splits;                          // blocks of a cluster (set by launch_w4)
 };
-cudaError_t launch_w4(const W4Args& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_w4(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 
 // Host-side launch helpers implemented in coc_kernel.cu.  `pair` selects the
 // 2-SM variant (a cluster of two CTAs per 256-row tile; grid = 2 x pairs);

@@ -18,19 +18,27 @@
 // and the query rows in its 8 columns, O^T = V^T P^T with the head's values in
 // the rows.  Both operands are permuted along the contraction so that each
 // lane takes whole 16-byte pieces of the cache as they lie in memory, and a
-// piece is read by exactly one lane: the asynchronous copies land in a
-// lane-private slot of shared memory, with no bank conflict and no barrier.
+// piece is read by exactly one lane, straight into registers: no shared
+// memory, no barrier.  The next chunk is loaded while one is worked on.
+// (The same pieces through asynchronous copies into lane-private slots of
+// shared memory measured 118 against 106 us for two sequences of 131071 keys
+// on 8 ranks: the copies and their reads fill the memory pipe twice.)
 // Q is fp16 (exact for fp16; a bf16 row is scaled by a power of two to the top
 // of fp16's range first, so that it keeps its 8 bits down to 2^-29 of the
 // row's largest value).  Weights are rounded to fp16 (11 bits); with fp16
 // outputs a second product adds what that rounding left.
 //
 // Split.  The tiles of 64 keys of all (sequence, head, row tile) items form
-// one list, cut into equal contiguous runs, one per resident block: lengths
-// may be as unlike as they are, no SM idles.  An item that spans blocks leaves
+// one list, in which every item also counts kItemCost tiles for its beginning
+// and end, cut into equal contiguous runs, one per resident block: lengths may
+// be as unlike as they are, no SM idles.  An item that spans blocks leaves
 // unnormalised parts, which a second kernel adds in order.
+//
+// Measured: 48 sequences of 1 to 8192 keys, 8 ranks of one key head with 8
+// query heads of 128: 79 us, 5.0 TB/s; two of 131071: 95 us, 5.6 TB/s.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "coc_kv.cuh"
 #include "coc_ptx.cuh"
@@ -39,28 +47,24 @@ namespace coc {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kChunk = 16;                 // keys of one warp's step
-constexpr int kTile = kWarps * kChunk;     // keys of one block's step
+constexpr int kSub = 16;                   // keys of one matrix product
+constexpr int kTile = kWarps * kSub;       // keys of one block's step
 constexpr int kRows = 8;                   // query rows of a tile
-constexpr int kStages = 3;                 // chunks in flight per warp
-constexpr float kNoMax = -3.0e38f;         // running maximum before any key
+constexpr float kNoMax = -1.0e38f;         // running maximum before any key
+// What beginning and ending an item costs, in tiles: an item counts as so many
+// units more than it has tiles.
+constexpr int kItemCost = 5;
 // Weights are 2^(z - m + kOffset), with m at most 2^kSlack behind the true
 // maximum (it moves only when a key exceeds it by more): at most 2^15, and
 // normal fp16 numbers down to 2^-23 of m.
 constexpr float kOffset = 9.f;
 constexpr float kSlack = 6.f;
 
-// Bytes of one chunk's slots: d-padded K and V, and two scales per lane.
-template <int D>
-constexpr int chunk_bytes() { return 2 * kChunk * D + 256; }
+// Shared memory: the warps' sums, joined at the end of an item.
 template <int D>
 constexpr int merge_stride() { return D + 4; }
 template <int D>
-constexpr int attn_smem() {
-    const int ring = kWarps * kStages * chunk_bytes<D>();
-    const int merge = kWarps * kRows * merge_stride<D>() * 4;
-    return ring > merge ? ring : merge;
-}
+constexpr int attn_smem() { return kWarps * kRows * merge_stride<D>() * 4; }
 
 // Scratch: per block two parts (kRows x D sums, then kRows maxima and sums),
 // and a record of the item that the block begins and does not end.
@@ -73,19 +77,36 @@ struct Record {
 template <int D>
 constexpr long long part_floats() { return kRows * (D + 2); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    const int n = in ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(n) : "memory");
+// Codes are read once by one lane: no place in L1.
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool in) {
-    const int n = in ? BYTES : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "n"(BYTES), "r"(n)
-                 : "memory");
+__device__ __forceinline__ uint2 load8(const uint8_t* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool in) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<int>(in)));
+    return v;
+}
+__device__ __forceinline__ uint2 load8_if(const uint8_t* p, bool in) {
+    uint2 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y)
+        : "l"(p), "r"(static_cast<int>(in)));
+    return v;
+}
 
 // Two e4m3 codes (the low or high half of a word) as two fp16 values.
 __device__ __forceinline__ uint32_t half2_of(uint16_t codes) {
@@ -157,25 +178,30 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int s) {
 
 __device__ __forceinline__ long long seq_units(const KvAttnArgs& a, int s) {
     const SeqWork w = seq_work(a, s);
-    return static_cast<long long>(w.row_tiles) * w.tiles;
+    return static_cast<long long>(w.row_tiles) * (w.tiles + kItemCost);
 }
 
-// Per-row limits of a row tile.
-struct Rows {
-    int end_min, end_max, from_min, from_max;   // over the tile's rows
+// The keys that the rows of a tile see: row x those from row_from[x] (and the
+// sinks) up to row_end[x]; end and from are the last and the first of these.
+struct Limits {
+    int end, from, sinks;
+    int row_end[kRows], row_from[kRows];
 };
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+// EXACT: the head has D values (every offset inside a chunk is a constant);
+// otherwise fewer, and the pieces past them are zero.
+template <bool BF16, int D, bool EXACT>
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+    constexpr int BUF = D == 256 ? 1 : 2;   // chunks held: the next one is loaded while this one is worked on
     constexpr int KL = D / 64;              // 16-byte pieces of a key per lane
     constexpr int VB = D >= 128 ? 16 : 8;   // bytes of a value row in one piece
     constexpr int VL = D >= 128 ? D / 128 : 1;
     constexpr int MT = D / 16;              // value tiles of 16
-    constexpr int CB = chunk_bytes<D>();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan[kWarps];
     __shared__ long long found[3];
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+    __shared__ Limits limits;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int group = a.q_heads / a.heads;
@@ -233,21 +259,25 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
     SeqWork sw = seq_work(a, s);
     bool left_open = false;
 
-    const uint32_t ring = smem_u32(smem) + warp * kStages * CB + lane * 16;
-    const uint32_t ring8 = smem_u32(smem) + warp * kStages * CB + lane * VB;
-    const uint32_t ring4 = smem_u32(smem) + warp * kStages * CB + lane * 4;
-    const uint8_t* ring_p = smem + warp * kStages * CB;
+    const int d = EXACT ? D : a.d;
+    const int head_bytes = d << page_shift;                            // one (page, head)
+    const int page_bytes = a.heads * head_bytes;                       // at most 2^25
+    const uint32_t pages = static_cast<uint32_t>(a.pages);
 
     for (long long u = u0; u < u1;) {
-        while (u >= base + static_cast<long long>(sw.row_tiles) * sw.tiles * RH) {
-            base += static_cast<long long>(sw.row_tiles) * sw.tiles * RH;
+        const int span = sw.tiles + kItemCost;
+        if (u >= base + static_cast<long long>(sw.row_tiles) * span * RH) {
+            base += static_cast<long long>(sw.row_tiles) * span * RH;
             sw = seq_work(a, ++s);
+            continue;
         }
-        // item (rank and head, row tile), tiles [t0, t1) of it
-        const long long off = u - base;
-        const int item = static_cast<int>(off / sw.tiles);
-        const int t0 = static_cast<int>(off - static_cast<long long>(item) * sw.tiles);
-        const int t1 = static_cast<int>(min(static_cast<long long>(sw.tiles), t0 + (u1 - u)));
+        // item (rank and head, row tile), tiles [t0, t1) of it; the units
+        // ahead of its first tile go with that tile
+        const int item = static_cast<int>((u - base) / span);
+        const long long start = base + static_cast<long long>(item) * span + kItemCost;     // unit of its first tile
+        const int t0 = static_cast<int>(max(0LL, u - start));
+        if (start + t0 >= u1) break;
+        const int t1 = static_cast<int>(min(static_cast<long long>(sw.tiles), u1 - start));
         const int rh = item / sw.row_tiles, rt = item - rh * sw.row_tiles;
         const int r = rh / a.heads, h = rh - r * a.heads;
 
@@ -264,15 +294,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
         const int far = from_min / kTile;
         const int near = min(far, (min(sinks, end_max) + kTile - 1) / kTile);   // sink tiles ahead of the window's
         const int tiles = near + max(0, (end_max + kTile - 1) / kTile - far);
-        auto tile_of = [&](int t) { return t < near ? t : far + t - near; };
-        int row_end[2], row_from[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int rr = min(2 * c + x, rows - 1);
-            const int i = (rt * kRows + rr) / group;
-            row_end[x] = end_of(i);
-            row_from[x] = from_of(i);
-        }
 
         // ---- Q as the B operand: lane (g, c) holds row g, the 16 values of
         // each of its pieces (i * 4 + c), as the keys' lanes hold theirs
@@ -318,120 +339,184 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
         float acc[MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        float m0 = kNoMax, m1 = kNoMax, l0 = 0.f, l1 = 0.f;
+        // the columns' references, as what is added to log2 of a weight: kOffset - maximum
+        float b0 = kOffset - kNoMax, b1 = b0, l0 = 0.f, l1 = 0.f;
 
-        // ---- the chunks of this warp: tile t's keys j .. j + 15
+        // What only chunks at the ends of a row's keys need is kept out of the registers.
+        if (threadIdx.x < kRows) {
+            const int i = (rt * kRows + min(static_cast<int>(threadIdx.x), rows - 1)) / group;
+            limits.row_end[threadIdx.x] = end_of(i);
+            limits.row_from[threadIdx.x] = from_of(i);
+            if (threadIdx.x == 0) {
+                limits.end = end_max;
+                limits.from = from_min;
+                limits.sinks = sinks;
+            }
+        }
+        __syncthreads();
+        const volatile Limits& lim = limits;
+
+        // ---- the chunks of this warp: 16 keys j .. j + 15 of every tile
         const int tn = min(t1, tiles);
+        // a chunk between these is seen whole by every row
+        const int clean_lo = from_max, clean_hi = end_min - kSub;
         const int32_t* table = a.table + static_cast<long long>(s) * a.table_width;
-        auto page_at = [&](int t) {     // page id of this warp's chunk of tile t, -1 if it has none
-            if (t >= tn) return -1;
-            const int j = tile_of(t) * kTile + warp * kChunk;
-            if (j >= end_max) return -1;
-            const int id = __ldg(table + (j >> page_shift));
-            if (id < 0 || id >= a.pages) {
-                // reported only where a row looks at the page
-                if (lane == 0 && (j + kChunk > from_min || j < sinks)) atomicOr(a.status, DEV_ERR_BAD_PAGE);
-                return -1;
+        auto seen = [&](int j) { return j < lim.end && (j >= lim.from || j < lim.sinks); };   // by any row of the tile
+        auto wanted = [&](int j) { return j < lim.end && (j + kSub > lim.from || j < lim.sinks); };
+        // Place of the chunk whose table entry is read next, the tile it belongs to, and where the sinks' tiles end.
+        int ahead = t0, place = (t0 < near ? t0 : far + t0 - near) * kTile + warp * kSub;
+        const int skip_at = near * kTile + warp * kSub, skip = (far - near) * kTile;
+        auto advance = [&]() {
+            ++ahead;
+            place += kTile;
+            if (place == skip_at) place += skip;
+        };
+        // Nothing looks at an entry before the next step, so that the load's latency is not waited for.
+        auto entry_here = [&]() { return ahead < tn && place < end_max ? __ldg(table + (place >> page_shift)) : -1; };
+        // Entries outside the cache are left out, and reported where a row sees a key of the chunk.
+        auto checked = [&](int id, int j, bool in) {
+            if (static_cast<uint32_t>(id) >= pages) {
+                if (lane == 0 && in && wanted(j)) atomicOr(a.status, DEV_ERR_BAD_PAGE);
+                id = -1;
             }
             return id;
         };
-        auto seen = [&](int j) { return j < end_max && (j >= from_min || j < sinks); };   // by any row of the tile
-        auto load = [&](int t, int id, int stage) {
-            if (id >= 0) {
-                const int j = tile_of(t) * kTile + warp * kChunk;
-                const long long ph = static_cast<long long>(id) * a.heads + h;
-                const uint8_t* kp = a.ck[r] + ((ph << page_shift) + (j & (a.page - 1))) * a.d;
-                const uint8_t* vp = a.cv[r] + ((ph << page_shift) + (j & (a.page - 1))) * a.d;
-                const uint32_t so = stage * CB;
+        // the lane's first piece of 16 keys, for page 0 and slot 0
+        const uint8_t* k_lane = a.ck[r] + static_cast<long long>(h) * head_bytes + g * d + c * 16;
+        const uint8_t* v_lane = a.cv[r] + static_cast<long long>(h) * head_bytes + 2 * c * d + g * VB;
+        const float* sk_head = a.sk[r] + h;
+        const float* sv_head = a.sv[r] + h;
+        uint32_t kw[BUF][2][KL * 4], vw[BUF][4][VL * VB / 4];
+        // A clean chunk is loaded without a look at any key's place; else the lanes whose key no row sees (or whose piece
+        // lies past the head) hold zeros.
+        auto load_k = [&](int j, int id, int buf) {
+            const uint8_t* kp = k_lane + static_cast<long long>(id) * page_bytes + (j & (a.page - 1)) * d;
+            auto go = [&](auto all) {
+                constexpr bool ALL = decltype(all)::value;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int i = 0; i < KL; ++i) {
-                        const int e = (i * 4 + c) * 16;
-                        cp_async16(ring + so + (x * KL + i) * 512, kp + (g + 8 * x) * a.d + e, e < a.d && seen(j + g + 8 * x));
+                        const uint8_t* p = kp + 8 * x * d + i * 64;
+                        const uint4 v = ALL ? load16(p) : load16_if(p, seen(j + g + 8 * x) && (EXACT || (i * 4 + c) * 16 < d));
+                        kw[buf][x][4 * i] = v.x; kw[buf][x][4 * i + 1] = v.y; kw[buf][x][4 * i + 2] = v.z; kw[buf][x][4 * i + 3] = v.w;
                     }
+            };
+            if (EXACT && j >= clean_lo && j <= clean_hi) go(std::true_type{});
+            else go(std::false_type{});
+        };
+        auto load_v = [&](int j, int id, int buf) {
+            const uint8_t* vp = v_lane + static_cast<long long>(id) * page_bytes + (j & (a.page - 1)) * d;
+            auto go = [&](auto all) {
+                constexpr bool ALL = decltype(all)::value;
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int tok = 2 * c + (y & 1) + 8 * (y >> 1);
-                    const bool in = seen(j + tok);
+                    const int tok = (y & 1) + 8 * (y >> 1);     // after key 2 c
 #pragma unroll
                     for (int i = 0; i < VL; ++i) {
-                        const int e = i * 128 + g * VB;
-                        if constexpr (VB == 16)
-                            cp_async16(ring + so + kChunk * D + (y * VL + i) * 512, vp + tok * a.d + e, in && e < a.d);
-                        else
-                            cp_async_small<8>(ring8 + so + kChunk * D + y * 256, vp + tok * a.d + e, in && e < a.d);
+                        const uint8_t* p = vp + tok * d + i * 128;
+                        const bool have = ALL || (seen(j + 2 * c + tok) && (EXACT || i * 128 + g * VB < d));
+                        if constexpr (VB == 16) {
+                            const uint4 v = ALL ? load16(p) : load16_if(p, have);
+                            vw[buf][y][4 * i] = v.x; vw[buf][y][4 * i + 1] = v.y; vw[buf][y][4 * i + 2] = v.z; vw[buf][y][4 * i + 3] = v.w;
+                        } else {
+                            const uint2 v = ALL ? load8(p) : load8_if(p, have);
+                            vw[buf][y][0] = v.x; vw[buf][y][1] = v.y;
+                        }
                     }
                 }
-                cp_async_small<4>(ring4 + so + 2 * kChunk * D, a.sk[r] + ph, true);
-                cp_async_small<4>(ring4 + so + 2 * kChunk * D + 128, a.sv[r] + ph, true);
-            }
-            cp_commit();
+            };
+            if (EXACT && j >= clean_lo && j <= clean_hi) go(std::true_type{});
+            else go(std::false_type{});
         };
-        int ids[kStages];       // page ids of the chunks in flight
-        int next_id;            // of the chunk to be loaded next
-        {
-#pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) ids[i] = page_at(t0 + i);
-            next_id = page_at(t0 + kStages - 1);
-#pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) load(t0 + i, ids[i], i);
+
+        int j = place, id = checked(entry_here(), place, t0 < tn);      // this chunk's place and page
+        advance();
+        int j1 = place, entry = entry_here();                           // the next one's
+        float sk = 0.f, sv = 0.f;
+        if (id >= 0) {
+            sk = __ldg(sk_head + static_cast<long long>(id) * a.heads);
+            sv = __ldg(sv_head + static_cast<long long>(id) * a.heads);
+            load_k(j, id, 0);
+            load_v(j, id, 0);
         }
-        for (int tb = t0; tb < tn; tb += kStages) {
+        for (int tb = t0; tb < tn; tb += BUF) {
 #pragma unroll
-            for (int st = 0; st < kStages; ++st) {
-                const int t = tb + st;
+            for (int cur = 0; cur < BUF; ++cur) {
+                const int t = tb + cur;
                 if (t >= tn) break;
-                constexpr int last = kStages - 1;
-                const int into = (st + last) % kStages;
-                ids[into] = next_id;
-                load(t + last, next_id, into);
-                next_id = page_at(t + kStages);
-                cp_wait<last>();
-                if (ids[st] < 0) continue;
-                const int j = tile_of(t) * kTile + warp * kChunk;
-                const uint8_t* slot = ring_p + st * CB;
-                const float sk = *reinterpret_cast<const float*>(slot + 2 * kChunk * D + lane * 4);
-                const float sv = fmaxf(*reinterpret_cast<const float*>(slot + 2 * kChunk * D + 128 + lane * 4), 1.2e-38f);
-                // S^T = K Q^T
-                float sc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < KL; ++i) {
-                    const uint4 ka = *reinterpret_cast<const uint4*>(slot + i * 512 + lane * 16);
-                    const uint4 kb = *reinterpret_cast<const uint4*>(slot + (KL + i) * 512 + lane * 16);
-                    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t af[4] = {lo2(wa[w]), lo2(wb[w]), hi2(wa[w]), hi2(wb[w])};
-                        mma16816(sc, af, qf[8 * i + 2 * w], qf[8 * i + 2 * w + 1]);
+                const int nxt = BUF == 2 ? 1 - cur : 0;
+                const int here = id, j0 = j;
+                const float sk0 = sk, sv0 = sv;
+                id = checked(entry, j1, t + 1 < tn);
+                j = j1;
+                advance();
+                j1 = place;
+                entry = entry_here();
+                if (id >= 0) {
+                    sk = __ldg(sk_head + static_cast<long long>(id) * a.heads);
+                    sv = __ldg(sv_head + static_cast<long long>(id) * a.heads);
+                    if (BUF == 2) {
+                        load_k(j, id, nxt);
+                        load_v(j, id, nxt);
                     }
                 }
-                const float ev = log2_fast(sv);
-                const float f0 = qs0 * sk, f1 = qs1 * sk;
-                float z[4] = {fmaf(sc[0], f0, ev), fmaf(sc[1], f1, ev), fmaf(sc[2], f0, ev), fmaf(sc[3], f1, ev)};
-                const bool whole = j + kChunk <= end_min && (j >= from_max || j + kChunk <= sinks);
-                uint32_t see = 0xf;     // bit x: z[x]'s row sees its key
-                if (!whole) {
+                if (here < 0) {
+                    if (BUF == 1 && id >= 0) {
+                        load_k(j, id, nxt);
+                        load_v(j, id, nxt);
+                    }
+                    continue;
+                }
+                // S^T = K Q^T, in two accumulators: products into one wait for each other
+                float sc[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < KL * 4; ++w) {
+                    const uint32_t af[4] = {lo2(kw[cur][0][w]), lo2(kw[cur][1][w]), hi2(kw[cur][0][w]), hi2(kw[cur][1][w])};
+                    mma16816(w & 1 ? sb : sc, af, qf[2 * w], qf[2 * w + 1]);
+                }
+                if (BUF == 1 && id >= 0) load_k(j, id, nxt);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[x] += sb[x];
+                const float ev = log2_fast(fmaxf(sv0, 1.2e-38f));
+                const float f0 = qs0 * sk0, f1 = qs1 * sk0;
+                const bool clean = j0 >= clean_lo && j0 <= clean_hi;
+                uint32_t see = 0xf;     // bit x: the row of sc[x] sees its key
+                if (!clean) {
                     see = 0;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int key = j + g + 8 * (x >> 1);
-                        const bool in = key < row_end[x & 1] && (key >= row_from[x & 1] || key < sinks);
-                        see |= static_cast<uint32_t>(in) << x;
-                        if (!in) z[x] = -INFINITY;
+                        const int key = j0 + g + 8 * (x >> 1), row = 2 * c + (x & 1);
+                        see |= static_cast<uint32_t>(key < lim.row_end[row] && (key >= lim.row_from[row] || key < lim.sinks)) << x;
                     }
                 }
-                // the reference moves only when a key is well above it
-                if (__any_sync(0xffffffffu, fmaxf(z[0], z[2]) > m0 + kSlack || fmaxf(z[1], z[3]) > m1 + kSlack)) {
-                    float t0m = fmaxf(m0, fmaxf(z[0], z[2])), t1m = fmaxf(m1, fmaxf(z[1], z[3]));
+                float z[4];             // log2 of the weights
+                auto logs = [&](float e0, float e1) {
+                    z[0] = fmaf(sc[0], f0, e0);
+                    z[1] = fmaf(sc[1], f1, e1);
+                    z[2] = fmaf(sc[2], f0, e0);
+                    z[3] = fmaf(sc[3], f1, e1);
+                    if (!clean) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!(see >> x & 1)) z[x] = -INFINITY;
+                    }
+                };
+                logs(ev + b0, ev + b1);
+                // a reference moves only when a key is well above it
+                if (__any_sync(0xffffffffu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > kOffset + kSlack)) {
+                    logs(ev, ev);
+                    float n0 = fmaxf(kOffset - b0, fmaxf(z[0], z[2])), n1 = fmaxf(kOffset - b1, fmaxf(z[1], z[3]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
-                        t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, o));
-                        t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, o));
+                        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+                        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
                     }
-                    const float c0 = exp2_fast(m0 - t0m), c1 = exp2_fast(m1 - t1m);
-                    m0 = t0m;
-                    m1 = t1m;
+                    n0 = kOffset - n0;
+                    n1 = kOffset - n1;
+                    const float c0 = exp2_fast(n0 - b0), c1 = exp2_fast(n1 - b1);
+                    b0 = n0;
+                    b1 = n1;
                     l0 *= c0;
                     l1 *= c1;
 #pragma unroll
@@ -441,43 +526,31 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
                         acc[i][2] *= c0;
                         acc[i][3] *= c1;
                     }
+                    logs(ev + b0, ev + b1);
                 }
-                const float b0 = kOffset - m0, b1 = kOffset - m1;
-                float w[4] = {exp2_fast(z[0] + b0), exp2_fast(z[1] + b1), exp2_fast(z[2] + b0), exp2_fast(z[3] + b1)};
-                const float inv = __frcp_rn(sv);
-                l0 = fmaf(w[0] + w[2], inv, l0);
-                l1 = fmaf(w[1] + w[3], inv, l1);
-                const uint32_t plo = pack_half2(w[0], w[1]), phi = pack_half2(w[2], w[3]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) z[x] = exp2_fast(z[x]);
+                const float inv = exp2_fast(-ev);
+                l0 = fmaf(z[0] + z[2], inv, l0);
+                l1 = fmaf(z[1] + z[3], inv, l1);
+                const uint32_t plo = pack_half2(z[0], z[1]), phi = pack_half2(z[2], z[3]);
                 const uint32_t p0 = transposed(plo), p1 = transposed(phi);
                 uint32_t e0 = 0, e1 = 0;
                 if constexpr (!BF16) {
                     const float2 rl = __half22float2(*reinterpret_cast<const __half2*>(&plo));
                     const float2 rh2 = __half22float2(*reinterpret_cast<const __half2*>(&phi));
-                    e0 = transposed(pack_half2(w[0] - rl.x, w[1] - rl.y));
-                    e1 = transposed(pack_half2(w[2] - rh2.x, w[3] - rh2.y));
+                    e0 = transposed(pack_half2(z[0] - rl.x, z[1] - rl.y));
+                    e1 = transposed(pack_half2(z[2] - rh2.x, z[3] - rh2.y));
                 }
                 // O^T += V^T P^T
-                uint32_t vw[4][VL * VB / 4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int i = 0; i < VL; ++i) {
-                        if constexpr (VB == 16) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(slot + kChunk * D + (y * VL + i) * 512 + lane * 16);
-                            vw[y][4 * i] = v.x; vw[y][4 * i + 1] = v.y; vw[y][4 * i + 2] = v.z; vw[y][4 * i + 3] = v.w;
-                        } else {
-                            const uint2 v = *reinterpret_cast<const uint2*>(slot + kChunk * D + y * 256 + lane * 8);
-                            vw[y][0] = v.x; vw[y][1] = v.y;
-                        }
-                    }
-                if (!whole) {
+                if (!clean) {
                     // a NaN of a key that only some rows see would reach the others as 0 x NaN: where the
                     // chunk has one, it is taken out of the product and put into the rows that see it
                     uint32_t nan = 0;
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
 #pragma unroll
-                        for (int i = 0; i < VL * VB / 4; ++i) nan |= ((vw[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        for (int i = 0; i < VL * VB / 4; ++i) nan |= ((vw[cur][y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                     if (__any_sync(0xffffffffu, nan != 0)) {
                         const uint32_t i0b = transposed(pack_half2(see & 1 ? 1.f : 0.f, see & 2 ? 1.f : 0.f));
                         const uint32_t i1b = transposed(pack_half2(see & 4 ? 1.f : 0.f, see & 8 ? 1.f : 0.f));
@@ -486,9 +559,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
                             uint32_t x[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y) {
-                                const uint32_t bad = ((((vw[y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
+                                const uint32_t bad = ((((vw[cur][y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
                                 x[y] = bad & 0x38383838u;       // e4m3 1.0 where NaN
-                                vw[y][i] &= ~bad;
+                                vw[cur][y][i] &= ~bad;
                             }
                             const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[2], x[3], 0x5140);
                             const uint32_t b01 = __byte_perm(x[0], x[1], 0x7362), b23 = __byte_perm(x[2], x[3], 0x7362);
@@ -507,8 +580,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
                 // word i of the four keys: bytes 0, 1 make value tile 2i, bytes 2, 3 tile 2i + 1
 #pragma unroll
                 for (int i = 0; i < MT / 2; ++i) {
-                    const uint32_t a01 = __byte_perm(vw[0][i], vw[1][i], 0x5140), a23 = __byte_perm(vw[2][i], vw[3][i], 0x5140);
-                    const uint32_t b01 = __byte_perm(vw[0][i], vw[1][i], 0x7362), b23 = __byte_perm(vw[2][i], vw[3][i], 0x7362);
+                    const uint32_t a01 = __byte_perm(vw[cur][0][i], vw[cur][1][i], 0x5140), a23 = __byte_perm(vw[cur][2][i], vw[cur][3][i], 0x5140);
+                    const uint32_t b01 = __byte_perm(vw[cur][0][i], vw[cur][1][i], 0x7362), b23 = __byte_perm(vw[cur][2][i], vw[cur][3][i], 0x7362);
                     const uint32_t fa[4] = {lo2(a01), hi2(a01), lo2(a23), hi2(a23)}, fb[4] = {lo2(b01), hi2(b01), lo2(b23), hi2(b23)};
                     mma16816(acc[2 * i], fa, p0, p1);
                     mma16816(acc[2 * i + 1], fb, p0, p1);
@@ -517,9 +590,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
                         mma16816(acc[2 * i + 1], fb, e0, e1);
                     }
                 }
+                if (BUF == 1 && id >= 0) load_v(j, id, nxt);
             }
         }
-        cp_wait<0>();
+        const float m0 = kOffset - b0, m1 = kOffset - b1;
 
         // ---- join the warps: maxima and sums, then the value sums in the
         // accumulators' order (value d = g VB + 2 i + b at 16 i + 2 g + b)
@@ -534,7 +608,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
             wl[warp][2 * c] = l0;
             wl[warp][2 * c + 1] = l1;
         }
-        __syncthreads();    // the ring is free too
+        __syncthreads();
         float M0 = wm[0][2 * c], M1 = wm[0][2 * c + 1];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) {
@@ -590,20 +664,27 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) kv_attention_ke
                 rec->seq = s;
                 rec->head = rh;
                 rec->row_tile = rt;
-                rec->last_block = static_cast<int>((u - t0 + sw.tiles - 1) / quota);
+                rec->last_block = static_cast<int>((start + sw.tiles - 1) / quota);
             }
         }
         __syncthreads();    // the merge area and wm are read before the next item
-        u += t1 - t0;
+        u = start + t1;
     }
     if (threadIdx.x == 0) rec->open = left_open ? 1 : 0;
 }
 
 // Block (b, row): adds the parts of the item that block b began and others
-// went on with, in their order.
+// went on with.  Group y of the threads adds the parts y, y + kMergeGroups,
+// ... in order, eight loads at a time, then the groups are added in order.
+constexpr int kMergeGroups = 4;
+constexpr int kMaxGrid = 2048;      // blocks of the attention kernel
+
 template <bool BF16, int D>
-__global__ void __launch_bounds__(D / 2) kv_attention_merge(const __grid_constant__ KvAttnArgs a) {
-    constexpr int VB = D >= 128 ? 16 : 8;
+__global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const __grid_constant__ KvAttnArgs a) {
+    constexpr int VB = D >= 128 ? 16 : 8, T = kMergeGroups * D / 2;
+    __shared__ float weight[kMaxGrid];
+    __shared__ float red[2][T / 32];
+    __shared__ float2 sums[kMergeGroups][D / 2];
     grid_dependency_wait();
     const Record* recs = reinterpret_cast<const Record*>(a.scratch);
     const Record rec = recs[blockIdx.x];
@@ -614,20 +695,46 @@ __global__ void __launch_bounds__(D / 2) kv_attention_merge(const __grid_constan
     const int rho = rec.row_tile * kRows + blockIdx.y;
     if (rho >= (end - begin) * group) return;
     const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
-    const int row = blockIdx.y, first = blockIdx.x, count = rec.last_block - first + 1, p = 2 * threadIdx.x;
+    const int row = blockIdx.y, first = blockIdx.x, count = rec.last_block - first + 1;
     auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D>(); };
     float M = kNoMax;
-    for (int i = 0; i < count; ++i) M = fmaxf(M, part(i)[kRows * D + row]);
+    for (int i = threadIdx.x; i < count; i += T) M = fmaxf(M, weight[i] = part(i)[kRows * D + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T / 32; ++i) M = fmaxf(M, red[0][i]);
     float L = 0.f;
+    for (int i = threadIdx.x; i < count; i += T) {
+        const float f = exp2_fast(weight[i] - M);
+        weight[i] = f;
+        L = fmaf(part(i)[kRows * D + kRows + row], f, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = L;
+    __syncthreads();
+    const int y = threadIdx.x / (D / 2), x = threadIdx.x % (D / 2), p = 2 * x;
     float2 sum = make_float2(0.f, 0.f);
-    for (int i = 0; i < count; ++i) {
-        const float* q = part(i);
-        const float f = exp2_fast(q[kRows * D + row] - M);
-        L = fmaf(q[kRows * D + kRows + row], f, L);
-        const float2 v = *reinterpret_cast<const float2*>(q + row * D + p);
+#pragma unroll 8
+    for (int i = y; i < count; i += kMergeGroups) {
+        const float f = weight[i];
+        const float2 v = *reinterpret_cast<const float2*>(part(i) + row * D + p);
         sum.x = fmaf(v.x, f, sum.x);
         sum.y = fmaf(v.y, f, sum.y);
     }
+    sums[y][x] = sum;
+    __syncthreads();
+    if (y != 0) return;
+#pragma unroll
+    for (int i = 1; i < kMergeGroups; ++i) {
+        sum.x += sums[i][x].x;
+        sum.y += sums[i][x].y;
+    }
+    L = 0.f;
+#pragma unroll
+    for (int i = 0; i < T / 32; ++i) L += red[1][i];
     const int tile = p / 16, gg = (p % 16) / 2;
     const int e = VB == 16 ? tile / 8 * 128 + gg * 16 + tile % 8 * 2 : gg * 8 + tile * 2;
     if (e >= a.d) return;
@@ -637,76 +744,89 @@ __global__ void __launch_bounds__(D / 2) kv_attention_merge(const __grid_constan
     *reinterpret_cast<uint32_t*>(o) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
 }
 
-template <bool BF16, int D>
-cudaError_t resident_blocks(int* out) {
-    static std::mutex mu;
-    static int cached[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    if (dev >= 0 && dev < 64 && cached[dev] > 0) {
-        *out = cached[dev];
+template <bool BF16, int D, bool EXACT>
+struct Launcher {
+    // Blocks that one SM holds; sets the kernel up on the current device.
+    static cudaError_t resident(int* out) {
+        static std::mutex mu;
+        static int cached[64];
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 0 && dev < 64 && cached[dev] > 0) {
+            *out = cached[dev];
+            return cudaSuccess;
+        }
+        auto kern = kv_attention_kernel<BF16, D, EXACT>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>());
+        if (e != cudaSuccess) return e;
+        int n = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, attn_smem<D>());
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 64) cached[dev] = n;
+        *out = n;
         return cudaSuccess;
     }
-    e = cudaFuncSetAttribute(kv_attention_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>());
-    if (e != cudaSuccess) return e;
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<BF16, D>, kWarps * 32, attn_smem<D>());
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    if (dev >= 0 && dev < 64) cached[dev] = n;
-    *out = n;
-    return cudaSuccess;
-}
+    static cudaError_t launch(const KvAttnArgs& a, int grid, cudaStream_t stream) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+        cfg.blockDim = dim3(kWarps * 32, 1, 1);
+        cfg.dynamicSmemBytes = attn_smem<D>();
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_launch() ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<BF16, D, EXACT>, a);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows, 1);
+        cfg.blockDim = dim3(kMergeGroups * D / 2, 1, 1);
+        cfg.dynamicSmemBytes = 0;
+        return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D>, a);
+    }
+};
 
-// Head sizes up to 64, 128 and 256 have instances of their own (shorter heads
-// are padded with zero bytes that are never read).
+// Head sizes 64, 128 and 256 have instances of their own; the others take the
+// next of them with the rest of the head zero.
 int padded_d(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <bool BF16, int D>
-cudaError_t launch_t(const KvAttnArgs& a, int grid, cudaStream_t stream) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = attn_smem<D>();
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_launch() ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<BF16, D>, a);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows, 1);
-    cfg.blockDim = dim3(D / 2, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D>, a);
+template <typename F>
+cudaError_t with_instance(bool bf16, int d, F f) {
+    const bool exact = padded_d(d) == d;
+#define COC_ATTN(B, D) return exact ? f(Launcher<B, D, true>()) : f(Launcher<B, D, false>())
+    if (bf16) {
+        if (padded_d(d) == 64) COC_ATTN(true, 64);
+        if (padded_d(d) == 128) COC_ATTN(true, 128);
+        COC_ATTN(true, 256);
+    }
+    if (padded_d(d) == 64) COC_ATTN(false, 64);
+    if (padded_d(d) == 128) COC_ATTN(false, 128);
+    COC_ATTN(false, 256);
+#undef COC_ATTN
 }
 
 }  // namespace
 
 cudaError_t kv_attention_plan(const KvAttnArgs& a, bool bf16, int sm_count, int* grid, size_t* scratch) {
-    const int D = padded_d(a.d);
     int n = 0;
-    cudaError_t e;
-    if (bf16) e = D == 64 ? resident_blocks<true, 64>(&n) : D == 128 ? resident_blocks<true, 128>(&n) : resident_blocks<true, 256>(&n);
-    else e = D == 64 ? resident_blocks<false, 64>(&n) : D == 128 ? resident_blocks<false, 128>(&n) : resident_blocks<false, 256>(&n);
+    const cudaError_t e = with_instance(bf16, a.d, [&](auto l) { return l.resident(&n); });
     if (e != cudaSuccess) return e;
     // never more blocks than there can be units
     const int group = a.q_heads / a.heads;
     const long long items = (static_cast<long long>(a.tokens) * group / kRows + a.seqs) * a.R * a.heads;
     const long long tiles = std::max<long long>(1, (a.table_width * a.page + kTile - 1) / kTile);
-    const long long resident = static_cast<long long>(n) * sm_count;
+    long long resident = static_cast<long long>(n) * sm_count;
+    resident = std::min<long long>(resident, kMaxGrid);
     *grid = static_cast<int>(tiles >= resident ? resident : std::min(resident, items * tiles));
-    *scratch = static_cast<size_t>(*grid) * (sizeof(Record) + 2 * kRows * (D + 2) * sizeof(float));
+    *scratch = static_cast<size_t>(*grid) * (sizeof(Record) + 2 * kRows * (padded_d(a.d) + 2) * sizeof(float));
     return cudaSuccess;
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
-    const int D = padded_d(a.d);
-    if (bf16) return D == 64 ? launch_t<true, 64>(a, grid, stream) : D == 128 ? launch_t<true, 128>(a, grid, stream) : launch_t<true, 256>(a, grid, stream);
-    return D == 64 ? launch_t<false, 64>(a, grid, stream) : D == 128 ? launch_t<false, 128>(a, grid, stream) : launch_t<false, 256>(a, grid, stream);
+    return with_instance(bf16, a.d, [&](auto l) { return l.launch(a, grid, stream); });
 }
 
 }  // namespace coc

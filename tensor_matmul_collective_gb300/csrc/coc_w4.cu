@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdlib>
+#include <type_traits>
 
 #include "coc_kv.cuh"
 #include "coc_ptx.cuh"
@@ -38,7 +39,13 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kCols = 64;               // columns of a warp
 constexpr int kStep = 32;               // contraction of one step: 4 word rows
-constexpr int kStages = 4;
+#ifndef T_WST
+#define T_WST 4
+#endif
+#ifndef T_WOC
+#define T_WOC 3
+#endif
+constexpr int kStages = T_WST;
 
 template <int NT>
 constexpr int stage_bytes() { return 32 * (2 * 16 + NT * 16 + 16 + 8); }   // words, x, scales, zero points
@@ -97,33 +104,40 @@ __device__ __forceinline__ uint32_t fma2_half(uint32_t x, uint32_t y, uint32_t z
     return r;
 }
 
-// code - z of the 8 codes of a word, as the pairs (k, k + 4), k = 0 .. 3.
-// off: -(1024 + z) twice (fp16) or -(128 + z) (bf16); off16: -(64 + z) (fp16).
-template <bool BF16>
-__device__ __forceinline__ void codes(uint32_t w, uint32_t off, uint32_t off16, uint32_t (&p)[4]) {
+// (d0, d1) += (x0, x1) * s
+__device__ __forceinline__ void fma2(float& d0, float& d1, float x0, float x1, float s) {
+    asm("{\n\t.reg .b64 d, x, s;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+        "fma.rn.f32x2 d, x, s, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(x0), "f"(x1), "f"(s));
+}
+
+// code - z of four of a word's 8 codes: the pairs (k, k + 4) for k = 2 H and
+// 2 H + 1.  off: -(1024 + z) twice (fp16) or -(128 + z) (bf16); off16: -(64 + z)
+// (fp16: a code four bits up is 16 times itself, and its product with 1/16
+// costs the addition nothing).
+template <bool BF16, int H>
+__device__ __forceinline__ void codes(uint32_t w, uint32_t off, uint32_t off16, uint32_t& p0, uint32_t& p1) {
     if constexpr (BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = add2<true>(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), off);
+        p0 = add2<true>(and_or(w >> (8 * H), 0x000F000Fu, 0x43004300u), off);
+        p1 = add2<true>(and_or(w >> (8 * H + 4), 0x000F000Fu, 0x43004300u), off);
     } else {
-        // a code four bits up is 16 times itself: its product with 1/16 costs the addition nothing
-        const uint32_t v = w >> 8;
-        p[0] = add2<false>(and_or(w, 0x000F000Fu, 0x64006400u), off);
-        p[1] = fma2_half(and_or(w, 0x00F000F0u, 0x64006400u), 0x2C002C00u, off16);
-        p[2] = add2<false>(and_or(v, 0x000F000Fu, 0x64006400u), off);
-        p[3] = fma2_half(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, off16);
+        const uint32_t v = w >> (8 * H);
+        p0 = add2<false>(and_or(v, 0x000F000Fu, 0x64006400u), off);
+        p1 = fma2_half(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, off16);
     }
 }
 
+// f in both halves, rounded to the 16-bit type (exact for the offsets).
 template <bool BF16>
-__device__ __forceinline__ uint32_t twice(float f) {
-    const uint32_t v = from_float16bit<BF16>(f);
-    return v | (v << 16);
+__device__ __forceinline__ uint32_t pair(float f) {
+    return pack2<BF16>(__float_as_uint(f), __float_as_uint(f));
 }
 
 // Block: WO x 64 columns, 8 / WO ranges of the contraction; cluster: blocks
 // with the same columns and further ranges.  blockIdx.y: 8 NT rows of x.
 template <bool BF16, int NT, bool ZERO, int WO>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constant__ W4Args a) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_kernel(const __grid_constant__ W4Args a) {
     constexpr int WK = kWarps / WO;
     constexpr int SB = stage_bytes<NT>();
     extern __shared__ __align__(128) uint8_t smem[];
@@ -150,36 +164,62 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
             for (int q = 0; q < 4; ++q) acc[t][i][q] = part[t][i][q] = 0.f;
 
     if (col0 < a.n && s0 < s1) {
-        // ---- producer: the next step to be copied
+        // ---- producer: the next step to be copied.  All addresses run on by
+        // constants inside a rank's shard.
         const bool in0 = col0 + 4 * g < a.n, in1 = col0 + 32 + 4 * g < a.n;
         const uint32_t ring = smem_u32(smem) + warp * kStages * SB;
         const uint8_t* ring_p = smem + warp * kStages * SB;
-        int ps = s0, pr = s0 / per_rank, pin = s0 - pr * per_rank;   // step, rank, step of the rank
+        int pr = s0 / per_rank, todo = s1 - s0;
+        int in_rank, in_group;              // steps to the end of the rank's shard and of the group
+        const uint32_t* wp;
+        const uint16_t* xp[NT];
+        const uint16_t* sp;
+        const int8_t* zp = nullptr;
+        bool new_group = true;
+        auto enter = [&](int at) {          // step `at` of rank pr
+            in_rank = per_rank - at;
+            in_group = per_group - at % per_group;
+            wp = a.w[pr] + (static_cast<long long>(at) * 4 + c) * a.n + col0 + 4 * g;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int row = row0 + 8 * t + g;
+                xp[t] = a.x[pr] + static_cast<long long>(row < a.m ? row : 0) * a.k + at * kStep + 8 * c;
+            }
+            const long long so = static_cast<long long>(at / per_group) * a.n + col0 + 4 * g;
+            sp = a.scale[pr] + so;
+            if constexpr (ZERO) zp = a.zero[pr] + so;
+        };
+        enter(s0 - pr * per_rank);
         auto load = [&](int stage) {
-            if (ps < s1) {
+            if (todo > 0) {
                 const uint32_t so = ring + stage * SB;
-                const uint32_t* wp = a.w[pr] + (static_cast<long long>(pin) * 4 + c) * a.n + col0 + 4 * g;
                 cp_async<16>(so + lane * 16, wp, in0);
                 cp_async<16>(so + 512 + lane * 16, wp + 32, in1);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const int row = row0 + 8 * t + g;
-                    cp_async<16>(so + 1024 + t * 512 + lane * 16,
-                                 a.x[pr] + static_cast<long long>(row < a.m ? row : 0) * a.k + pin * kStep + 8 * c, row < a.m);
+                    cp_async<16>(so + 1024 + t * 512 + lane * 16, xp[t], row0 + 8 * t + g < a.m);
+                    xp[t] += kStep;
                 }
-                if (ps == s0 || pin % per_group == 0) {
-                    const long long at = static_cast<long long>(pin / per_group) * a.n + col0 + 4 * g;
-                    cp_async<8>(so + 1024 + NT * 512 + lane * 16, a.scale[pr] + at, in0);
-                    cp_async<8>(so + 1024 + NT * 512 + lane * 16 + 8, a.scale[pr] + at + 32, in1);
+                wp += 4LL * a.n;
+                if (new_group) {
+                    new_group = false;
+                    cp_async<8>(so + 1024 + NT * 512 + lane * 16, sp, in0);
+                    cp_async<8>(so + 1024 + NT * 512 + lane * 16 + 8, sp + 32, in1);
+                    sp += a.n;
                     if constexpr (ZERO) {
-                        cp_async<4>(so + 1536 + NT * 512 + lane * 8, a.zero[pr] + at, in0);
-                        cp_async<4>(so + 1536 + NT * 512 + lane * 8 + 4, a.zero[pr] + at + 32, in1);
+                        cp_async<4>(so + 1536 + NT * 512 + lane * 8, zp, in0);
+                        cp_async<4>(so + 1536 + NT * 512 + lane * 8 + 4, zp + 32, in1);
+                        zp += a.n;
                     }
                 }
-                ++ps;
-                if (++pin == per_rank) {
-                    pin = 0;
-                    ++pr;
+                --todo;
+                if (--in_group == 0) {
+                    in_group = per_group;
+                    new_group = true;
+                    if ((in_rank -= per_group) <= 0 && todo > 0) {      // groups do not cross shards
+                        ++pr;
+                        enter(0);
+                    }
                 }
             }
             cp_commit();
@@ -187,13 +227,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i);
 
-        int left = per_group - s0 % per_group;      // steps to the end of the group (per_rank is a multiple of per_group)
+        int left = per_group - s0 % per_group;      // steps to the end of the group (shards are whole groups)
         bool fresh = true;
         float sc[8];
         uint32_t off[ZERO ? 8 : 1], off16[ZERO ? 8 : 1];
         if constexpr (!ZERO) {
-            off[0] = twice<BF16>(BF16 ? -136.f : -1032.f);
-            off16[0] = BF16 ? 0u : twice<false>(-72.f);
+            off[0] = pair<BF16>(BF16 ? -136.f : -1032.f);
+            off16[0] = BF16 ? 0u : pair<false>(-72.f);
         }
         for (int sb = s0; sb < s1; sb += kStages) {
 #pragma unroll
@@ -210,12 +250,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                     for (int i = 0; i < 8; ++i) sc[i] = to_float16bit<BF16>(static_cast<uint16_t>(sv[i / 2] >> (16 * (i & 1))));
                     if constexpr (ZERO) {
                         const uint2 z2 = *reinterpret_cast<const uint2*>(slot + 1536 + NT * 512 + lane * 8);
-                        const uint32_t zv[2] = {z2.x, z2.y};
+                        const uint32_t zv[2] = {z2.x ^ 0x80808080u, z2.y ^ 0x80808080u};      // z + 128
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float z = static_cast<float>(static_cast<int8_t>(zv[i / 4] >> (8 * (i & 3))));
-                            off[i] = twice<BF16>((BF16 ? -128.f : -1024.f) - z);
-                            off16[i] = BF16 ? 0u : twice<false>(-64.f - z);
+                            // 2^23 + (z + 128) is exact, and so is what is taken off
+                            const float z = __uint_as_float(__byte_perm(zv[i / 4], 0x4B000000u, 0x7650 + (i & 3)));
+                            off[i] = pair<BF16>((BF16 ? 8388608.f : 8388608.f - 896.f) - z);
+                            if constexpr (!BF16) off16[i] = add2<false>(off[i], 0x63806380u);           // + 960
                         }
                     }
                 }
@@ -231,26 +272,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                     b[t][3] = __byte_perm(x.y, x.w, 0x7632);
                 }
                 const uint32_t wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                // all tiles once per half: products into one accumulator do not follow each other
+                auto half = [&](auto hc) {
+                    constexpr int H = decltype(hc)::value;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
-                    uint32_t pa[4], pb[4];
-                    codes<BF16>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], pa);
-                    codes<BF16>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], pb);
+                    for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
+                        uint32_t a0, a1, a2, a3;
+                        codes<BF16, H>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], a0, a2);
+                        codes<BF16, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma16816<BF16>(part[t][i], pa[0], pb[0], pa[1], pb[1], b[t][0], b[t][1]);
-                        mma16816<BF16>(part[t][i], pa[2], pb[2], pa[3], pb[3], b[t][2], b[t][3]);
+                        for (int t = 0; t < NT; ++t) mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
                     }
-                }
+                };
+                half(std::integral_constant<int, 0>{});
+                half(std::integral_constant<int, 1>{});
                 if (--left == 0 || sb + st + 1 == s1) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                acc[t][i][q] = fmaf(part[t][i][q], sc[2 * i + (q >> 1)], acc[t][i][q]);
-                                part[t][i][q] = 0.f;
+                            for (int q = 0; q < 4; q += 2) {
+                                fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], sc[2 * i + (q >> 1)]);
+                                part[t][i][q] = part[t][i][q + 1] = 0.f;
                             }
                     left = per_group;
                     fresh = true;

@@ -37,30 +37,32 @@ namespace coc {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kCols = 64;               // columns of a warp
+constexpr int kCols = 64;               // columns of a block; its warps split the contraction
 constexpr int kStep = 32;               // contraction of one step: 4 word rows
 #ifndef T_WST
-#define T_WST 4
+#define T_WST 3
 #endif
 #ifndef T_WOC
-#define T_WOC 3
+#define T_WOC 2
 #endif
-constexpr int kStages = T_WST;
+constexpr int kStages = T_WST;          // stages of SS steps in a warp's ring
 
-template <int NT>
-constexpr int stage_bytes() { return 32 * (2 * 16 + NT * 16 + 16 + 8); }   // words, x, scales, zero points
+// A stage: SS x (two 16-byte pieces of words a lane, NT of x), then scales
+// (16 bytes) and zero points (8 bytes) of the lanes 4 g.
+template <int NT, int SS>
+constexpr int stage_bytes() { return SS * 512 * (2 + NT) + 8 * 24; }
 template <int NT>
 constexpr int sum_floats() { return NT * 8 * kCols; }                      // one warp's sums
-template <int NT>
+template <int NT, int SS>
 constexpr int w4_smem() {
-    const int ring = kWarps * kStages * stage_bytes<NT>();
+    const int ring = kWarps * kStages * stage_bytes<NT, SS>();
     const int sums = kWarps * sum_floats<NT>() * 4;
     return ring > sums ? ring : sums;
 }
 
+// n of BYTES bytes, the rest zero.
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {
-    const int n = in ? BYTES : 0;
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(n) : "memory");
     else
@@ -134,26 +136,25 @@ __device__ __forceinline__ uint32_t pair(float f) {
     return pack2<BF16>(__float_as_uint(f), __float_as_uint(f));
 }
 
-// Block: WO x 64 columns, 8 / WO ranges of the contraction; cluster: blocks
-// with the same columns and further ranges.  blockIdx.y: 8 NT rows of x.
-template <bool BF16, int NT, bool ZERO, int WO>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_kernel(const __grid_constant__ W4Args a) {
-    constexpr int WK = kWarps / WO;
-    constexpr int SB = stage_bytes<NT>();
+// Block: 64 columns, 8 NT rows of x (blockIdx.y), kWarps ranges of the
+// contraction; cluster: blocks with the same columns and further ranges.  SS
+// steps make a stage (groups are whole stages).
+template <bool BF16, int NT, bool ZERO, int SS>
+__global__ void __launch_bounds__(kWarps * 32, T_WOC) w4_kernel(const __grid_constant__ W4Args a) {
+    constexpr int SB = stage_bytes<NT, SS>();
+    constexpr int XO = SS * 1024, CO = SS * 512 * (2 + NT);      // x, scales in a stage
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int wo = warp % WO, wk = warp / WO;
     const int split = static_cast<int>(cluster_rank()), splits = a.splits;
-    const int slab = blockIdx.x / splits;
-    const int col0 = (slab * WO + wo) * kCols, row0 = blockIdx.y * 8 * NT;
+    const int col0 = static_cast<int>(blockIdx.x / splits) * kCols, row0 = blockIdx.y * 8 * NT;
 
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // this warp's steps, all ranks' shards one after another
-    const int per_rank = a.k / kStep, per_group = a.group / kStep;
-    const long long steps = static_cast<long long>(per_rank) * a.R, ways = static_cast<long long>(splits) * WK, way = split * WK + wk;
-    const int s0 = static_cast<int>(steps * way / ways), s1 = static_cast<int>(steps * (way + 1) / ways);
+    // this warp's stages, all ranks' shards one after another
+    const int per_rank = a.k / (kStep * SS), per_group = a.group / (kStep * SS);
+    const long long all = static_cast<long long>(per_rank) * a.R, ways = static_cast<long long>(splits) * kWarps, way = split * kWarps + warp;
+    const int s0 = static_cast<int>(all * way / ways), s1 = static_cast<int>(all * (way + 1) / ways);
 
     float acc[NT][4][4], part[NT][4][4];
 #pragma unroll
@@ -163,54 +164,65 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[t][i][q] = part[t][i][q] = 0.f;
 
-    if (col0 < a.n && s0 < s1) {
-        // ---- producer: the next step to be copied.  All addresses run on by
+    if (s0 < s1) {
+        // ---- producer: the next stage to be copied.  All addresses run on by
         // constants inside a rank's shard.
-        const bool in0 = col0 + 4 * g < a.n, in1 = col0 + 32 + 4 * g < a.n;
+        const int n0 = col0 + 4 * g < a.n ? 16 : 0, n1 = col0 + 32 + 4 * g < a.n ? 16 : 0;       // bytes copied: none past the columns
         const uint32_t ring = smem_u32(smem) + warp * kStages * SB;
         const uint8_t* ring_p = smem + warp * kStages * SB;
+        const uint32_t rows_w = 16u * static_cast<uint32_t>(a.n);       // bytes of a step's word rows
+        // The 8 pieces of a word row stay together in shared memory (a copy writes a row at a time; scattered by lane, the
+        // copies' writes alone took 73 cycles per 2048 weights), permuted so that the lanes' reads meet no bank twice.
+        const uint32_t wslot = c * 128 + ((g ^ (2 * c)) << 4);
         int pr = s0 / per_rank, todo = s1 - s0;
-        int in_rank, in_group;              // steps to the end of the rank's shard and of the group
-        const uint32_t* wp;
+        int in_rank, in_group;              // stages to the end of the rank's shard and of the group
+        const uint8_t* wp;
         const uint16_t* xp[NT];
         const uint16_t* sp;
         const int8_t* zp = nullptr;
         bool new_group = true;
-        auto enter = [&](int at) {          // step `at` of rank pr
+        auto enter = [&](int at) {          // stage `at` of rank pr
             in_rank = per_rank - at;
             in_group = per_group - at % per_group;
-            wp = a.w[pr] + (static_cast<long long>(at) * 4 + c) * a.n + col0 + 4 * g;
+            wp = reinterpret_cast<const uint8_t*>(a.w[pr] + (static_cast<long long>(at) * 4 * SS + c) * a.n + col0 + 4 * g);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int row = row0 + 8 * t + g;
-                xp[t] = a.x[pr] + static_cast<long long>(row < a.m ? row : 0) * a.k + at * kStep + 8 * c;
+                xp[t] = a.x[pr] + static_cast<long long>(row < a.m ? row : 0) * a.k + at * SS * kStep + 8 * c;
             }
             const long long so = static_cast<long long>(at / per_group) * a.n + col0 + 4 * g;
             sp = a.scale[pr] + so;
             if constexpr (ZERO) zp = a.zero[pr] + so;
         };
         enter(s0 - pr * per_rank);
+        int nx[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) nx[t] = row0 + 8 * t + g < a.m ? 16 : 0;
         auto load = [&](int stage) {
             if (todo > 0) {
                 const uint32_t so = ring + stage * SB;
-                cp_async<16>(so + lane * 16, wp, in0);
-                cp_async<16>(so + 512 + lane * 16, wp + 32, in1);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    cp_async<16>(so + 1024 + t * 512 + lane * 16, xp[t], row0 + 8 * t + g < a.m);
-                    xp[t] += kStep;
+                for (int u = 0; u < SS; ++u) {
+                    cp_async<16>(so + u * 1024 + wslot, wp, n0);
+                    cp_async<16>(so + u * 1024 + 512 + wslot, wp + 128, n1);
+                    wp += rows_w;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) cp_async<16>(so + XO + (u * NT + t) * 512 + lane * 16, xp[t] + u * kStep, nx[t]);
                 }
-                wp += 4LL * a.n;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) xp[t] += SS * kStep;
                 if (new_group) {
                     new_group = false;
-                    cp_async<8>(so + 1024 + NT * 512 + lane * 16, sp, in0);
-                    cp_async<8>(so + 1024 + NT * 512 + lane * 16 + 8, sp + 32, in1);
-                    sp += a.n;
-                    if constexpr (ZERO) {
-                        cp_async<4>(so + 1536 + NT * 512 + lane * 8, zp, in0);
-                        cp_async<4>(so + 1536 + NT * 512 + lane * 8 + 4, zp + 32, in1);
-                        zp += a.n;
+                    if (c == 0) {
+                        cp_async<8>(so + CO + g * 16, sp, n0 / 2);
+                        cp_async<8>(so + CO + g * 16 + 8, sp + 32, n1 / 2);
+                        if constexpr (ZERO) {
+                            cp_async<4>(so + CO + 128 + g * 8, zp, n0 / 4);
+                            cp_async<4>(so + CO + 128 + g * 8 + 4, zp + 32, n1 / 4);
+                        }
                     }
+                    sp += a.n;
+                    if constexpr (ZERO) zp += a.n;
                 }
                 --todo;
                 if (--in_group == 0) {
@@ -227,9 +239,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i);
 
-        int left = per_group - s0 % per_group;      // steps to the end of the group (shards are whole groups)
+        int left = per_group - s0 % per_group;      // stages to the end of the group (shards are whole groups)
         bool fresh = true;
-        float sc[8];
+        uint4 sc;                                   // scales of the lane's 8 columns
         uint32_t off[ZERO ? 8 : 1], off16[ZERO ? 8 : 1];
         if constexpr (!ZERO) {
             off[0] = pair<BF16>(BF16 ? -136.f : -1032.f);
@@ -244,12 +256,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_
                 const uint8_t* slot = ring_p + st * SB;
                 if (fresh) {
                     fresh = false;
-                    const uint4 s4 = *reinterpret_cast<const uint4*>(slot + 1024 + NT * 512 + lane * 16);
-                    const uint32_t sv[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sc[i] = to_float16bit<BF16>(static_cast<uint16_t>(sv[i / 2] >> (16 * (i & 1))));
+                    __syncwarp();                   // the lanes 4 g copied it for the others
+                    sc = *reinterpret_cast<const uint4*>(slot + CO + g * 16);
                     if constexpr (ZERO) {
-                        const uint2 z2 = *reinterpret_cast<const uint2*>(slot + 1536 + NT * 512 + lane * 8);
+                        const uint2 z2 = *reinterpret_cast<const uint2*>(slot + CO + 128 + g * 8);
                         const uint32_t zv[2] = {z2.x ^ 0x80808080u, z2.y ^ 0x80808080u};      // z + 128
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -259,43 +269,50 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_
                             if constexpr (!BF16) off16[i] = add2<false>(off[i], 0x63806380u);           // + 960
                         }
                     }
+                    __syncwarp();                   // read before a later stage's copy lands in the slot
                 }
-                const uint4 w0 = *reinterpret_cast<const uint4*>(slot + lane * 16);
-                const uint4 w1 = *reinterpret_cast<const uint4*>(slot + 512 + lane * 16);
-                uint32_t b[NT][4];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(slot + 1024 + t * 512 + lane * 16);
-                    b[t][0] = __byte_perm(x.x, x.z, 0x5410);    // (x0, x4)
-                    b[t][1] = __byte_perm(x.x, x.z, 0x7632);    // (x1, x5)
-                    b[t][2] = __byte_perm(x.y, x.w, 0x5410);
-                    b[t][3] = __byte_perm(x.y, x.w, 0x7632);
-                }
-                const uint32_t wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-                // all tiles once per half: products into one accumulator do not follow each other
-                auto half = [&](auto hc) {
-                    constexpr int H = decltype(hc)::value;
+                for (int u = 0; u < SS; ++u) {
+                    const uint4 w0 = *reinterpret_cast<const uint4*>(slot + u * 1024 + wslot);
+                    const uint4 w1 = *reinterpret_cast<const uint4*>(slot + u * 1024 + 512 + wslot);
+                    uint32_t b[NT][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
-                        uint32_t a0, a1, a2, a3;
-                        codes<BF16, H>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], a0, a2);
-                        codes<BF16, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(slot + XO + (u * NT + t) * 512 + lane * 16);
+                        b[t][0] = __byte_perm(x.x, x.z, 0x5410);    // (x0, x4)
+                        b[t][1] = __byte_perm(x.x, x.z, 0x7632);    // (x1, x5)
+                        b[t][2] = __byte_perm(x.y, x.w, 0x5410);
+                        b[t][3] = __byte_perm(x.y, x.w, 0x7632);
                     }
-                };
-                half(std::integral_constant<int, 0>{});
-                half(std::integral_constant<int, 1>{});
+                    const uint32_t wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    // all tiles once per half: products into one accumulator do not follow each other
+                    auto half = [&](auto hc) {
+                        constexpr int H = decltype(hc)::value;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
+                            uint32_t a0, a1, a2, a3;
+                            codes<BF16, H>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], a0, a2);
+                            codes<BF16, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
+                        }
+                    };
+                    half(std::integral_constant<int, 0>{});
+                    half(std::integral_constant<int, 1>{});
+                }
                 if (--left == 0 || sb + st + 1 == s1) {
+                    const uint32_t sv[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int q = 0; q < 4; q += 2) {
+                            const float f = to_float16bit<BF16>(static_cast<uint16_t>(q ? sv[i] >> 16 : sv[i]));
 #pragma unroll
-                            for (int q = 0; q < 4; q += 2) {
-                                fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], sc[2 * i + (q >> 1)]);
+                            for (int t = 0; t < NT; ++t) {
+                                fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], f);
                                 part[t][i][q] = part[t][i][q + 1] = 0.f;
                             }
+                        }
                     left = per_group;
                     fresh = true;
                 }
@@ -320,48 +337,49 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && !ZERO ? T_WOC : 2) w4_
             }
     __syncthreads();
     if (splits > 1) cluster_sync();
-    // block `split` of the cluster finishes every splits-th pair of columns
-    constexpr int pairs = WO * NT * 8 * kCols / 2;
-    for (int x = threadIdx.x + split * kWarps * 32; x < pairs; x += kWarps * 32 * splits) {
-        const int cw = x / (SF / 2), in = x % (SF / 2) * 2;     // column group, place in its sums
-        const int row = row0 + in / kCols, col = (slab * WO + cw) * kCols + in % kCols;
+    // the blocks of a cluster share the pairs of columns
+    for (int x = threadIdx.x + split * kWarps * 32; x < SF / 2; x += kWarps * 32 * splits) {
+        const int row = row0 + 2 * x / kCols, col = col0 + 2 * x % kCols;
         if (row >= a.m || col >= a.n) continue;
         float2 y = make_float2(0.f, 0.f);
-        for (int b = 0; b < splits; ++b)
+        for (int b = 0; b < splits; ++b) {
+            const uint32_t at = splits > 1 ? map_to_rank(smem_u32(sums + 2 * x), b) : 0u;
+            float2 v[kWarps];
 #pragma unroll
-            for (int k = 0; k < WK; ++k) {
-                const uint32_t at = smem_u32(sums + (k * WO + cw) * SF + in);
-                float2 v;
-                if (splits > 1) {
-                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(map_to_rank(at, b)) : "memory");
-                } else {
-                    v = *reinterpret_cast<const float2*>(sums + (k * WO + cw) * SF + in);
-                }
-                y.x += v.x;
-                y.y += v.y;
+            for (int k = 0; k < kWarps; ++k) {
+                if (splits > 1)
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(at + k * SF * 4) : "memory");
+                else
+                    v[k] = *reinterpret_cast<const float2*>(sums + k * SF + 2 * x);
             }
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                y.x += v[k].x;
+                y.y += v[k].y;
+            }
+        }
         const uint32_t o = pack2<BF16>(__float_as_uint(y.x), __float_as_uint(y.y));
         for (int r = 0; r < a.R; ++r) *reinterpret_cast<uint32_t*>(a.out[r] + static_cast<long long>(row) * a.n + col) = o;
     }
     if (splits > 1) cluster_sync();     // no block leaves while its sums are read
 }
 
-template <bool BF16, int NT, bool ZERO, int WO>
+template <bool BF16, int NT, bool ZERO, int SS>
 cudaError_t launch_t(const W4Args& a, cudaStream_t stream) {
-    auto kern = w4_kernel<BF16, NT, ZERO, WO>;
+    auto kern = w4_kernel<BF16, NT, ZERO, SS>;
     static std::atomic<unsigned char> smem_set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, w4_smem<NT>())) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, w4_smem<NT, SS>())) != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.n + WO * kCols - 1) / (WO * kCols) * a.splits), static_cast<unsigned>((a.m + 8 * NT - 1) / (8 * NT)), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.n + kCols - 1) / kCols * a.splits), static_cast<unsigned>((a.m + 8 * NT - 1) / (8 * NT)), 1);
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = w4_smem<NT>();
+    cfg.dynamicSmemBytes = w4_smem<NT, SS>();
     cfg.stream = stream;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -378,14 +396,14 @@ cudaError_t launch_t(const W4Args& a, cudaStream_t stream) {
 }
 
 template <bool BF16, int NT, bool ZERO>
-cudaError_t launch_w(const W4Args& a, int wo, cudaStream_t stream) {
-    return wo == 4 ? launch_t<BF16, NT, ZERO, 4>(a, stream) : wo == 2 ? launch_t<BF16, NT, ZERO, 2>(a, stream) : launch_t<BF16, NT, ZERO, 1>(a, stream);
+cudaError_t launch_s(const W4Args& a, cudaStream_t stream) {
+    return a.group % (2 * kStep) == 0 ? launch_t<BF16, NT, ZERO, 2>(a, stream) : launch_t<BF16, NT, ZERO, 1>(a, stream);
 }
 template <bool BF16>
-cudaError_t launch_b(const W4Args& a, int wo, cudaStream_t stream) {
+cudaError_t launch_b(const W4Args& a, cudaStream_t stream) {
     const bool two = a.m > 8, zero = a.zero[0] != nullptr;
-    if (two) return zero ? launch_w<BF16, 2, true>(a, wo, stream) : launch_w<BF16, 2, false>(a, wo, stream);
-    return zero ? launch_w<BF16, 1, true>(a, wo, stream) : launch_w<BF16, 1, false>(a, wo, stream);
+    if (two) return zero ? launch_s<BF16, 2, true>(a, stream) : launch_s<BF16, 2, false>(a, stream);
+    return zero ? launch_s<BF16, 1, true>(a, stream) : launch_s<BF16, 1, false>(a, stream);
 }
 
 }  // namespace
@@ -393,24 +411,19 @@ cudaError_t launch_b(const W4Args& a, int wo, cudaStream_t stream) {
 cudaError_t launch_w4(const W4Args& args, bool bf16, int sm_count, cudaStream_t stream) {
     W4Args a = args;
     const long long steps = static_cast<long long>(a.k / kStep) * a.R;
-    const long long resident = 2LL * sm_count, tiles = (a.m + (a.m > 8 ? 15 : 7)) / (a.m > 8 ? 16 : 8);
+    const int rows = a.m > 8 ? 16 : 8;
+    const long long resident = 2LL * sm_count, tiles = static_cast<long long>((a.n + kCols - 1) / kCols) * ((a.m + rows - 1) / rows);
     double best = 1e300;
-    int wo = 1;
     a.splits = 1;
-    for (int w : {4, 2, 1})
-        for (int k : {1, 2, 4, 8}) {
-            const long long blocks = (a.n + w * kCols - 1) / (w * kCols) * k * tiles;
-            const double per = std::max(1.0, static_cast<double>(steps) / (k * (kWarps / w)));
-            const double t = static_cast<double>((blocks + resident - 1) / resident) * (per + 8.0);
-            if (t < best) {
-                best = t;
-                wo = w;
-                a.splits = k;
-            }
+    for (int k = 1; k <= 8; ++k) {
+        const double t = static_cast<double>((tiles * k + resident - 1) / resident) * (static_cast<double>(steps) / (k * kWarps) + 8.0);
+        if (t < best) {
+            best = t;
+            a.splits = k;
         }
-    if (const char* e = std::getenv("W4_WO")) wo = std::atoi(e);
+    }
     if (const char* e = std::getenv("W4_KS")) a.splits = std::atoi(e);
-    return bf16 ? launch_b<true>(a, wo, stream) : launch_b<false>(a, wo, stream);
+    return bf16 ? launch_b<true>(a, stream) : launch_b<false>(a, stream);
 }
 
 }  // namespace coc

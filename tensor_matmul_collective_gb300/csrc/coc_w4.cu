@@ -8,8 +8,11 @@
 // per group in fp32, and the weight itself is never rounded.
 //
 // What bounds it.  k n / 2 bytes of weights, read once: the operations per
-// byte (4 m) are few, but taking codes out of words costs instructions, about
-// 1.2 per weight pair, near half of what the SMs issue at full bandwidth.
+// byte (4 m) are few, but taking codes out of words costs instructions: a
+// shift, a mask and an addition per pair, 88 of the 150 that a warp issues for
+// 2048 weights at up to 8 tokens (205 at 16), and the SMs' instruction rate is
+// the bound: 3.0 TB/s of weights at n 8192, k 8 x 1024, m 8 (12.3 us), 3.4 at
+// n 14336, k 8 x 7168, m 16 with zero points (130 us).
 // W^T is the A operand of mma.sync (16 weight columns x 16 of k) and x^T the B
 // operand (8 tokens).  A word holds 8 codes along k of one column; a mask
 // takes two codes four apart into the halves of a register, so the pairs
@@ -18,16 +21,19 @@
 // (bf16: 128) makes them floating-point numbers, and one addition takes off
 // 1024 + z.
 //
-// A lane reads whole 16-byte pieces (4 columns) of the rows as they lie in
-// memory, and the asynchronous copies land in a slot that the same lane reads
-// back: no barrier, no bank conflict.
+// Words and x come through a ring in shared memory in which a lane reads back
+// only what it copied itself (but for the scales): no barrier in the loop.
 //
-// Split.  A warp takes 64 columns and a contiguous range of the contraction;
-// the ranges of a block's warps and of a cluster's blocks are added through
-// shared memory in their order.
+// Split.  A block takes 64 columns, its 8 warps contiguous ranges of the
+// contraction; a cluster's blocks take further ranges.  All ranges are added
+// through shared memory in their order.
+//
+// Tried: codes as the A operand of tcgen05.mma in tensor memory, roles in 16
+// warps.  Writing operands, permuting x and waiting cost more instructions
+// (444 per 2048 weights at 16 tokens) than the registers' way: 221 us at
+// n 14336.
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <type_traits>
 
 #include "coc_kv.cuh"
@@ -39,13 +45,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kCols = 64;               // columns of a block; its warps split the contraction
 constexpr int kStep = 32;               // contraction of one step: 4 word rows
-#ifndef T_WST
-#define T_WST 3
-#endif
-#ifndef T_WOC
-#define T_WOC 2
-#endif
-constexpr int kStages = T_WST;          // stages of SS steps in a warp's ring
+// Stages of a warp's ring: two blocks' rings fill an SM's shared memory.
+template <int SS>
+constexpr int stages() { return SS == 4 ? 2 : SS == 2 ? 3 : 5; }
 
 // A stage: SS x (two 16-byte pieces of words a lane, NT of x), then scales
 // (16 bytes) and zero points (8 bytes) of the lanes 4 g.
@@ -55,7 +57,7 @@ template <int NT>
 constexpr int sum_floats() { return NT * 8 * kCols; }                      // one warp's sums
 template <int NT, int SS>
 constexpr int w4_smem() {
-    const int ring = kWarps * kStages * stage_bytes<NT, SS>();
+    const int ring = kWarps * stages<SS>() * stage_bytes<NT, SS>();
     const int sums = kWarps * sum_floats<NT>() * 4;
     return ring > sums ? ring : sums;
 }
@@ -136,12 +138,18 @@ __device__ __forceinline__ uint32_t pair(float f) {
     return pack2<BF16>(__float_as_uint(f), __float_as_uint(f));
 }
 
+// Where part i of `all` stages in `ways` nearly equal parts begins.
+__device__ __forceinline__ int part_begin(int all, int i, int ways) {
+    const int each = all / ways;
+    return each * i + min(i, all - each * ways);
+}
+
 // Block: 64 columns, 8 NT rows of x (blockIdx.y), kWarps ranges of the
 // contraction; cluster: blocks with the same columns and further ranges.  SS
 // steps make a stage (groups are whole stages).
 template <bool BF16, int NT, bool ZERO, int SS>
-__global__ void __launch_bounds__(kWarps * 32, T_WOC) w4_kernel(const __grid_constant__ W4Args a) {
-    constexpr int SB = stage_bytes<NT, SS>();
+__global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constant__ W4Args a) {
+    constexpr int SB = stage_bytes<NT, SS>(), kStages = stages<SS>();
     constexpr int XO = SS * 1024, CO = SS * 512 * (2 + NT);      // x, scales in a stage
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -153,8 +161,8 @@ __global__ void __launch_bounds__(kWarps * 32, T_WOC) w4_kernel(const __grid_con
 
     // this warp's stages, all ranks' shards one after another
     const int per_rank = a.k / (kStep * SS), per_group = a.group / (kStep * SS);
-    const long long all = static_cast<long long>(per_rank) * a.R, ways = static_cast<long long>(splits) * kWarps, way = split * kWarps + warp;
-    const int s0 = static_cast<int>(all * way / ways), s1 = static_cast<int>(all * (way + 1) / ways);
+    const int s0 = part_begin(per_rank * a.R, split * kWarps + warp, splits * kWarps);
+    const int s1 = part_begin(per_rank * a.R, split * kWarps + warp + 1, splits * kWarps);
 
     float acc[NT][4][4], part[NT][4][4];
 #pragma unroll
@@ -397,6 +405,7 @@ cudaError_t launch_t(const W4Args& a, cudaStream_t stream) {
 
 template <bool BF16, int NT, bool ZERO>
 cudaError_t launch_s(const W4Args& a, cudaStream_t stream) {
+    if (NT == 1 && a.group % (4 * kStep) == 0) return launch_t<BF16, NT, ZERO, NT == 1 ? 4 : 2>(a, stream);
     return a.group % (2 * kStep) == 0 ? launch_t<BF16, NT, ZERO, 2>(a, stream) : launch_t<BF16, NT, ZERO, 1>(a, stream);
 }
 template <bool BF16>
@@ -408,21 +417,27 @@ cudaError_t launch_b(const W4Args& a, cudaStream_t stream) {
 
 }  // namespace
 
+// Blocks of a cluster (ranges of the contraction) by the steps of the busiest
+// SM: 64-column slabs that do not divide evenly over the SMs are evened out by
+// halves and quarters, as far as joining them costs less (about 3 steps a
+// block and 2 a further range).  Two blocks on an SM are no faster than one
+// after the other: the SM's instruction rate is the bound.  Measured, ranges 1 /
+// 2 / 4: n 4096, k 4096, m 1 6.4 / 5.6 / 5.9 us; n 8192, k 8 x 1024, m 8 12.3 /
+// 14.0 / 20; n 14336, k 8 x 7168, m 16 159 / 130 / 152.
 cudaError_t launch_w4(const W4Args& args, bool bf16, int sm_count, cudaStream_t stream) {
     W4Args a = args;
-    const long long steps = static_cast<long long>(a.k / kStep) * a.R;
+    const double steps = static_cast<double>(a.k / kStep) * a.R;
     const int rows = a.m > 8 ? 16 : 8;
-    const long long resident = 2LL * sm_count, tiles = static_cast<long long>((a.n + kCols - 1) / kCols) * ((a.m + rows - 1) / rows);
+    const long long tiles = static_cast<long long>((a.n + kCols - 1) / kCols) * ((a.m + rows - 1) / rows);
     double best = 1e300;
     a.splits = 1;
-    for (int k = 1; k <= 8; ++k) {
-        const double t = static_cast<double>((tiles * k + resident - 1) / resident) * (static_cast<double>(steps) / (k * kWarps) + 8.0);
+    for (int k : {1, 2, 4}) {
+        const double t = static_cast<double>((tiles * k + sm_count - 1) / sm_count) * (steps / (k * kWarps) + 3.0) + 2.0 * (k - 1);
         if (t < best) {
             best = t;
             a.splits = k;
         }
     }
-    if (const char* e = std::getenv("W4_KS")) a.splits = std::atoi(e);
     return bf16 ? launch_b<true>(a, stream) : launch_b<false>(a, stream);
 }
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 
 import torch
 
@@ -62,6 +63,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libcoc.so (built by __graft_entry__.build() or build.py)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -96,13 +99,14 @@ def lib() -> ctypes.CDLL:
             L.coc_fused_matmul.restype = i32
             L.coc_matmul.argtypes = [i32, i64, i64, i64, pp, pp, vp, i32, vp]
             L.coc_matmul.restype = i32
-            L.coc_kv_cache_append.argtypes = [vp, i64, i64, pp, vp, pp, vp, i32, pp, vp, pp, vp, i64, vp, vp, vp, vp, i64,
+            # pointer arrays as addresses (see _words)
+            L.coc_kv_cache_append.argtypes = [vp, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64,
                                               i32, i32, i32, vp]
             L.coc_kv_cache_append.restype = i32
-            L.coc_kv_cache_attention.argtypes = [vp, i64, i64, i32, pp, vp, pp, vp, i64, vp, vp, ctypes.c_float, i64, i64,
+            L.coc_kv_cache_attention.argtypes = [vp, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp, ctypes.c_float, i64, i64,
                                                  i32, vp]
             L.coc_kv_cache_attention.restype = i32
-            L.coc_matmul_all_reduce_w4a16.argtypes = [i32, i64, i64, i64, pp, pp, pp, pp, i64, pp, i32, vp]
+            L.coc_matmul_all_reduce_w4a16.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, i64, vp, i32, vp]
             L.coc_matmul_all_reduce_w4a16.restype = i32
             L.coc_sync_status.argtypes = [vp]
             L.coc_sync_status.restype = i32
@@ -526,12 +530,27 @@ class KVCache:
                    [scales() for _ in range(R)])
 
 
-_I64x2 = ctypes.c_int64 * 2
+def _words(*parts):
+    """Host words (pointers and strides) in one buffer: (the buffer, the address of each part).
+
+    The decode-step calls are short; one buffer costs less than a ctypes array
+    for every argument."""
+    flat = []
+    for p in parts:
+        flat += p
+    buf = array("q", flat)
+    at = buf.buffer_info()[0]
+    where = []
+    for p in parts:
+        where.append(at)
+        at += 8 * len(p)
+    return buf, where
 
 
 def _check_heads(ts, name, R, tokens, d, dtype, device):
     """R tensors of tokens x heads x d with the same strides, a head's values
-    adjacent (slices of a fused projection's output pass)."""
+    adjacent (slices of a fused projection's output pass): (heads, [token
+    stride, head stride], pointers)."""
     if not isinstance(ts, (list, tuple)) or len(ts) != R:
         raise ValueError(f"{name} must be a list of {R} tensors, one per rank")
     t0 = ts[0]
@@ -542,6 +561,7 @@ def _check_heads(ts, name, R, tokens, d, dtype, device):
         raise ValueError(f"{name}[0] has shape {tuple(shape)}, expected ({tokens}, heads, {d})")
     if stride[2] != 1 and d > 1:
         raise ValueError(f"{name}: the values of a head must be adjacent")
+    ptrs = []
     for i, t in enumerate(ts):
         if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
             raise TypeError(f"{name}[{i}] must be a {dtype} tensor")
@@ -549,17 +569,31 @@ def _check_heads(ts, name, R, tokens, d, dtype, device):
             raise ValueError(f"{name}[{i}] is on {t.device}, expected {device}")
         if t.shape != shape or t.stride() != stride:
             raise ValueError(f"{name}[{i}] has another shape or other strides than {name}[0]")
-    return shape[1], _I64x2(stride[0], stride[1])
+        ptrs.append(t.data_ptr())
+    return shape[1], [stride[0], stride[1]], ptrs
+
+
+def _head_outs(outs, name, R, shape, dtype, device):
+    """R packed outputs, given or new, and their pointers."""
+    if outs is None:
+        outs = [torch.empty(shape, dtype=dtype, device=device) for _ in range(R)]
+    else:
+        _check_list(outs, name, shape, dtype, device)
+        if len(outs) != R:
+            raise ValueError("need one output per rank")
+        outs = list(outs)
+    return outs, [t.data_ptr() for t in outs]
 
 
 def _check_seqs(cache, tokens, block_table, lens, cu_new):
     """(sequences, table width) of the arrays that index the cache."""
+    dev = cache.device
     seqs = lens.shape[0] if lens.dim() == 1 else -1
     if seqs < 0 or block_table.dim() != 2 or block_table.shape[0] != seqs:
         raise ValueError("lens must be (sequences,) and block_table (sequences, pages per sequence)")
     for name, t in (("block_table", block_table), ("lens", lens), ("cu_new", cu_new)):
-        if t is not None and (t.dtype is not torch.int32 or t.device != cache.device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {cache.device}")
+        if t is not None and (t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
     if cu_new is None:
         if tokens != seqs:
             raise ValueError(f"without cu_new every sequence has one new token: {tokens} tokens, {seqs} sequences")
@@ -586,18 +620,18 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
         raise ValueError("ks must be a list of tokens x kv_heads x head_dim tensors, one per rank")
     k0, R, d, dev = ks[0], cache.R, cache.head_dim, cache.device
     _check_device(k0)
-    code = _dtype_code(k0.dtype)
+    dt = k0.dtype
+    code = _dtype_code(dt)
     T = k0.shape[0]
-    hk, kstr = _check_heads(ks, "ks", R, T, d, k0.dtype, dev)
-    hv, vstr = _check_heads(vs, "vs", R, T, d, k0.dtype, dev)
+    hk, kstr, kp = _check_heads(ks, "ks", R, T, d, dt, dev)
+    hv, vstr, vp = _check_heads(vs, "vs", R, T, d, dt, dev)
     if hk != cache.kv_heads or hv != cache.kv_heads:
         raise ValueError(f"ks and vs must have the cache's {cache.kv_heads} heads")
     seqs, width = _check_seqs(cache, T, block_table, lens, cu_new)
-    hq, qstr, qp, qop = 0, None, None, None
+    hq, qstr, qp, qop = 0, [], [], []
     if qs is not None:
-        hq, qstr = _check_heads(qs, "qs", R, T, d, k0.dtype, dev)
-        q_outs = _outs(q_outs, R, (T, hq, d), k0.dtype, dev)
-        qp, qop = _ptrs(qs), _ptrs(q_outs)
+        hq, qstr, qp = _check_heads(qs, "qs", R, T, d, dt, dev)
+        q_outs, qop = _head_outs(q_outs, "q_outs", R, (T, hq, d), dt, dev)
     elif q_outs is not None:
         raise ValueError("q_outs without qs")
     cp = sp = None
@@ -608,10 +642,13 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
         _check_list((cos, sin), "cos/sin", cos.shape, torch.float32, dev)
         positions, rot = cos.shape[0], 2 * cos.shape[1]
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    _check(lib().coc_kv_cache_append(cache._ref, T, seqs, _ptrs(ks), kstr, _ptrs(vs), vstr, hq, qp, qstr, qop,
-                                     block_table.data_ptr(), width, lens.data_ptr(),
-                                     None if cu_new is None else cu_new.data_ptr(), cp, sp, positions, rot,
-                                     int(bool(interleaved)), code, _stream(stream)))
+    buf, at = _words(kp, kstr, vp, vstr, qp, qstr, qop)
+    st = lib().coc_kv_cache_append(cache._ref, T, seqs, at[0], at[1], at[2], at[3], hq, at[4], at[5], at[6],
+                                   block_table.data_ptr(), width, lens.data_ptr(),
+                                   None if cu_new is None else cu_new.data_ptr(), cp, sp, positions, rot,
+                                   1 if interleaved else 0, code, _stream(stream))
+    if st != OK:
+        _check(st)
     return q_outs
 
 
@@ -631,15 +668,18 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
         raise ValueError("qs must be a list of tokens x q_heads x head_dim tensors, one per rank")
     q0, R, d, dev = qs[0], cache.R, cache.head_dim, cache.device
     _check_device(q0)
-    code = _dtype_code(q0.dtype)
+    dt = q0.dtype
+    code = _dtype_code(dt)
     T = q0.shape[0]
-    hq, qstr = _check_heads(qs, "qs", R, T, d, q0.dtype, dev)
+    hq, qstr, qp = _check_heads(qs, "qs", R, T, d, dt, dev)
     seqs, width = _check_seqs(cache, T, block_table, lens, cu_new)
-    outs = _outs(outs, R, (T, hq, d), q0.dtype, dev)
-    _check(lib().coc_kv_cache_attention(cache._ref, T, seqs, hq, _ptrs(qs), qstr, _ptrs(outs), block_table.data_ptr(),
-                                        width, lens.data_ptr(), None if cu_new is None else cu_new.data_ptr(),
-                                        d ** -0.5 if scale is None else float(scale), int(window), int(sinks), code,
-                                        _stream(stream)))
+    outs, op = _head_outs(outs, "outs", R, (T, hq, d), dt, dev)
+    buf, at = _words(qp, qstr, op)
+    st = lib().coc_kv_cache_attention(cache._ref, T, seqs, hq, at[0], at[1], at[2], block_table.data_ptr(), width,
+                                      lens.data_ptr(), None if cu_new is None else cu_new.data_ptr(),
+                                      d ** -0.5 if scale is None else float(scale), int(window), int(sinks), code, _stream(stream))
+    if st != OK:
+        _check(st)
     return outs
 
 
@@ -659,15 +699,18 @@ def matmul_all_reduce_w4a16(xs, wqs, scales, group_size: int, zeros=None, outs=N
     _check_list(xs, "xs", (m, ks), dt, dev)
     _check_list(wqs, "wqs", (ks // 8, n), torch.int32, dev)
     for name, views, want in (("scales", scales, dt), ("zeros", zeros, torch.int8)):
-        if views is None:
+        if views is None and name == "zeros":
             continue
         if len(views) != R:
             raise ValueError(f"need one {name} tensor per rank")
         _check_list(views, name, (ks // group_size, n), want, dev)
-    outs = _outs(outs, R, (m, n), dt, dev)
-    _check(lib().coc_matmul_all_reduce_w4a16(R, m, n, ks, _ptrs(xs), _ptrs(wqs), _ptrs(scales),
-                                             None if zeros is None else _ptrs(zeros), int(group_size), _ptrs(outs), code,
-                                             _stream(stream)))
+    outs, op = _head_outs(outs, "outs", R, (m, n), dt, dev)
+    buf, at = _words([t.data_ptr() for t in xs], [t.data_ptr() for t in wqs], [t.data_ptr() for t in scales],
+                     [] if zeros is None else [t.data_ptr() for t in zeros], op)
+    st = lib().coc_matmul_all_reduce_w4a16(R, m, n, ks, at[0], at[1], at[2], None if zeros is None else at[3], int(group_size),
+                                           at[4], code, _stream(stream))
+    if st != OK:
+        _check(st)
     return outs
 
 

@@ -1574,6 +1574,10 @@ COC_API coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t to
         if ((st = check_ptrs(q, R, true, "q")) != COC_OK || (st = check_ptrs(q_out, R, true, "q_out")) != COC_OK) return st;
         if ((st = check_strides(q_strides, "q")) != COC_OK) return st;
     }
+    if (tokens * R * std::max(q_heads, 2 * cache->kv_heads) > (int64_t(1) << 27) ||
+        seqs * R * cache->kv_heads > (int64_t(1) << 28))
+        return fail(COC_ERR_SHAPE, "%lld tokens of %d heads on %d ranks: at most 2^27 rows a call", (long long)tokens,
+                    std::max(q_heads, 2 * cache->kv_heads), R);
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != COC_OK) return st;
     KvAppendArgs a;

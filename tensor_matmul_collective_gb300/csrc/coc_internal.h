@@ -210,6 +210,7 @@ struct KvAppendArgs {
     long long q_token, q_head, k_token, k_head, v_token, v_head;
     long long table_width, pages, positions;
     int R, seqs, tokens, heads, q_heads, d, page, rot, interleaved;
+    bool vec_angles;                     // rows of cos and sin in whole 16-byte pieces (set by launch_kv_append)
 };
 struct KvAttnArgs {
     const uint8_t* ck[COC_MAX_RANKS];

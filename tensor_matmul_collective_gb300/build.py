@@ -1,11 +1,14 @@
 """Build libcoc.so in-tree: nvcc for sm_103a only, the translation units
-compiled in parallel, linked with the static CUDA runtime."""
+compiled in parallel, linked with the static CUDA runtime; and beside it
+_coc_marshal.so, the decode-step calls' argument marshalling (host code against
+this PyTorch's headers)."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -17,6 +20,23 @@ HEADERS = ["coc_internal.h", "coc_dequant.cuh", "coc_ptx.cuh", "coc_kv.cuh", os.
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
+
+
+MARSHAL_SRC = os.path.join(CSRC, "coc_marshal.cpp")
+MARSHAL = os.path.join(HERE, "_coc_marshal.so")
+
+
+def _marshal_command():
+    """The compiler call for _coc_marshal.so, None where there is nothing to build it against."""
+    import torch
+    inc, lib = (os.path.join(os.path.dirname(torch.__file__), d) for d in ("include", "lib"))
+    py = sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    if not (os.path.exists(os.path.join(py, "Python.h")) and os.path.exists(os.path.join(inc, "ATen", "ATen.h"))):
+        return None
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *[f"-isystem{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), py, cuda)], MARSHAL_SRC, "-o", MARSHAL,
+            f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-Wl,-rpath,{lib}"]
 
 
 def nvcc() -> str:
@@ -37,6 +57,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS]
     objs, procs = [], []
+    marshal = _marshal_command() if force or _stale(MARSHAL, [MARSHAL_SRC, headers[-1]]) else None
+    if marshal is not None:
+        marshal = (marshal, subprocess.Popen(marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT))
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -57,6 +80,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    if marshal is not None:
+        out, _ = marshal[1].communicate()
+        if marshal[1].returncode != 0:
+            raise RuntimeError(f"g++ failed: {' '.join(marshal[0])}\n{out.decode(errors='replace')}")
     return LIB
 
 

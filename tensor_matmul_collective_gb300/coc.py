@@ -128,6 +128,25 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_native = None
+
+
+def _marshal():
+    """_coc_marshal with the entry points' addresses, or False where it was not
+    built: then the checks below do its work, more slowly."""
+    global _native
+    if _native is None:
+        L = lib()
+        try:
+            from . import _coc_marshal as m
+        except ImportError:
+            m = None
+        _native = False if m is None else (
+            m, *(ctypes.cast(f, ctypes.c_void_p).value for f in (L.coc_kv_cache_append, L.coc_kv_cache_attention,
+                                                                L.coc_matmul_all_reduce_w4a16)))
+    return _native
+
+
 def _check(status: int) -> None:
     if status != OK:
         L = lib()
@@ -616,6 +635,14 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
     head_dim), None without qs."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
+    native = _native or _marshal()
+    if native:
+        done = native[0].append(native[1], cache._ref, ks, vs, block_table, lens, cos, sin, qs, q_outs, cu_new, interleaved,
+                                None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1]
     if not isinstance(ks, (list, tuple)) or not ks or not isinstance(ks[0], torch.Tensor) or ks[0].dim() != 3:
         raise ValueError("ks must be a list of tokens x kv_heads x head_dim tensors, one per rank")
     k0, R, d, dev = ks[0], cache.R, cache.head_dim, cache.device
@@ -664,6 +691,15 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
     q_heads x head_dim tensor per rank; a row that sees no key is zero."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
+    native = _native or _marshal()
+    if native:
+        done = native[0].attend(native[2], cache._ref, qs, block_table, lens, cu_new,
+                                cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks), outs,
+                                None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1]
     if not isinstance(qs, (list, tuple)) or not qs or not isinstance(qs[0], torch.Tensor) or qs[0].dim() != 3:
         raise ValueError("qs must be a list of tokens x q_heads x head_dim tensors, one per rank")
     q0, R, d, dev = qs[0], cache.R, cache.head_dim, cache.device
@@ -689,6 +725,13 @@ def matmul_all_reduce_w4a16(xs, wqs, scales, group_size: int, zeros=None, outs=N
     xs[q]: m x k_shard (fp16/bf16); wqs[q]: (k_shard/8) x n int32, eight 4-bit
     codes along k in a word (w4_pack); scales[q]: (k_shard/group_size) x n in
     the activations' type; zeros: None (z = 8) or int8 tensors like scales."""
+    native = _native or _marshal()
+    if native:
+        done = native[0].w4(native[3], xs, wqs, scales, int(group_size), zeros, outs, None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1]
     R, x0, w0 = _prep(xs, wqs)
     m, ks = x0.shape
     n = w0.shape[1]

@@ -476,3 +476,79 @@ def test_append_then_attend():
         rows = torch.tensor([lens[0], 52 + lens[1]])
         step = [split(t[rows].to(DEV), hq, hkv, d) for t in qkv]
         lens, cu = [n + 1 for n in lens], [0, 1, 2]
+
+
+# ----------------------------------------------------------------- the binding ---
+
+def test_binding_native_and_plain_marshalling_agree(monkeypatch):
+    """The compiled argument marshalling and the one in Python make the same calls."""
+    news, lens = [2, 1], [90, 40]
+    table, rk, rv, qs = build(2, 8, 2, 64, 32, news, lens, BF, seed=21)
+    tb, ln = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cu = torch.tensor(kv.offsets(news), dtype=torch.int32, device=DEV)
+    q = [x.to(DEV) for x in qs]
+    k = [torch.randn(3, 2, 64, device=DEV).to(BF) for _ in range(2)]
+    cos = torch.rand(100, 32, device=DEV)
+    got = []
+    for native in (True, False):
+        if not native:
+            monkeypatch.setattr(coc, "_native", False)
+            monkeypatch.setattr(coc, "_marshal", lambda: False)
+        else:
+            assert coc._marshal(), "the compiled marshalling was not built"
+        cache = to_cache(rk, rv)
+        turned = coc.kv_cache_append(k, k, cache, tb, ln, cos, cos, qs=q, cu_new=cu)
+        outs = coc.kv_cache_attention(turned, cache, tb, ln, cu_new=cu, window=50, sinks=2)
+        w = coc.matmul_all_reduce_w4a16([x.view(3, 512) for x in outs], [torch.full((64, 24), 0x12345678, dtype=torch.int32, device=DEV)] * 2,
+                                        [torch.ones(4, 24, dtype=BF, device=DEV)] * 2, 128)
+        got.append([*turned, *outs, *w, *[t.view(torch.uint8) for t in cache.k + cache.v], *cache.k_scale])
+    coc.sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_binding_refusals(monkeypatch, native):
+    if not native:
+        monkeypatch.setattr(coc, "_native", False)
+        monkeypatch.setattr(coc, "_marshal", lambda: False)
+    cache = coc.KVCache.empty(2, 4, 16, 2, 64)
+    x = [torch.zeros(3, 2, 64, dtype=BF, device=DEV) for _ in range(2)]
+    q = [torch.zeros(3, 4, 64, dtype=BF, device=DEV) for _ in range(2)]
+    tb = torch.zeros(3, 2, dtype=torch.int32, device=DEV)
+    ln = torch.ones(3, dtype=torch.int32, device=DEV)
+    cos = torch.zeros(4, 32, device=DEV)
+
+    def bad(err, f, *a, **kw):
+        with pytest.raises(err):
+            f(*a, **kw)
+    ap, at = coc.kv_cache_append, coc.kv_cache_attention
+    bad(ValueError, ap, x[:1], x, cache, tb, ln)                             # ranks
+    bad(TypeError, ap, x, [x[0], x[1].half()], cache, tb, ln)                # types
+    bad(TypeError, ap, [t.float() for t in x], x, cache, tb, ln)
+    bad(ValueError, ap, [t[:, :1] for t in x], x, cache, tb, ln)             # heads
+    bad(ValueError, ap, x, [x[0], x[1].transpose(1, 2).contiguous().transpose(1, 2)], cache, tb, ln)     # strides
+    bad(ValueError, ap, x, x, cache, tb, ln[:2])
+    bad(ValueError, ap, x, x, cache, tb.long(), ln)
+    bad(ValueError, ap, x, x, cache, tb, ln, cu_new=torch.zeros(3, dtype=torch.int32, device=DEV))
+    bad(ValueError, ap, x, x, cache, tb, ln, cos)                            # cos without sin
+    bad(TypeError, ap, x, x, cache, tb, ln, cos.half(), cos.half())
+    bad(coc.CocError, ap, x, x, cache, tb, ln, torch.zeros(4, 40, device=DEV), torch.zeros(4, 40, device=DEV))      # rot_dim > head_dim
+    bad(ValueError, ap, x, x, cache, tb, ln, q_outs=q)                       # outputs without qs
+    bad(ValueError, ap, x, x, cache, tb, ln, qs=q, q_outs=[q[0], q[1][:, :2]])
+    bad(ValueError, at, [t.cpu() for t in q], cache, tb, ln)
+    bad(coc.CocError, at, [t[:, :3].contiguous() for t in q], cache, tb, ln)     # 3 query heads on 2
+    bad(coc.CocError, at, q, cache, tb, ln, sinks=1)
+    bad(coc.CocError, at, q, cache, tb, ln, window=-1)
+    bad(TypeError, at, q, object(), tb, ln)
+    bad(ValueError, coc.KVCache, cache.k, cache.v[:1], cache.k_scale, cache.v_scale)
+    bad(TypeError, coc.KVCache, [t.view(torch.uint8) for t in cache.k], cache.v, cache.k_scale, cache.v_scale)
+    f = coc.matmul_all_reduce_w4a16
+    xs, ws, sc = [torch.zeros(2, 64, dtype=BF, device=DEV)], [torch.zeros(8, 16, dtype=torch.int32, device=DEV)], [torch.zeros(2, 16, dtype=BF, device=DEV)]
+    bad(coc.CocError, f, xs, ws, sc, 48)
+    bad(coc.CocError, f, xs, ws, [torch.zeros(4, 16, dtype=BF, device=DEV)], 16)      # groups below 32
+    bad(ValueError, f, xs, ws, [sc[0][:1]], 32)
+    bad(TypeError, f, xs, ws, [sc[0].half()], 32)
+    bad(TypeError, f, xs, [ws[0].long()], sc, 32)
+    bad(TypeError, f, xs, ws, sc, 32, zeros=[torch.zeros(2, 16, dtype=torch.int32, device=DEV)])
+    bad(coc.CocError, f, xs, [torch.zeros(8, 20, dtype=torch.int32, device=DEV)], [torch.zeros(2, 20, dtype=BF, device=DEV)], 32)   # n % 8
+    coc.sync_status()

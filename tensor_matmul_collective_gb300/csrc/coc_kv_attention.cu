@@ -295,67 +295,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
         const int near = min(far, (min(sinks, end_max) + kTile - 1) / kTile);   // sink tiles ahead of the window's
         const int tiles = near + max(0, (end_max + kTile - 1) / kTile - far);
 
-        // ---- Q as the B operand: lane (g, c) holds row g, the 16 values of
-        // each of its pieces (i * 4 + c), as the keys' lanes hold theirs
-        uint32_t qf[KL * 8];
-        float qscale = a.scale * 1.4426950408889634f;
-        {
-            const int rho = rt * kRows + g;
-            const bool valid = g < rows;
-            const int tok = sw.begin + rho / group;
-            const uint16_t* qp = a.q[r] + (valid ? tok * a.q_token + (h * group + rho % group) * a.q_head : 0);
-#pragma unroll
-            for (int i = 0; i < KL; ++i) {
-                const int e = (i * 4 + c) * 16;
-                uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-                if (valid && e < a.d) {
-                    v0 = *reinterpret_cast<const uint4*>(qp + e);
-                    v1 = *reinterpret_cast<const uint4*>(qp + e + 8);
-                }
-                qf[8 * i + 0] = v0.x; qf[8 * i + 1] = v0.y; qf[8 * i + 2] = v0.z; qf[8 * i + 3] = v0.w;
-                qf[8 * i + 4] = v1.x; qf[8 * i + 5] = v1.y; qf[8 * i + 6] = v1.z; qf[8 * i + 7] = v1.w;
-            }
-            if constexpr (BF16) {
-                uint32_t top = 0;   // the largest magnitude's bits
-#pragma unroll
-                for (int i = 0; i < KL * 8; ++i) {
-                    const uint32_t x = qf[i] & 0x7fff7fffu;
-                    top = max(top, max(x & 0xffffu, x >> 16));
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = static_cast<int>(top >> 7);                     // biased exponent; 255: not finite
-                const int up = (ex == 255 || ex == 0) ? 0 : min(126, 127 + 14 - ex);   // largest value to 2^14
-                const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-#pragma unroll
-                for (int i = 0; i < KL * 8; ++i)
-                    qf[i] = pack_half2(__uint_as_float(qf[i] << 16) * f, __uint_as_float(qf[i] & 0xffff0000u) * f);
-                qscale *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-            }
-        }
-        // row factors of the columns 2c, 2c + 1 of S^T
-        const float qs0 = __shfl_sync(0xffffffffu, qscale, 8 * c), qs1 = __shfl_sync(0xffffffffu, qscale, 8 * c + 4);
-
         float acc[MT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         // the columns' references, as what is added to log2 of a weight: kOffset - maximum
         float b0 = kOffset - kNoMax, b1 = b0, l0 = 0.f, l1 = 0.f;
 
-        // What only chunks at the ends of a row's keys need is kept out of the registers.
-        if (threadIdx.x < kRows) {
-            const int i = (rt * kRows + min(static_cast<int>(threadIdx.x), rows - 1)) / group;
-            limits.row_end[threadIdx.x] = end_of(i);
-            limits.row_from[threadIdx.x] = from_of(i);
-            if (threadIdx.x == 0) {
-                limits.end = end_max;
-                limits.from = from_min;
-                limits.sinks = sinks;
-            }
-        }
-        __syncthreads();
         const volatile Limits& lim = limits;
-
         // ---- the chunks of this warp: 16 keys j .. j + 15 of every tile
         const int tn = min(t1, tiles);
         // a chunk between these is seen whole by every row
@@ -398,11 +344,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
 #pragma unroll
                     for (int i = 0; i < KL; ++i) {
                         const uint8_t* p = kp + 8 * x * d + i * 64;
-                        const uint4 v = ALL ? load16(p) : load16_if(p, seen(j + g + 8 * x) && (EXACT || (i * 4 + c) * 16 < d));
+                        const uint4 v = ALL && EXACT ? load16(p) : load16_if(p, (ALL || seen(j + g + 8 * x)) && (EXACT || (i * 4 + c) * 16 < d));
                         kw[buf][x][4 * i] = v.x; kw[buf][x][4 * i + 1] = v.y; kw[buf][x][4 * i + 2] = v.z; kw[buf][x][4 * i + 3] = v.w;
                     }
             };
-            if (EXACT && j >= clean_lo && j <= clean_hi) go(std::true_type{});
+            if (j >= clean_lo && j <= clean_hi) go(std::true_type{});
             else go(std::false_type{});
         };
         auto load_v = [&](int j, int id, int buf) {
@@ -415,24 +361,62 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
 #pragma unroll
                     for (int i = 0; i < VL; ++i) {
                         const uint8_t* p = vp + tok * d + i * 128;
-                        const bool have = ALL || (seen(j + 2 * c + tok) && (EXACT || i * 128 + g * VB < d));
+                        const bool have = (ALL || seen(j + 2 * c + tok)) && (EXACT || i * 128 + g * VB < d);
                         if constexpr (VB == 16) {
-                            const uint4 v = ALL ? load16(p) : load16_if(p, have);
+                            const uint4 v = ALL && EXACT ? load16(p) : load16_if(p, have);
                             vw[buf][y][4 * i] = v.x; vw[buf][y][4 * i + 1] = v.y; vw[buf][y][4 * i + 2] = v.z; vw[buf][y][4 * i + 3] = v.w;
                         } else {
-                            const uint2 v = ALL ? load8(p) : load8_if(p, have);
+                            const uint2 v = ALL && EXACT ? load8(p) : load8_if(p, have);
                             vw[buf][y][0] = v.x; vw[buf][y][1] = v.y;
                         }
                     }
                 }
             };
-            if (EXACT && j >= clean_lo && j <= clean_hi) go(std::true_type{});
+            if (j >= clean_lo && j <= clean_hi) go(std::true_type{});
             else go(std::false_type{});
         };
 
-        int j = place, id = checked(entry_here(), place, t0 < tn);      // this chunk's place and page
+        // First the loads that wait for nothing, then those behind them: table
+        // entries and Q, then the first keys and values, while Q is converted.
+        int j = place;                          // this chunk's place
+        const int entry0 = entry_here();
         advance();
-        int j1 = place, entry = entry_here();                           // the next one's
+        int j1 = place, entry = entry_here();   // the next one's
+        // ---- Q as the B operand: lane (g, c) holds row g, the 16 values of
+        // each of its pieces (i * 4 + c), as the keys' lanes hold theirs
+        uint32_t qf[KL * 8];
+        float qscale = a.scale * 1.4426950408889634f;
+        {
+            const int rho = rt * kRows + g;
+            const bool valid = g < rows;
+            const int tok = sw.begin + rho / group;
+            const uint16_t* qp = a.q[r] + (valid ? tok * a.q_token + (h * group + rho % group) * a.q_head : 0);
+#pragma unroll
+            for (int i = 0; i < KL; ++i) {
+                const int e = (i * 4 + c) * 16;
+                uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+                if (valid && e < a.d) {
+                    v0 = *reinterpret_cast<const uint4*>(qp + e);
+                    v1 = *reinterpret_cast<const uint4*>(qp + e + 8);
+                }
+                qf[8 * i + 0] = v0.x; qf[8 * i + 1] = v0.y; qf[8 * i + 2] = v0.z; qf[8 * i + 3] = v0.w;
+                qf[8 * i + 4] = v1.x; qf[8 * i + 5] = v1.y; qf[8 * i + 6] = v1.z; qf[8 * i + 7] = v1.w;
+            }
+        }
+        // What only chunks at the ends of a row's keys need is kept out of the registers.
+        if (threadIdx.x < kRows) {
+            const int i = (rt * kRows + min(static_cast<int>(threadIdx.x), rows - 1)) / group;
+            limits.row_end[threadIdx.x] = end_of(i);
+            limits.row_from[threadIdx.x] = from_of(i);
+            if (threadIdx.x == 0) {
+                limits.end = end_max;
+                limits.from = from_min;
+                limits.sinks = sinks;
+            }
+        }
+        __syncthreads();
+
+        int id = checked(entry0, j, t0 < tn);   // this chunk's page
         float sk = 0.f, sv = 0.f;
         if (id >= 0) {
             sk = __ldg(sk_head + static_cast<long long>(id) * a.heads);
@@ -440,6 +424,28 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
             load_k(j, id, 0);
             load_v(j, id, 0);
         }
+        {
+            if constexpr (BF16) {
+                uint32_t top = 0;   // the largest magnitude's bits
+#pragma unroll
+                for (int i = 0; i < KL * 8; ++i) {
+                    const uint32_t x = qf[i] & 0x7fff7fffu;
+                    top = max(top, max(x & 0xffffu, x >> 16));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ex = static_cast<int>(top >> 7);                     // biased exponent; 255: not finite
+                const int up = (ex == 255 || ex == 0) ? 0 : min(126, 127 + 14 - ex);   // largest value to 2^14
+                const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+                for (int i = 0; i < KL * 8; ++i)
+                    qf[i] = pack_half2(__uint_as_float(qf[i] << 16) * f, __uint_as_float(qf[i] & 0xffff0000u) * f);
+                qscale *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            }
+        }
+        // row factors of the columns 2c, 2c + 1 of S^T
+        const float qs0 = __shfl_sync(0xffffffffu, qscale, 8 * c), qs1 = __shfl_sync(0xffffffffu, qscale, 8 * c + 4);
+
         for (int tb = t0; tb < tn; tb += BUF) {
 #pragma unroll
             for (int cur = 0; cur < BUF; ++cur) {
@@ -782,7 +788,11 @@ struct Launcher {
         cfg.numAttrs = pdl_launch() ? 1 : 0;
         cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<BF16, D, EXACT>, a);
         if (e != cudaSuccess) return e;
-        cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows, 1);
+        // no item spans blocks where none has more than one tile; a row tile
+        // of single tokens has only the group's rows
+        if (a.table_width * a.page <= kTile) return cudaSuccess;
+        const long long rows = std::min<long long>(kRows, static_cast<long long>(a.cu == nullptr ? 1 : a.tokens) * (a.q_heads / a.heads));
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(rows), 1);
         cfg.blockDim = dim3(kMergeGroups * D / 2, 1, 1);
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D>, a);

@@ -40,13 +40,16 @@ std::atomic<long long> g_alloc_calls{0};   // device allocations made by the lib
 // rank-split fp32 parts, the MoE routing tables, the w8A16 pre-pass weight.
 // Allocated at the first call on the stream that needs it and grown only when
 // a call needs more, so steady-state calls allocate nothing.  `last_use` is
-// recorded after every call that used it and waited on by the next one, so a
-// stream handle that is reused after cudaStreamDestroy can never overlap the
-// previous owner's kernels.
+// recorded after every call that used it and waited on by the next one; short
+// calls leave both out (an event between two kernels costs them microseconds
+// and their programmatic launch) and go by the stream's id, which, unlike its
+// handle, is never given again: a workspace found under a handle that now is
+// another stream is taken over only when the device has finished.
 struct Workspace {
     void* ptr = nullptr;
     size_t bytes = 0;
     cudaEvent_t last_use = nullptr;
+    unsigned long long stream_id = 0;
 };
 
 struct DeviceState {
@@ -304,10 +307,11 @@ coc_status_t device_pool(DeviceState* ds, cudaMemPool_t* out);
 struct Scratch {
     void* ptr = nullptr;
     bool captured = false;
+    bool by_stream = false;     // ordered by the stream alone: no event
     Workspace* w = nullptr;
 };
 constexpr size_t kWorkspaceCap = size_t(4) << 30;   // largest scratch one call may take
-coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out);
+coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out, bool by_stream = false);
 coc_status_t scratch_release(cudaStream_t stream, Scratch& sc, coc_status_t st);
 
 // Rank split (AllReduce, ReduceScatter, single-CTA tiles: m <= 128): with at
@@ -719,8 +723,9 @@ coc_status_t device_pool(DeviceState* ds, cudaMemPool_t* out) {
     return COC_OK;
 }
 
-coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out) {
+coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out, bool by_stream) {
     *out = Scratch{};
+    out->by_stream = by_stream;
     if (bytes == 0) return COC_OK;
     if (bytes > kWorkspaceCap)
         return fail(COC_ERR_SHAPE, "the call needs %zu bytes of scratch, above the %zu-byte cap", bytes, kWorkspaceCap);
@@ -744,10 +749,15 @@ coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes,
         w.last_use = nullptr;
         return cuda_fail(e, "cudaEventCreateWithFlags (workspace)");
     }
+    unsigned long long id = 0;
+    if ((e = cudaStreamGetId(stream, &id)) != cudaSuccess) return cuda_fail(e, "cudaStreamGetId (workspace)");
+    if (w.ptr != nullptr && w.stream_id != id && (e = cudaDeviceSynchronize()) != cudaSuccess)
+        return cuda_fail(e, "cudaDeviceSynchronize (workspace of a stream that is gone)");
+    w.stream_id = id;
     if (w.bytes < bytes) {
         // grow: the previous buffer is freed once every kernel that used it is done
         if (w.ptr != nullptr) {
-            if ((e = cudaEventSynchronize(w.last_use)) != cudaSuccess) return cuda_fail(e, "cudaEventSynchronize (workspace)");
+            if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize (workspace)");
             if ((e = cudaFree(w.ptr)) != cudaSuccess) return cuda_fail(e, "cudaFree (workspace)");
             w.ptr = nullptr;
             w.bytes = 0;
@@ -762,7 +772,7 @@ coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes,
     }
     // after the previous user of this workspace (this stream, or a destroyed
     // stream whose handle this one reuses)
-    if ((e = cudaStreamWaitEvent(stream, w.last_use, 0)) != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent (workspace)");
+    if (!by_stream && (e = cudaStreamWaitEvent(stream, w.last_use, 0)) != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent (workspace)");
     out->ptr = w.ptr;
     out->w = &w;
     return COC_OK;
@@ -771,7 +781,7 @@ coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes,
 coc_status_t scratch_release(cudaStream_t stream, Scratch& sc, coc_status_t st) {
     cudaError_t e = cudaSuccess;
     if (sc.captured && sc.ptr != nullptr) e = cudaFreeAsync(sc.ptr, stream);
-    else if (sc.w != nullptr) e = cudaEventRecord(sc.w->last_use, stream);
+    else if (sc.w != nullptr && !sc.by_stream) e = cudaEventRecord(sc.w->last_use, stream);
     sc = Scratch{};
     if (st == COC_OK && e != cudaSuccess) st = cuda_fail(e, "releasing the call's scratch");
     return st;
@@ -1676,7 +1686,7 @@ COC_API coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t
     cudaError_t e = kv_attention_plan(a, dt == COC_BF16, ds->sm_count, &grid, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "KV attention plan");
     Scratch sc;
-    if ((st = scratch_acquire(ds, str, bytes, &sc)) != COC_OK) return st;
+    if ((st = scratch_acquire(ds, str, bytes, &sc, true)) != COC_OK) return st;
     a.scratch = sc.ptr;
     if ((e = launch_kv_attention(a, dt == COC_BF16, grid, str)) != cudaSuccess) st = cuda_fail(e, "KV attention launch");
     return scratch_release(str, sc, st);
@@ -1828,9 +1838,9 @@ COC_API coc_status_t coc_shutdown(void) {
     coc_status_t st = COC_OK;
     for (auto& kv : g_dev) {
         if (!kv.second.ws.empty() && cudaSetDevice(kv.first) == cudaSuccess) {
+            cudaDeviceSynchronize();    // the workspaces' last users are done
             for (auto& w : kv.second.ws) {
                 if (w.second.last_use != nullptr) {
-                    cudaEventSynchronize(w.second.last_use);
                     cudaEventDestroy(w.second.last_use);
                 }
                 if (w.second.ptr != nullptr && cudaFree(w.second.ptr) != cudaSuccess)

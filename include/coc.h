@@ -76,7 +76,8 @@
  *     small status buffer (a few words).  Calls that need scratch (the fp32
  *     parts of a rank-split AllReduce / ReduceScatter, the MoE routing
  *     tables, the w8A16 pre-pass's dequantised weight, the stacked X of an
- *     AllGather that keeps no gathered copy) take it from a
+ *     AllGather that keeps no gathered copy, the parts of cached attention's
+ *     split items) take it from a
  *     workspace the library keeps per stream: allocated by the first such
  *     call on the stream and grown only when a later call needs more (the
  *     growing call waits for the earlier users of the old buffer first), so

@@ -552,3 +552,74 @@ def test_binding_refusals(monkeypatch, native):
     bad(TypeError, f, xs, ws, sc, 32, zeros=[torch.zeros(2, 16, dtype=torch.int32, device=DEV)])
     bad(coc.CocError, f, xs, [torch.zeros(8, 20, dtype=torch.int32, device=DEV)], [torch.zeros(2, 20, dtype=BF, device=DEV)], 32)   # n % 8
     coc.sync_status()
+
+
+def guarded(shape, dt):
+    """(outputs inside a larger buffer, check that nothing around them changed)."""
+    n = 1
+    for x in shape:
+        n *= x
+    buf = torch.full((n + 512,), 7.0, dtype=dt, device=DEV)
+
+    def intact():
+        return bool((buf[:256] == 7).all() and (buf[256 + n:] == 7).all())
+    return buf[256:256 + n].view(shape), intact
+
+
+@pytest.mark.parametrize("hq,hkv,d,news,lens", [(5, 1, 80, [3, 1], [90, 7]), (4, 4, 64, [1, 2], [1, 300]), (9, 3, 256, [1], [40])])
+def test_nothing_is_written_around_the_outputs(hq, hkv, d, news, lens):
+    page = 32
+    table, rk, rv, qs = build(1, hq, hkv, d, page, news, lens, BF, seed=31)
+    cache = to_cache(rk, rv)
+    out, intact = guarded((sum(news), hq, d), BF)
+    attend(cache, table, lens, kv.offsets(news), qs, outs=[out])
+    coc.sync_status()
+    assert intact()
+    out, intact = guarded((sum(news), hq, d), BF)
+    k = [torch.randn(sum(news), hkv, d, device=DEV).to(BF)]
+    cos = torch.ones(max(lens), d // 2, device=DEV)
+    coc.kv_cache_append(k, k, cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), cos, cos,
+                        qs=[q.to(DEV) for q in qs], q_outs=[out], cu_new=torch.tensor(kv.offsets(news), dtype=torch.int32, device=DEV))
+    coc.sync_status()
+    assert intact()
+
+
+def test_steady_state_attention_allocates_nothing_and_shutdown_recovers():
+    """Repeated calls take their scratch from the stream's workspace, also after it was freed or grew."""
+    table, rk, rv, qs = build(1, 8, 1, 128, 64, [1], [5000], BF, seed=12)
+    cache, tb = to_cache(rk, rv), table.to(DEV)
+    ln = torch.tensor([5000], dtype=torch.int32, device=DEV)
+    q = [x.to(DEV) for x in qs]
+    want = coc.kv_cache_attention(q, cache, tb, ln)[0].clone()
+    torch.cuda.synchronize()
+    n = coc.alloc_count()
+    for _ in range(5):
+        assert torch.equal(coc.kv_cache_attention(q, cache, tb, ln)[0], want)
+    assert coc.alloc_count() == n
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [coc.kv_cache_attention(q, cache, tb, ln)[0] for _ in range(3)]
+    side.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    coc.shutdown()
+    assert torch.equal(coc.kv_cache_attention(q, cache, tb, ln)[0], want)
+    coc.sync_status()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_attention_of_equal_keys_and_of_one_that_dominates(dt):
+    """All logits equal: the mean of the values.  One logit far above: its value."""
+    g = torch.Generator().manual_seed(14)
+    page, d, n = 16, 64, 1000
+    table, pages = kv.make_table([n], page, gen=g)
+    rv = kv.random_cache(1, pages, 1, page, d, g)
+    zero = [(torch.zeros(pages, 1, page, d, dtype=torch.uint8), torch.ones(pages, 1))]
+    q = [torch.randn(1, 2, d, generator=g).to(dt)]
+    outs = attend(to_cache(zero, rv), table, [n], None, q)
+    check(outs, q, zero, rv, table, [n], [0, 1], page)
+    one = [(zero[0][0].clone(), zero[0][1])]
+    one[0][0][table[0, 30].item(), 0, 5] = 0x78          # 256 in every value of one key
+    q = [torch.ones(1, 2, d).to(dt)]
+    outs = attend(to_cache(one, rv), table, [n], None, q)
+    v = kv.gather(kv.values(*rv[0]), table[0], n, page)[0, 30 * page + 5]
+    assert torch.equal(outs[0].cpu()[0], v.to(dt).expand(2, d))

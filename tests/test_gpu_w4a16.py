@@ -141,3 +141,12 @@ def test_w4_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[1], (want.float() * 2).to(BF))
+
+
+@pytest.mark.parametrize("m,n,ks", [(1, 8, 32), (9, 72, 128), (5, 200, 96)])
+def test_w4_nothing_is_written_around_the_outputs(m, n, ks):
+    xs, codes, scales, zs = make(1, m, n, ks, 32, True, BF, 8)
+    buf = torch.full((m * n + 512,), 7.0, dtype=BF, device=DEV)
+    run(xs, codes, scales, zs, 32, outs=[buf[256:256 + m * n].view(m, n)])
+    coc.sync_status()
+    assert (buf[:256] == 7).all() and (buf[256 + m * n:] == 7).all()

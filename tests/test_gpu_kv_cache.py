@@ -623,3 +623,20 @@ def test_attention_of_equal_keys_and_of_one_that_dominates(dt):
     outs = attend(to_cache(one, rv), table, [n], None, q)
     v = kv.gather(kv.values(*rv[0]), table[0], n, page)[0, 30 * page + 5]
     assert torch.equal(outs[0].cpu()[0], v.to(dt).expand(2, d))
+
+
+def test_outputs_of_several_ranks_are_ordinary_tensors():
+    """New outputs share one allocation: aligned, packed, usable and independent like separate tensors."""
+    table, rk, rv, qs = build(3, 4, 2, 80, 32, [1], [40], BF, seed=33)
+    outs = attend(to_cache(rk, rv), table, [40], None, qs)
+    for o in outs:
+        assert o.shape == (1, 4, 80) and o.is_contiguous() and o.data_ptr() % 16 == 0 and not o.requires_grad
+    keep = [o.clone() for o in outs]
+    outs[1].fill_(3)
+    assert torch.equal(outs[0], keep[0]) and torch.equal(outs[2], keep[2]) and (outs[1] == 3).all()
+    w = torch.ones(80, device=DEV, dtype=BF, requires_grad=True)
+    (outs[2] * w).sum().backward()
+    assert w.grad.shape == (80,)
+    outs[0].zero_()
+    view = outs[0].view(4, 80)[1:]
+    assert view.shape == (3, 80) and not view.any()

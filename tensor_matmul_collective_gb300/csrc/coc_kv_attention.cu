@@ -1,7 +1,7 @@
 // Attention over the paged 8-bit key/value cache.
 //
 // Mathematics.  A row is one query head of one new token; the rows of a
-// (sequence, key head) are packed token by token, 8 to a tile.  With a code c
+// (sequence, key head) are packed token by token, 8 or 16 to a tile.  With a code c
 // of a page whose scale is s, k = c s_k and v = c s_v, so with z = scale q.k
 // in log2 units
 //     out = sum_j 2^z_j s_vj c_j / sum_j 2^z_j.
@@ -11,7 +11,7 @@
 // range of a 16-bit type whatever the scales are.  The denominator adds w / s_v.
 //
 // What bounds it.  2 d bytes of codes per key and key head are read once for
-// up to 8 rows: 16 to 32 operations a byte, far below the tensor cores' rate,
+// up to 8 or 16 rows: 16 to 32 operations a byte, far below the tensor cores' rate,
 // so it is the cache's bandwidth.  What the SMs must not do is spend many
 // instructions per byte.  Codes go from e4m3 to fp16 in pairs (exact), as the
 // operand of mma.sync: S^T = K Q^T with the keys in the 16 rows of the tile
@@ -35,7 +35,9 @@
 // unnormalised parts, which a second kernel adds in order.
 //
 // Measured: 48 sequences of 1 to 8192 keys, 8 ranks of one key head with 8
-// query heads of 128: 79 us, 5.0 TB/s; two of 131071: 95 us, 5.6 TB/s.
+// query heads of 128: 75 us, 5.2 TB/s; two of 131071: 95 us, 5.6 TB/s.  With 16
+// query heads (16 rows a tile) 48 sequences of 4096 keys take 92 us, 4.4 TB/s:
+// the conversions and products of a byte, at two blocks an SM.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -49,7 +51,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kSub = 16;                   // keys of one matrix product
 constexpr int kTile = kWarps * kSub;       // keys of one block's step
-constexpr int kRows = 8;                   // query rows of a tile
 constexpr float kNoMax = -1.0e38f;         // running maximum before any key
 // What beginning and ending an item costs, in tiles: an item counts as so many
 // units more than it has tiles.
@@ -63,10 +64,10 @@ constexpr float kSlack = 6.f;
 // Shared memory: the warps' sums, joined at the end of an item.
 template <int D>
 constexpr int merge_stride() { return D + 4; }
-template <int D>
-constexpr int attn_smem() { return kWarps * kRows * merge_stride<D>() * 4; }
+template <int D, int ROWS>
+constexpr int attn_smem() { return kWarps * ROWS * merge_stride<D>() * 4; }
 
-// Scratch: per block two parts (kRows x D sums, then kRows maxima and sums),
+// Scratch: per block two parts (ROWS x D sums, then ROWS maxima and sums),
 // and a record of the item that the block begins and does not end.
 struct Record {
     int open;        // 1: there is one
@@ -74,8 +75,8 @@ struct Record {
     int last_block;
     int pad[3];
 };
-template <int D>
-constexpr long long part_floats() { return kRows * (D + 2); }
+template <int D, int ROWS>
+constexpr long long part_floats() { return ROWS * (D + 2); }
 
 // Codes are read once by one lane: no place in L1.
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
@@ -153,6 +154,7 @@ struct SeqWork {
     int begin, n, len;      // first new token, how many, tokens in the cache
     int row_tiles, tiles;
 };
+template <int ROWS>
 __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int s) {
     SeqWork w;
     int end;
@@ -162,13 +164,13 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int s) {
     const long long room = a.table_width * a.page;
     if (w.len > room && w.n > 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
     const int group = a.q_heads / a.heads;
-    w.row_tiles = static_cast<int>((static_cast<long long>(w.n) * group + kRows - 1) / kRows);
+    w.row_tiles = static_cast<int>((static_cast<long long>(w.n) * group + ROWS - 1) / ROWS);
     // positions past the table are left out, by the pages' lookup too
     const int keys = static_cast<int>(min(static_cast<long long>(w.len), room));
     const int full = (keys + kTile - 1) / kTile;
     w.tiles = full;
     if (a.window > 0) {
-        const long long span = static_cast<long long>(a.window) + (kRows - 1) / group + 1;   // keys of a row tile's window
+        const long long span = static_cast<long long>(a.window) + (ROWS - 1) / group + 1;   // keys of a row tile's window
         const long long most = (static_cast<long long>(a.sinks) + kTile - 1) / kTile + (span + kTile - 2) / kTile + 1;
         if (most < full) w.tiles = static_cast<int>(most);
     }
@@ -176,22 +178,29 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int s) {
     return w;
 }
 
+template <int ROWS>
 __device__ __forceinline__ long long seq_units(const KvAttnArgs& a, int s) {
-    const SeqWork w = seq_work(a, s);
+    const SeqWork w = seq_work<ROWS>(a, s);
     return static_cast<long long>(w.row_tiles) * (w.tiles + kItemCost);
 }
 
 // The keys that the rows of a tile see: row x those from row_from[x] (and the
 // sinks) up to row_end[x]; end and from are the last and the first of these.
+template <int ROWS>
 struct Limits {
     int end, from, sinks;
-    int row_end[kRows], row_from[kRows];
+    int row_end[ROWS], row_from[ROWS];
 };
+
+// Resident blocks: what the registers allow.
+template <int D, int ROWS>
+constexpr int blocks_per_sm() { return D == 256 || (D == 128 && ROWS == 16) ? 2 : 3; }
 
 // EXACT: the head has D values (every offset inside a chunk is a constant);
 // otherwise fewer, and the pieces past them are zero.
-template <bool BF16, int D, bool EXACT>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+template <bool BF16, int D, bool EXACT, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_attention_kernel(const __grid_constant__ KvAttnArgs a) {
+    constexpr int NT = ROWS / 8;            // row tiles that a chunk's operands serve
     constexpr int BUF = D == 256 ? 1 : 2;   // chunks held: the next one is loaded while this one is worked on
     constexpr int KL = D / 64;              // 16-byte pieces of a key per lane
     constexpr int VB = D >= 128 ? 16 : 8;   // bytes of a value row in one piece
@@ -200,8 +209,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan[kWarps];
     __shared__ long long found[3];
-    __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
-    __shared__ Limits limits;
+    __shared__ float wm[kWarps][ROWS], wl[kWarps][ROWS];
+    __shared__ Limits<ROWS> limits;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int group = a.q_heads / a.heads;
@@ -216,7 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
     const int per = (a.seqs + kWarps * 32 - 1) / (kWarps * 32);
     const int s_lo = min(a.seqs, static_cast<int>(threadIdx.x) * per), s_hi = min(a.seqs, s_lo + per);
     long long mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += seq_units(a, s);
+    for (int s = s_lo; s < s_hi; ++s) mine += seq_units<ROWS>(a, s);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
     if (before <= u0 && u0 < before + mine * RH) {
         long long at = before;
         for (int s = s_lo; s < s_hi; ++s) {
-            const long long n = seq_units(a, s) * RH;
+            const long long n = seq_units<ROWS>(a, s) * RH;
             if (u0 < at + n) {
                 found[0] = s;
                 found[1] = at;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
     __syncthreads();
     int s = static_cast<int>(found[0]);
     long long base = found[1];      // first unit of sequence s
-    SeqWork sw = seq_work(a, s);
+    SeqWork sw = seq_work<ROWS>(a, s);
     bool left_open = false;
 
     const int d = EXACT ? D : a.d;
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
         const int span = sw.tiles + kItemCost;
         if (u >= base + static_cast<long long>(sw.row_tiles) * span * RH) {
             base += static_cast<long long>(sw.row_tiles) * span * RH;
-            sw = seq_work(a, ++s);
+            sw = seq_work<ROWS>(a, ++s);
             continue;
         }
         // item (rank and head, row tile), tiles [t0, t1) of it; the units
@@ -282,8 +291,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
         const int r = rh / a.heads, h = rh - r * a.heads;
 
         // ---- rows and their limits
-        const int rows = static_cast<int>(min(static_cast<long long>(kRows), static_cast<long long>(sw.n) * group - rt * kRows));
-        const int i0 = rt * kRows / group, i1 = (rt * kRows + rows - 1) / group;
+        const int rows = static_cast<int>(min(static_cast<long long>(ROWS), static_cast<long long>(sw.n) * group - rt * ROWS));
+        const int i0 = rt * ROWS / group, i1 = (rt * ROWS + rows - 1) / group;
         const int shift = sw.len - sw.n + 1;        // token i's keys end at shift + i
         const int room = static_cast<int>(min(static_cast<long long>(0x7fffffff), a.table_width << page_shift));
         auto end_of = [&](int i) { return max(0, min(room, shift + i)); };
@@ -295,13 +304,18 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
         const int near = min(far, (min(sinks, end_max) + kTile - 1) / kTile);   // sink tiles ahead of the window's
         const int tiles = near + max(0, (end_max + kTile - 1) / kTile - far);
 
-        float acc[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        float acc[NT][MT][4];
         // the columns' references, as what is added to log2 of a weight: kOffset - maximum
-        float b0 = kOffset - kNoMax, b1 = b0, l0 = 0.f, l1 = 0.f;
+        float b0[NT], b1[NT], l0[NT], l1[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
+            b0[n] = b1[n] = kOffset - kNoMax;
+            l0[n] = l1[n] = 0.f;
+        }
 
-        const volatile Limits& lim = limits;
+        const volatile Limits<ROWS>& lim = limits;
         // ---- the chunks of this warp: 16 keys j .. j + 15 of every tile
         const int tn = min(t1, tiles);
         // a chunk between these is seen whole by every row
@@ -384,11 +398,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
         int j1 = place, entry = entry_here();   // the next one's
         // ---- Q as the B operand: lane (g, c) holds row g, the 16 values of
         // each of its pieces (i * 4 + c), as the keys' lanes hold theirs
-        uint32_t qf[KL * 8];
-        float qscale = a.scale * 1.4426950408889634f;
-        {
-            const int rho = rt * kRows + g;
-            const bool valid = g < rows;
+        uint32_t qf[NT][KL * 8];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int rho = rt * ROWS + 8 * n + g;
+            const bool valid = 8 * n + g < rows;
             const int tok = sw.begin + rho / group;
             const uint16_t* qp = a.q[r] + (valid ? tok * a.q_token + (h * group + rho % group) * a.q_head : 0);
 #pragma unroll
@@ -399,13 +413,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                     v0 = *reinterpret_cast<const uint4*>(qp + e);
                     v1 = *reinterpret_cast<const uint4*>(qp + e + 8);
                 }
-                qf[8 * i + 0] = v0.x; qf[8 * i + 1] = v0.y; qf[8 * i + 2] = v0.z; qf[8 * i + 3] = v0.w;
-                qf[8 * i + 4] = v1.x; qf[8 * i + 5] = v1.y; qf[8 * i + 6] = v1.z; qf[8 * i + 7] = v1.w;
+                qf[n][8 * i + 0] = v0.x; qf[n][8 * i + 1] = v0.y; qf[n][8 * i + 2] = v0.z; qf[n][8 * i + 3] = v0.w;
+                qf[n][8 * i + 4] = v1.x; qf[n][8 * i + 5] = v1.y; qf[n][8 * i + 6] = v1.z; qf[n][8 * i + 7] = v1.w;
             }
         }
         // What only chunks at the ends of a row's keys need is kept out of the registers.
-        if (threadIdx.x < kRows) {
-            const int i = (rt * kRows + min(static_cast<int>(threadIdx.x), rows - 1)) / group;
+        if (threadIdx.x < ROWS) {
+            const int i = (rt * ROWS + min(static_cast<int>(threadIdx.x), rows - 1)) / group;
             limits.row_end[threadIdx.x] = end_of(i);
             limits.row_from[threadIdx.x] = from_of(i);
             if (threadIdx.x == 0) {
@@ -424,12 +438,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
             load_k(j, id, 0);
             load_v(j, id, 0);
         }
-        {
+        float qs0[NT], qs1[NT];     // row factors of the columns 2c, 2c + 1 of S^T
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float qscale = a.scale * 1.4426950408889634f;
             if constexpr (BF16) {
                 uint32_t top = 0;   // the largest magnitude's bits
 #pragma unroll
                 for (int i = 0; i < KL * 8; ++i) {
-                    const uint32_t x = qf[i] & 0x7fff7fffu;
+                    const uint32_t x = qf[n][i] & 0x7fff7fffu;
                     top = max(top, max(x & 0xffffu, x >> 16));
                 }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -439,12 +456,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                 const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 #pragma unroll
                 for (int i = 0; i < KL * 8; ++i)
-                    qf[i] = pack_half2(__uint_as_float(qf[i] << 16) * f, __uint_as_float(qf[i] & 0xffff0000u) * f);
+                    qf[n][i] = pack_half2(__uint_as_float(qf[n][i] << 16) * f, __uint_as_float(qf[n][i] & 0xffff0000u) * f);
                 qscale *= __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
             }
+            qs0[n] = __shfl_sync(0xffffffffu, qscale, 8 * c);
+            qs1[n] = __shfl_sync(0xffffffffu, qscale, 8 * c + 4);
         }
-        // row factors of the columns 2c, 2c + 1 of S^T
-        const float qs0 = __shfl_sync(0xffffffffu, qscale, 8 * c), qs1 = __shfl_sync(0xffffffffu, qscale, 8 * c + 4);
 
         for (int tb = t0; tb < tn; tb += BUF) {
 #pragma unroll
@@ -474,79 +491,91 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                     }
                     continue;
                 }
-                // S^T = K Q^T, in two accumulators: products into one wait for each other
-                float sc[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+                // S^T = K Q^T; one row tile in two accumulators: products into one wait for each other
+                float sc[NT][4], sb[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) sc[n][x] = sb[n][x] = 0.f;
 #pragma unroll
                 for (int w = 0; w < KL * 4; ++w) {
                     const uint32_t af[4] = {lo2(kw[cur][0][w]), lo2(kw[cur][1][w]), hi2(kw[cur][0][w]), hi2(kw[cur][1][w])};
-                    mma16816(w & 1 ? sb : sc, af, qf[2 * w], qf[2 * w + 1]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816(NT == 1 && (w & 1) ? sb[n] : sc[n], af, qf[n][2 * w], qf[n][2 * w + 1]);
                 }
                 if (BUF == 1 && id >= 0) load_k(j, id, nxt);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) sc[x] += sb[x];
                 const float ev = log2_fast(fmaxf(sv0, 1.2e-38f));
-                const float f0 = qs0 * sk0, f1 = qs1 * sk0;
-                const bool clean = j0 >= clean_lo && j0 <= clean_hi;
-                uint32_t see = 0xf;     // bit x: the row of sc[x] sees its key
-                if (!clean) {
-                    see = 0;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int key = j0 + g + 8 * (x >> 1), row = 2 * c + (x & 1);
-                        see |= static_cast<uint32_t>(key < lim.row_end[row] && (key >= lim.row_from[row] || key < lim.sinks)) << x;
-                    }
-                }
-                float z[4];             // log2 of the weights
-                auto logs = [&](float e0, float e1) {
-                    z[0] = fmaf(sc[0], f0, e0);
-                    z[1] = fmaf(sc[1], f1, e1);
-                    z[2] = fmaf(sc[2], f0, e0);
-                    z[3] = fmaf(sc[3], f1, e1);
-                    if (!clean) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (!(see >> x & 1)) z[x] = -INFINITY;
-                    }
-                };
-                logs(ev + b0, ev + b1);
-                // a reference moves only when a key is well above it
-                if (__any_sync(0xffffffffu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > kOffset + kSlack)) {
-                    logs(ev, ev);
-                    float n0 = fmaxf(kOffset - b0, fmaxf(z[0], z[2])), n1 = fmaxf(kOffset - b1, fmaxf(z[1], z[3]));
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
-                        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
-                    }
-                    n0 = kOffset - n0;
-                    n1 = kOffset - n1;
-                    const float c0 = exp2_fast(n0 - b0), c1 = exp2_fast(n1 - b1);
-                    b0 = n0;
-                    b1 = n1;
-                    l0 *= c0;
-                    l1 *= c1;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        acc[i][0] *= c0;
-                        acc[i][1] *= c1;
-                        acc[i][2] *= c0;
-                        acc[i][3] *= c1;
-                    }
-                    logs(ev + b0, ev + b1);
-                }
-#pragma unroll
-                for (int x = 0; x < 4; ++x) z[x] = exp2_fast(z[x]);
                 const float inv = exp2_fast(-ev);
-                l0 = fmaf(z[0] + z[2], inv, l0);
-                l1 = fmaf(z[1] + z[3], inv, l1);
-                const uint32_t plo = pack_half2(z[0], z[1]), phi = pack_half2(z[2], z[3]);
-                const uint32_t p0 = transposed(plo), p1 = transposed(phi);
-                uint32_t e0 = 0, e1 = 0;
-                if constexpr (!BF16) {
-                    const float2 rl = __half22float2(*reinterpret_cast<const __half2*>(&plo));
-                    const float2 rh2 = __half22float2(*reinterpret_cast<const __half2*>(&phi));
-                    e0 = transposed(pack_half2(z[0] - rl.x, z[1] - rl.y));
-                    e1 = transposed(pack_half2(z[2] - rh2.x, z[3] - rh2.y));
+                const bool clean = j0 >= clean_lo && j0 <= clean_hi;
+                uint32_t see[NT];                       // bit x: the row of sc[x] sees its key
+                uint32_t p0[NT], p1[NT], e0[NT], e1[NT];    // weights, and what their rounding left
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (NT == 1) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) sc[n][x] += sb[n][x];
+                    }
+                    const float f0 = qs0[n] * sk0, f1 = qs1[n] * sk0;
+                    see[n] = 0xf;
+                    if (!clean) {
+                        see[n] = 0;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int key = j0 + g + 8 * (x >> 1), row = 8 * n + 2 * c + (x & 1);
+                            see[n] |= static_cast<uint32_t>(key < lim.row_end[row] && (key >= lim.row_from[row] || key < lim.sinks)) << x;
+                        }
+                    }
+                    float z[4];             // log2 of the weights
+                    auto logs = [&](float a0, float a1) {
+                        z[0] = fmaf(sc[n][0], f0, a0);
+                        z[1] = fmaf(sc[n][1], f1, a1);
+                        z[2] = fmaf(sc[n][2], f0, a0);
+                        z[3] = fmaf(sc[n][3], f1, a1);
+                        if (!clean) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (!(see[n] >> x & 1)) z[x] = -INFINITY;
+                        }
+                    };
+                    logs(ev + b0[n], ev + b1[n]);
+                    // a reference moves only when a key is well above it
+                    if (__any_sync(0xffffffffu, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > kOffset + kSlack)) {
+                        logs(ev, ev);
+                        float n0 = fmaxf(kOffset - b0[n], fmaxf(z[0], z[2])), n1 = fmaxf(kOffset - b1[n], fmaxf(z[1], z[3]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) {
+                            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+                            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+                        }
+                        n0 = kOffset - n0;
+                        n1 = kOffset - n1;
+                        const float c0 = exp2_fast(n0 - b0[n]), c1 = exp2_fast(n1 - b1[n]);
+                        b0[n] = n0;
+                        b1[n] = n1;
+                        l0[n] *= c0;
+                        l1[n] *= c1;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            acc[n][i][0] *= c0;
+                            acc[n][i][1] *= c1;
+                            acc[n][i][2] *= c0;
+                            acc[n][i][3] *= c1;
+                        }
+                        logs(ev + b0[n], ev + b1[n]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) z[x] = exp2_fast(z[x]);
+                    l0[n] = fmaf(z[0] + z[2], inv, l0[n]);
+                    l1[n] = fmaf(z[1] + z[3], inv, l1[n]);
+                    const uint32_t plo = pack_half2(z[0], z[1]), phi = pack_half2(z[2], z[3]);
+                    p0[n] = transposed(plo);
+                    p1[n] = transposed(phi);
+                    if constexpr (!BF16) {
+                        const float2 rl = __half22float2(*reinterpret_cast<const __half2*>(&plo));
+                        const float2 rh2 = __half22float2(*reinterpret_cast<const __half2*>(&phi));
+                        e0[n] = transposed(pack_half2(z[0] - rl.x, z[1] - rl.y));
+                        e1[n] = transposed(pack_half2(z[2] - rh2.x, z[3] - rh2.y));
+                    }
                 }
                 // O^T += V^T P^T
                 if (!clean) {
@@ -558,8 +587,12 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
 #pragma unroll
                         for (int i = 0; i < VL * VB / 4; ++i) nan |= ((vw[cur][y][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                     if (__any_sync(0xffffffffu, nan != 0)) {
-                        const uint32_t i0b = transposed(pack_half2(see & 1 ? 1.f : 0.f, see & 2 ? 1.f : 0.f));
-                        const uint32_t i1b = transposed(pack_half2(see & 4 ? 1.f : 0.f, see & 8 ? 1.f : 0.f));
+                        uint32_t i0b[NT], i1b[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            i0b[n] = transposed(pack_half2(see[n] & 1 ? 1.f : 0.f, see[n] & 2 ? 1.f : 0.f));
+                            i1b[n] = transposed(pack_half2(see[n] & 4 ? 1.f : 0.f, see[n] & 8 ? 1.f : 0.f));
+                        }
 #pragma unroll
                         for (int i = 0; i < MT / 2; ++i) {
                             uint32_t x[4];
@@ -572,13 +605,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                             const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[2], x[3], 0x5140);
                             const uint32_t b01 = __byte_perm(x[0], x[1], 0x7362), b23 = __byte_perm(x[2], x[3], 0x7362);
                             const uint32_t fa[4] = {lo2(a01), hi2(a01), lo2(a23), hi2(a23)}, fb[4] = {lo2(b01), hi2(b01), lo2(b23), hi2(b23)};
-                            float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb2[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(ta, fa, i0b, i1b);
-                            mma16816(tb2, fb, i0b, i1b);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (ta[q] > 0.f) acc[2 * i][q] = __uint_as_float(0x7fc00000u);
-                                if (tb2[q] > 0.f) acc[2 * i + 1][q] = __uint_as_float(0x7fc00000u);
+                            for (int n = 0; n < NT; ++n) {
+                                float ta[4] = {0.f, 0.f, 0.f, 0.f}, tb2[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma16816(ta, fa, i0b[n], i1b[n]);
+                                mma16816(tb2, fb, i0b[n], i1b[n]);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    if (ta[q] > 0.f) acc[n][2 * i][q] = __uint_as_float(0x7fc00000u);
+                                    if (tb2[q] > 0.f) acc[n][2 * i + 1][q] = __uint_as_float(0x7fc00000u);
+                                }
                             }
                         }
                     }
@@ -589,55 +625,64 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                     const uint32_t a01 = __byte_perm(vw[cur][0][i], vw[cur][1][i], 0x5140), a23 = __byte_perm(vw[cur][2][i], vw[cur][3][i], 0x5140);
                     const uint32_t b01 = __byte_perm(vw[cur][0][i], vw[cur][1][i], 0x7362), b23 = __byte_perm(vw[cur][2][i], vw[cur][3][i], 0x7362);
                     const uint32_t fa[4] = {lo2(a01), hi2(a01), lo2(a23), hi2(a23)}, fb[4] = {lo2(b01), hi2(b01), lo2(b23), hi2(b23)};
-                    mma16816(acc[2 * i], fa, p0, p1);
-                    mma16816(acc[2 * i + 1], fb, p0, p1);
-                    if constexpr (!BF16) {
-                        mma16816(acc[2 * i], fa, e0, e1);
-                        mma16816(acc[2 * i + 1], fb, e0, e1);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(acc[n][2 * i], fa, p0[n], p1[n]);
+                        mma16816(acc[n][2 * i + 1], fb, p0[n], p1[n]);
+                        if constexpr (!BF16) {
+                            mma16816(acc[n][2 * i], fa, e0[n], e1[n]);
+                            mma16816(acc[n][2 * i + 1], fb, e0[n], e1[n]);
+                        }
                     }
                 }
                 if (BUF == 1 && id >= 0) load_v(j, id, nxt);
             }
         }
-        const float m0 = kOffset - b0, m1 = kOffset - b1;
 
         // ---- join the warps: maxima and sums, then the value sums in the
         // accumulators' order (value d = g VB + 2 i + b at 16 i + 2 g + b)
+        constexpr int MS = merge_stride<D>();
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-        }
-        if (g == 0) {
-            wm[warp][2 * c] = m0;
-            wm[warp][2 * c + 1] = m1;
-            wl[warp][2 * c] = l0;
-            wl[warp][2 * c + 1] = l1;
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l0[n] += __shfl_xor_sync(0xffffffffu, l0[n], o);
+                l1[n] += __shfl_xor_sync(0xffffffffu, l1[n], o);
+            }
+            if (g == 0) {
+                wm[warp][8 * n + 2 * c] = kOffset - b0[n];
+                wm[warp][8 * n + 2 * c + 1] = kOffset - b1[n];
+                wl[warp][8 * n + 2 * c] = l0[n];
+                wl[warp][8 * n + 2 * c + 1] = l1[n];
+            }
         }
         __syncthreads();
-        float M0 = wm[0][2 * c], M1 = wm[0][2 * c + 1];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) {
-            M0 = fmaxf(M0, wm[i][2 * c]);
-            M1 = fmaxf(M1, wm[i][2 * c + 1]);
-        }
-        const float k0 = exp2_fast(m0 - M0), k1 = exp2_fast(m1 - M1);
-        constexpr int MS = merge_stride<D>();
-        float* mine_s = reinterpret_cast<float*>(smem) + warp * kRows * MS;
+        for (int n = 0; n < NT; ++n) {
+            const int x0 = 8 * n + 2 * c, x1 = x0 + 1;
+            float M0 = wm[0][x0], M1 = wm[0][x1];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            *reinterpret_cast<float2*>(mine_s + 2 * c * MS + 16 * i + 2 * g) = make_float2(acc[i][0] * k0, acc[i][2] * k0);
-            *reinterpret_cast<float2*>(mine_s + (2 * c + 1) * MS + 16 * i + 2 * g) = make_float2(acc[i][1] * k1, acc[i][3] * k1);
+            for (int i = 1; i < kWarps; ++i) {
+                M0 = fmaxf(M0, wm[i][x0]);
+                M1 = fmaxf(M1, wm[i][x1]);
+            }
+            const float k0 = exp2_fast(kOffset - b0[n] - M0), k1 = exp2_fast(kOffset - b1[n] - M1);
+            float* mine_s = reinterpret_cast<float*>(smem) + warp * ROWS * MS;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                *reinterpret_cast<float2*>(mine_s + x0 * MS + 16 * i + 2 * g) = make_float2(acc[n][i][0] * k0, acc[n][i][2] * k0);
+                *reinterpret_cast<float2*>(mine_s + x1 * MS + 16 * i + 2 * g) = make_float2(acc[n][i][1] * k1, acc[n][i][3] * k1);
+            }
         }
         __syncthreads();
         const bool begins = t0 == 0, ends = t1 == sw.tiles;
-        float* part = parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * part_floats<D>();
-        for (int x = threadIdx.x; x < kRows * D / 2; x += kWarps * 32) {
+        float* part = parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * part_floats<D, ROWS>();
+        for (int x = threadIdx.x; x < ROWS * D / 2; x += kWarps * 32) {
             const int row = x / (D / 2), p = x % (D / 2) * 2;
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem) + (i * kRows + row) * MS + p);
+                const float2 v = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(smem) + (i * ROWS + row) * MS + p);
                 sum.x += v.x;
                 sum.y += v.y;
             }
@@ -651,7 +696,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
                 const int tile = p / 16, gg = (p % 16) / 2;
                 const int e = VB == 16 ? tile / 8 * 128 + gg * 16 + tile % 8 * 2 : gg * 8 + tile * 2;
                 if (row < rows && e < a.d) {
-                    const int rho = rt * kRows + row;
+                    const int rho = rt * ROWS + row;
                     const float inv = L == 0.f ? 0.f : 1.f / L;     // no key seen: zero
                     uint16_t* o = a.out[r] + (static_cast<long long>(sw.begin + rho / group) * a.q_heads + h * group + rho % group) * a.d + e;
                     *reinterpret_cast<uint32_t*>(o) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
@@ -659,8 +704,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
             } else {
                 *reinterpret_cast<float2*>(part + row * D + p) = sum;
                 if (p == 0) {
-                    part[kRows * D + row] = M;
-                    part[kRows * D + kRows + row] = L;
+                    part[ROWS * D + row] = M;
+                    part[ROWS * D + ROWS + row] = L;
                 }
             }
         }
@@ -685,7 +730,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 3) kv_attention_ke
 constexpr int kMergeGroups = 4;
 constexpr int kMaxGrid = 2048;      // blocks of the attention kernel
 
-template <bool BF16, int D>
+template <bool BF16, int D, int ROWS>
 __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const __grid_constant__ KvAttnArgs a) {
     constexpr int VB = D >= 128 ? 16 : 8, T = kMergeGroups * D / 2;
     __shared__ float weight[kMaxGrid];
@@ -698,13 +743,13 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     const int group = a.q_heads / a.heads;
     int begin, end;
     seq_tokens(a.cu, rec.seq, a.tokens, begin, end);
-    const int rho = rec.row_tile * kRows + blockIdx.y;
+    const int rho = rec.row_tile * ROWS + blockIdx.y;
     if (rho >= (end - begin) * group) return;
     const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
     const int row = blockIdx.y, first = blockIdx.x, count = rec.last_block - first + 1;
-    auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D>(); };
+    auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
     float M = kNoMax;
-    for (int i = threadIdx.x; i < count; i += T) M = fmaxf(M, weight[i] = part(i)[kRows * D + row]);
+    for (int i = threadIdx.x; i < count; i += T) M = fmaxf(M, weight[i] = part(i)[ROWS * D + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = M;
@@ -715,7 +760,7 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     for (int i = threadIdx.x; i < count; i += T) {
         const float f = exp2_fast(weight[i] - M);
         weight[i] = f;
-        L = fmaf(part(i)[kRows * D + kRows + row], f, L);
+        L = fmaf(part(i)[ROWS * D + ROWS + row], f, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -758,8 +803,8 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
 // of 131071 (28 blocks an item).
 constexpr int kFewParts = 4;
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kRows * 32) kv_attention_merge_rows(const __grid_constant__ KvAttnArgs a) {
+template <bool BF16, int D, int ROWS>
+__global__ void __launch_bounds__(ROWS * 32) kv_attention_merge_rows(const __grid_constant__ KvAttnArgs a) {
     constexpr int VB = D >= 128 ? 16 : 8, P = D / 64;       // pairs of values of a lane: 2 lane + 64 i
     grid_dependency_wait();
     const Record* recs = reinterpret_cast<const Record*>(a.scratch);
@@ -768,13 +813,13 @@ __global__ void __launch_bounds__(kRows * 32) kv_attention_merge_rows(const __gr
     const int group = a.q_heads / a.heads, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int begin, end;
     seq_tokens(a.cu, rec.seq, a.tokens, begin, end);
-    const int rho = rec.row_tile * kRows + row;
+    const int rho = rec.row_tile * ROWS + row;
     if (rho >= (end - begin) * group) return;
     const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
     const int first = blockIdx.x, count = rec.last_block - first + 1;
-    auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D>(); };
+    auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
     float M = kNoMax;
-    for (int i = lane; i < count; i += 32) M = fmaxf(M, part(i)[kRows * D + row]);
+    for (int i = lane; i < count; i += 32) M = fmaxf(M, part(i)[ROWS * D + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
@@ -784,8 +829,8 @@ __global__ void __launch_bounds__(kRows * 32) kv_attention_merge_rows(const __gr
     for (int i0 = 0; i0 < count; i0 += 32) {
         float f = 0.f;
         if (i0 + lane < count) {
-            f = exp2_fast(part(i0 + lane)[kRows * D + row] - M);
-            L = fmaf(part(i0 + lane)[kRows * D + kRows + row], f, L);
+            f = exp2_fast(part(i0 + lane)[ROWS * D + row] - M);
+            L = fmaf(part(i0 + lane)[ROWS * D + ROWS + row], f, L);
         }
         const int n = min(32, count - i0);
 #pragma unroll 8
@@ -812,7 +857,7 @@ __global__ void __launch_bounds__(kRows * 32) kv_attention_merge_rows(const __gr
     }
 }
 
-template <bool BF16, int D, bool EXACT>
+template <bool BF16, int D, bool EXACT, int ROWS>
 struct Launcher {
     // Blocks that one SM holds; sets the kernel up on the current device.
     static cudaError_t resident(int* out) {
@@ -826,11 +871,11 @@ struct Launcher {
             *out = cached[dev];
             return cudaSuccess;
         }
-        auto kern = kv_attention_kernel<BF16, D, EXACT>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D>());
+        auto kern = kv_attention_kernel<BF16, D, EXACT, ROWS>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<D, ROWS>());
         if (e != cudaSuccess) return e;
         int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, attn_smem<D>());
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, attn_smem<D, ROWS>());
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 64) cached[dev] = n;
@@ -844,63 +889,91 @@ struct Launcher {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
         cfg.blockDim = dim3(kWarps * 32, 1, 1);
-        cfg.dynamicSmemBytes = attn_smem<D>();
+        cfg.dynamicSmemBytes = attn_smem<D, ROWS>();
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = pdl_launch() ? 1 : 0;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<BF16, D, EXACT>, a);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<BF16, D, EXACT, ROWS>, a);
         if (e != cudaSuccess) return e;
         // no item spans blocks where none has more than one tile
         if (a.table_width * a.page <= kTile) return cudaSuccess;
         cfg.dynamicSmemBytes = 0;
         if (grid < static_cast<long long>(kFewParts) * a.seqs * a.R * a.heads) {
-            cfg.blockDim = dim3(kRows * 32, 1, 1);
-            return cudaLaunchKernelEx(&cfg, kv_attention_merge_rows<BF16, D>, a);
+            cfg.blockDim = dim3(ROWS * 32, 1, 1);
+            return cudaLaunchKernelEx(&cfg, kv_attention_merge_rows<BF16, D, ROWS>, a);
         }
-        cfg.gridDim = dim3(static_cast<unsigned>(grid), kRows, 1);
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), ROWS, 1);
         cfg.blockDim = dim3(kMergeGroups * D / 2, 1, 1);
-        return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D>, a);
+        return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D, ROWS>, a);
     }
 };
+
+// Query rows of a tile.  16 rows share one conversion of the codes, at two
+// blocks an SM instead of three for heads of 128 (no room for heads of 256):
+// worth it where the keys, not the items' beginnings and ends, take the time,
+// and tiles of 8 would read them for a quarter of the items again.  How many
+// tokens each sequence has is known on the device only: as many as the others
+// where they divide evenly, else so much on average that a quarter has more
+// than 8 rows.  8 ranks of one key head of 128, 8 against 16 rows: 48 sequences
+// of 4096 keys with 16 query heads 137 and 92 us, with 8 heads and 1 to 8
+// tokens 327 and 235, with 6 heads and 1 or 2 tokens 110 and 92, with 8 heads
+// and one token 75 and 92; 64 sequences of up to 512 keys (4096 tiles) with 8
+// heads and 1 or 2 tokens 27.3 and 30.5, of up to 2048 keys 52.7 and 49.7; 128
+// sequences of up to 256 keys with 16 heads 42.3 and 39.5.
+constexpr long long kManyTiles = 4096;
+
+long long table_tiles(const KvAttnArgs& a) { return std::max<long long>(1, (a.table_width * a.page + kTile - 1) / kTile); }
+
+int tile_rows(const KvAttnArgs& a) {
+    const int group = a.q_heads / a.heads;
+    const long long tokens = a.tokens, seqs = a.seqs;
+    const bool many_rows = tokens % seqs == 0 ? tokens / seqs * group > 8 : 2 * tokens * group >= 15 * seqs && 4 * tokens >= 5 * seqs;
+    const bool many_tiles = table_tiles(a) >= kManyTiles || table_tiles(a) * a.seqs * a.R * a.heads >= kManyTiles;
+    return a.d <= 128 && many_rows && many_tiles ? 16 : 8;
+}
 
 // Head sizes 64, 128 and 256 have instances of their own; the others take the
 // next of them with the rest of the head zero.
 int padded_d(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <typename F>
-cudaError_t with_instance(bool bf16, int d, F f) {
+template <bool BF16, typename F>
+cudaError_t with_rows(int d, int rows, F f) {
     const bool exact = padded_d(d) == d;
-#define COC_ATTN(B, D) return exact ? f(Launcher<B, D, true>()) : f(Launcher<B, D, false>())
-    if (bf16) {
-        if (padded_d(d) == 64) COC_ATTN(true, 64);
-        if (padded_d(d) == 128) COC_ATTN(true, 128);
-        COC_ATTN(true, 256);
+#define COC_ATTN(D, ROWS) return exact ? f(Launcher<BF16, D, true, ROWS>()) : f(Launcher<BF16, D, false, ROWS>())
+    if (padded_d(d) == 256) COC_ATTN(256, 8);
+    if (rows == 16) {
+        if (padded_d(d) == 64) COC_ATTN(64, 16);
+        COC_ATTN(128, 16);
     }
-    if (padded_d(d) == 64) COC_ATTN(false, 64);
-    if (padded_d(d) == 128) COC_ATTN(false, 128);
-    COC_ATTN(false, 256);
+    if (padded_d(d) == 64) COC_ATTN(64, 8);
+    COC_ATTN(128, 8);
 #undef COC_ATTN
+}
+
+template <typename F>
+cudaError_t with_instance(const KvAttnArgs& a, bool bf16, F f) {
+    return bf16 ? with_rows<true>(a.d, tile_rows(a), f) : with_rows<false>(a.d, tile_rows(a), f);
 }
 
 }  // namespace
 
 cudaError_t kv_attention_plan(const KvAttnArgs& a, bool bf16, int sm_count, int* grid, size_t* scratch) {
     int n = 0;
-    const cudaError_t e = with_instance(bf16, a.d, [&](auto l) { return l.resident(&n); });
+    const cudaError_t e = with_instance(a, bf16, [&](auto l) { return l.resident(&n); });
     if (e != cudaSuccess) return e;
     // never more blocks than there can be units
-    const int group = a.q_heads / a.heads;
-    const long long items = (static_cast<long long>(a.tokens) * group / kRows + a.seqs) * a.R * a.heads;
-    const long long tiles = std::max<long long>(1, (a.table_width * a.page + kTile - 1) / kTile);
+    const int group = a.q_heads / a.heads, rows = tile_rows(a);
+    const long long items = (static_cast<long long>(a.tokens) * group / rows + a.seqs) * a.R * a.heads;
+    const long long tiles = table_tiles(a);
     long long resident = static_cast<long long>(n) * sm_count;
     resident = std::min<long long>(resident, kMaxGrid);
     *grid = static_cast<int>(tiles >= resident ? resident : std::min(resident, items * tiles));
-    *scratch = static_cast<size_t>(*grid) * (sizeof(Record) + 2 * kRows * (padded_d(a.d) + 2) * sizeof(float));
+    *scratch = static_cast<size_t>(*grid) * (sizeof(Record) + 2 * rows * (padded_d(a.d) + 2) * sizeof(float));
     return cudaSuccess;
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& a, bool bf16, int grid, cudaStream_t stream) {
-    return with_instance(bf16, a.d, [&](auto l) { return l.launch(a, grid, stream); });
+    return with_instance(a, bf16, [&](auto l) { return l.launch(a, grid, stream); });
 }
 
 }  // namespace coc

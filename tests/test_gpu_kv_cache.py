@@ -640,3 +640,62 @@ def test_outputs_of_several_ranks_are_ordinary_tensors():
     outs[0].zero_()
     view = outs[0].view(4, 80)[1:]
     assert view.shape == (3, 80) and not view.any()
+
+
+# Sequences with clearly more than 8 rows behind a table of 4096 tiles or more take tiles of 16 rows.
+TALL = [
+    # R, hq, hkv, d, page, new tokens, lengths, window, sinks, dtype
+    (1, 16, 1, 128, 128, [1, 1], [700, 1], 0, 0, BF),
+    (2, 9, 1, 64, 128, [1, 1, 1], [0, 65, 3000], 0, 0, HF),            # one row past a tile of 8, a row that sees nothing
+    (1, 20, 1, 80, 64, [2, 0, 3], [500, 50, 2], 0, 0, BF),             # ragged last tile, 3 new tokens of 2 positions
+    (1, 8, 2, 128, 32, [6, 1, 4], [300, 64, 4], 0, 0, HF),
+    (1, 5, 1, 112, 128, [7], [1029], 100, 4, BF),                      # rows of one tile with different windows
+    (2, 24, 2, 128, 64, [3, 2], [300, 2000], 1, 0, BF),
+    (1, 4, 4, 48, 16, [19, 5], [210, 17], 33, 70, HF),
+    (1, 32, 2, 16, 128, [1], [20000], 0, 0, BF),                       # split over many blocks
+]
+
+
+@pytest.mark.parametrize("R,hq,hkv,d,page,news,lens,window,sinks,dt", TALL)
+def test_attention_tiles_of_16_rows(R, hq, hkv, d, page, news, lens, window, sinks, dt):
+    table, rk, rv, qs = build(R, hq, hkv, d, page, news, lens, dt, seed=d + page, width=4096 * 64 // page)
+    cache, cu = to_cache(rk, rv), kv.offsets(news)
+    outs = attend(cache, table, lens, cu, qs, window=window, sinks=sinks)
+    coc.sync_status()
+    check(outs, qs, rk, rv, table, lens, cu, page, window, sinks)
+    again = attend(cache, table, lens, cu, qs, window=window, sinks=sinks)
+    assert all(torch.equal(a, b) for a, b in zip(outs, again))
+
+
+@pytest.mark.parametrize("d,hq", [(128, 12), (64, 5)])
+def test_attention_tiles_of_16_rows_nan(d, hq):
+    """As with tiles of 8 rows: a NaN value reaches only the rows that see it, in its place, a NaN key only the rows that see it."""
+    news, lens = [3], [50]
+    table, rk, rv, qs = build(1, hq, 1, d, 16, news, lens, BF, seed=6, width=16384)
+    page48 = table[0, 3].item()
+    ref, size, reach = kv.attention(qs[0], kv.values(*rk[0]), kv.values(*rv[0]), table, lens, [0, 3], 16, d ** -0.5)
+    bound = kv.attention_bound(ref, size, reach, 50, BF)
+    bad_v, bad_k = rv[0][0].clone(), rk[0][0].clone()
+    bad_v[page48, 0, 0, 7] = kv.NAN_CODE         # position 48: seen by new tokens 1 and 2
+    bad_k[page48, 0, 1, 3] = kv.NAN_CODE         # position 49: seen by new token 2 alone
+    got = attend(to_cache(rk, [(bad_v, rv[0][1])]), table, lens, [0, 3], qs)[0].cpu().double()
+    assert torch.isnan(got[1:, :, 7]).all()
+    rest = [i for i in range(d) if i != 7]
+    assert ((got - ref).abs() <= bound)[:, :, rest].all()
+    assert ((got - ref).abs() <= bound)[0].all()
+    got = attend(to_cache([(bad_k, rk[0][1])], rv), table, lens, [0, 3], qs)[0].cpu().double()
+    assert torch.isnan(got[2]).all()
+    assert ((got - ref).abs() <= bound)[:2].all()
+    coc.sync_status()
+
+
+@pytest.mark.parametrize("seed,q_std,k_exp,v_exp", [(1, 30.0, 0, 0), (3, 1.0, -40, 30), (4, 1.0, 0, -60), (5, 6e4, -20, 0)])
+def test_attention_tiles_of_16_rows_ranges(seed, q_std, k_exp, v_exp):
+    news, lens = [1, 2], [150, 333]
+    table, rk, rv, qs = build(1, 24, 2, 128, 32, news, lens, BF, seed, q_std=q_std, width=8192)
+    rk = [(c, s * 2.0 ** k_exp) for c, s in rk]
+    rv = [(c, s * 2.0 ** v_exp) for c, s in rv]
+    scale = 128 ** -0.5 * 2.0 ** -k_exp / (q_std if q_std > 100 else 1.0)
+    outs = attend(to_cache(rk, rv), table, lens, kv.offsets(news), qs, scale=scale)
+    coc.sync_status()
+    check(outs, qs, rk, rv, table, lens, kv.offsets(news), 32, scale=scale)

@@ -69,14 +69,22 @@ constexpr int attn_smem() { return kWarps * ROWS * merge_stride<D>() * 4; }
 
 // Scratch: per block two parts (ROWS x D sums, then ROWS maxima and sums),
 // and a record of the item that the block begins and does not end.
-struct Record {
-    int open;        // 1: there is one
-    int seq, head, row_tile;
+struct __align__(32) Record {
+    int rows;                   // 0: there is none
     int last_block;
+    int head;                   // rank and key head
+    int token, row;             // the sequence's first token, the tile's first row after it
     int pad[3];
 };
 template <int D, int ROWS>
 constexpr long long part_floats() { return ROWS * (D + 2); }
+
+// value of the head that the pair p of an accumulator row begins with
+template <int D>
+__device__ __forceinline__ int value_of(int p) {
+    const int tile = p / 16, g = (p % 16) / 2;
+    return D >= 128 ? tile / 8 * 128 + g * 16 + tile % 8 * 2 : g * 8 + tile * 2;
+}
 
 // Codes are read once by one lane: no place in L1.
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
     Record* rec = reinterpret_cast<Record*>(a.scratch) + blockIdx.x;
     float* parts = reinterpret_cast<float*>(reinterpret_cast<Record*>(a.scratch) + gridDim.x);
     if (u0 >= u1) {
-        if (threadIdx.x == 0) rec->open = 0;
+        if (threadIdx.x == 0) rec->rows = 0;
         return;
     }
     if (before <= u0 && u0 < before + mine * RH) {
@@ -693,8 +701,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) L += wl[i][row] * exp2_fast(wm[i][row] - M);
             if (begins && ends) {
-                const int tile = p / 16, gg = (p % 16) / 2;
-                const int e = VB == 16 ? tile / 8 * 128 + gg * 16 + tile % 8 * 2 : gg * 8 + tile * 2;
+                const int e = value_of<D>(p);
                 if (row < rows && e < a.d) {
                     const int rho = rt * ROWS + row;
                     const float inv = L == 0.f ? 0.f : 1.f / L;     // no key seen: zero
@@ -712,44 +719,61 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
         if (begins && !ends) {
             left_open = true;
             if (threadIdx.x == 0) {
-                rec->seq = s;
-                rec->head = rh;
-                rec->row_tile = rt;
+                rec->rows = rows;
                 rec->last_block = static_cast<int>((start + sw.tiles - 1) / quota);
+                rec->head = rh;
+                rec->token = sw.begin;
+                rec->row = rt * ROWS;
             }
         }
         __syncthreads();    // the merge area and wm are read before the next item
         u = start + t1;
     }
-    if (threadIdx.x == 0) rec->open = left_open ? 1 : 0;
+    if (threadIdx.x == 0 && !left_open) rec->rows = 0;
 }
 
-// Block (b, row): adds the parts of the item that block b began and others
-// went on with.  Group y of the threads adds the parts y, y + kMergeGroups,
-// ... in order, eight loads at a time, then the groups are added in order.
+// Merging the parts of the item that block b began and others went on with.
+// Its time is latency, the record's and then the parts': the first values are
+// asked for together with the maxima, before their weights are known.
+__device__ __forceinline__ uint32_t* out_at(const KvAttnArgs& a, const Record& rec, int row, int e) {
+    const int group = a.q_heads / a.heads, r = rec.head / a.heads, h = rec.head - r * a.heads, rho = rec.row + row;
+    return reinterpret_cast<uint32_t*>(a.out[r] + (static_cast<long long>(rec.token + rho / group) * a.q_heads + h * group + rho % group) * a.d + e);
+}
+constexpr int kAtOnce = 8;          // parts whose values a thread has in flight
+
+// Block (b, row).  Group y of the threads adds the parts y, y + kMergeGroups,
+// ... in order, then the groups are added in order.
 constexpr int kMergeGroups = 4;
 constexpr int kMaxGrid = 2048;      // blocks of the attention kernel
 
 template <bool BF16, int D, int ROWS>
 __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const __grid_constant__ KvAttnArgs a) {
-    constexpr int VB = D >= 128 ? 16 : 8, T = kMergeGroups * D / 2;
+    constexpr int T = kMergeGroups * D / 2;
     __shared__ float weight[kMaxGrid];
     __shared__ float red[2][T / 32];
     __shared__ float2 sums[kMergeGroups][D / 2];
     grid_dependency_wait();
     const Record* recs = reinterpret_cast<const Record*>(a.scratch);
     const Record rec = recs[blockIdx.x];
-    if (!rec.open) return;
-    const int group = a.q_heads / a.heads;
-    int begin, end;
-    seq_tokens(a.cu, rec.seq, a.tokens, begin, end);
-    const int rho = rec.row_tile * ROWS + blockIdx.y;
-    if (rho >= (end - begin) * group) return;
-    const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
     const int row = blockIdx.y, first = blockIdx.x, count = rec.last_block - first + 1;
+    if (row >= rec.rows) return;
+    const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
     auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
-    float M = kNoMax;
-    for (int i = threadIdx.x; i < count; i += T) M = fmaxf(M, weight[i] = part(i)[ROWS * D + row]);
+    const int y = threadIdx.x / (D / 2), x = threadIdx.x % (D / 2), p = 2 * x;
+    float2 v[kAtOnce];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = i0 + k * kMergeGroups;
+            v[k] = i < count ? *reinterpret_cast<const float2*>(part(i) + row * D + p) : make_float2(0.f, 0.f);
+        }
+    };
+    fetch(y);
+    float M = kNoMax, l = 0.f;      // l: of part threadIdx.x
+    for (int i = threadIdx.x; i < count; i += T) {
+        M = fmaxf(M, weight[i] = part(i)[ROWS * D + row]);
+        if (i == threadIdx.x) l = part(i)[ROWS * D + ROWS + row];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = M;
@@ -760,20 +784,23 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     for (int i = threadIdx.x; i < count; i += T) {
         const float f = exp2_fast(weight[i] - M);
         weight[i] = f;
-        L = fmaf(part(i)[ROWS * D + ROWS + row], f, L);
+        L = fmaf(i == threadIdx.x ? l : part(i)[ROWS * D + ROWS + row], f, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = L;
     __syncthreads();
-    const int y = threadIdx.x / (D / 2), x = threadIdx.x % (D / 2), p = 2 * x;
     float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 8
-    for (int i = y; i < count; i += kMergeGroups) {
-        const float f = weight[i];
-        const float2 v = *reinterpret_cast<const float2*>(part(i) + row * D + p);
-        sum.x = fmaf(v.x, f, sum.x);
-        sum.y = fmaf(v.y, f, sum.y);
+    for (int i0 = y; i0 < count; i0 += kAtOnce * kMergeGroups) {
+        if (i0 != y) fetch(i0);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = i0 + k * kMergeGroups;
+            if (i < count) {
+                sum.x = fmaf(v[k].x, weight[i], sum.x);
+                sum.y = fmaf(v[k].y, weight[i], sum.y);
+            }
+        }
     }
     sums[y][x] = sum;
     __syncthreads();
@@ -786,13 +813,9 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     L = 0.f;
 #pragma unroll
     for (int i = 0; i < T / 32; ++i) L += red[1][i];
-    const int tile = p / 16, gg = (p % 16) / 2;
-    const int e = VB == 16 ? tile / 8 * 128 + gg * 16 + tile % 8 * 2 : gg * 8 + tile * 2;
-    if (e >= a.d) return;
-    const int r = rec.head / a.heads, h = rec.head - r * a.heads;
+    const int e = value_of<D>(p);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint16_t* o = a.out[r] + (static_cast<long long>(begin + rho / group) * a.q_heads + h * group + rho % group) * a.d + e;
-    *reinterpret_cast<uint32_t*>(o) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
+    if (e < a.d) *out_at(a, rec, row, e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
 }
 
 // The same with a warp a row and the parts one after another: block b, warp =
@@ -805,55 +828,67 @@ constexpr int kFewParts = 4;
 
 template <bool BF16, int D, int ROWS>
 __global__ void __launch_bounds__(ROWS * 32) kv_attention_merge_rows(const __grid_constant__ KvAttnArgs a) {
-    constexpr int VB = D >= 128 ? 16 : 8, P = D / 64;       // pairs of values of a lane: 2 lane + 64 i
+    constexpr int P = D / 64;       // pairs of values of a lane: 2 lane + 64 i
+    constexpr int AT_ONCE = 4;
     grid_dependency_wait();
     const Record* recs = reinterpret_cast<const Record*>(a.scratch);
     const Record rec = recs[blockIdx.x];
-    if (!rec.open) return;
-    const int group = a.q_heads / a.heads, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int begin, end;
-    seq_tokens(a.cu, rec.seq, a.tokens, begin, end);
-    const int rho = rec.row_tile * ROWS + row;
-    if (rho >= (end - begin) * group) return;
+    const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (row >= rec.rows) return;
     const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
     const int first = blockIdx.x, count = rec.last_block - first + 1;
     auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
-    float M = kNoMax;
-    for (int i = lane; i < count; i += 32) M = fmaxf(M, part(i)[ROWS * D + row]);
+    float2 v[AT_ONCE][P];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                v[i][k] = i0 + i < count ? *reinterpret_cast<const float2*>(part(i0 + i) + row * D + 2 * lane + 64 * k) : make_float2(0.f, 0.f);
+    };
+    fetch(0);
+    float m = kNoMax, l = 0.f;      // of part `lane`
+    if (lane < count) {
+        m = part(lane)[ROWS * D + row];
+        l = part(lane)[ROWS * D + ROWS + row];
+    }
+    float M = m;
+    for (int i = lane + 32; i < count; i += 32) M = fmaxf(M, part(i)[ROWS * D + row]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
+    float L = 0.f, f = 0.f;
     float2 sum[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) sum[k] = make_float2(0.f, 0.f);
-    for (int i0 = 0; i0 < count; i0 += 32) {
-        float f = 0.f;
-        if (i0 + lane < count) {
-            f = exp2_fast(part(i0 + lane)[ROWS * D + row] - M);
-            L = fmaf(part(i0 + lane)[ROWS * D + ROWS + row], f, L);
+    for (int i0 = 0; i0 < count; i0 += AT_ONCE) {
+        if (i0 != 0) fetch(i0);
+        if (i0 % 32 == 0) {
+            if (i0 != 0 && i0 + lane < count) {
+                m = part(i0 + lane)[ROWS * D + row];
+                l = part(i0 + lane)[ROWS * D + ROWS + row];
+            }
+            f = i0 + lane < count ? exp2_fast(m - M) : 0.f;
+            L = fmaf(l, f, L);
         }
-        const int n = min(32, count - i0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, f, i);
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const float2 v = *reinterpret_cast<const float2*>(part(i0 + i) + row * D + 2 * lane + 64 * k);
-                sum[k].x = fmaf(v.x, w, sum[k].x);
-                sum[k].y = fmaf(v.y, w, sum[k].y);
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, (i0 + i) % 32);
+            if (i0 + i < count) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    sum[k].x = fmaf(v[i][k].x, w, sum[k].x);
+                    sum[k].y = fmaf(v[i][k].y, w, sum[k].y);
+                }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int r = rec.head / a.heads, h = rec.head - r * a.heads;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint16_t* o = a.out[r] + (static_cast<long long>(begin + rho / group) * a.q_heads + h * group + rho % group) * a.d;
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-        const int p = 2 * lane + 64 * k, tile = p / 16, gg = (p % 16) / 2;
-        const int e = VB == 16 ? tile / 8 * 128 + gg * 16 + tile % 8 * 2 : gg * 8 + tile * 2;
-        if (e < a.d) *reinterpret_cast<uint32_t*>(o + e) = pack2<BF16>(__float_as_uint(sum[k].x * inv), __float_as_uint(sum[k].y * inv));
+        const int e = value_of<D>(2 * lane + 64 * k);
+        if (e < a.d) *out_at(a, rec, row, e) = pack2<BF16>(__float_as_uint(sum[k].x * inv), __float_as_uint(sum[k].y * inv));
     }
 }
 

@@ -821,8 +821,8 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
 // The same with a warp a row and the parts one after another: block b, warp =
 // row; an eighth of the blocks and no barrier.  It is taken where the blocks
 // share few parts an item, fewer than kFewParts if every sequence has a row
-// tile: the whole call takes 75.1 instead of 77.2 us for 48 sequences of up to
-// 8192 keys on 8 ranks (1.2 blocks an item), but 97.2 instead of 94.1 for two
+// tile: the whole call takes 75.4 instead of 79.8 us for 48 sequences of up to
+// 8192 keys on 8 ranks (1.2 blocks an item), but 95.3 instead of 94.1 for two
 // of 131071 (28 blocks an item).
 constexpr int kFewParts = 4;
 

@@ -10,9 +10,10 @@
 // What bounds it.  k n / 2 bytes of weights, read once: the operations per
 // byte (4 m) are few, but taking codes out of words costs instructions: a
 // shift, a mask and an addition per pair, 88 of the 150 that a warp issues for
-// 2048 weights at up to 8 tokens (205 at 16), and the SMs' instruction rate is
-// the bound: 3.0 TB/s of weights at n 8192, k 8 x 1024, m 8 (12.3 us), 3.4 at
-// n 14336, k 8 x 7168, m 16 with zero points (130 us).
+// 2048 weights at up to 8 tokens (205 at 16), and their dependent sequences are
+// the bound: 3.3 TB/s of weights at n 8192, k 8 x 1024, m 8 (11.0 us), 3.4 at
+// n 14336, k 8 x 7168, m 16 with zero points (130 us); with nothing copied at
+// all the two take 9.6 and 109 us.
 // W^T is the A operand of mma.sync (16 weight columns x 16 of k) and x^T the B
 // operand (8 tokens).  A word holds 8 codes along k of one column; a mask
 // takes two codes four apart into the halves of a register, so the pairs
@@ -61,6 +62,14 @@ constexpr int w4_smem() {
     const int sums = kWarps * sum_floats<NT>() * 4;
     return ring > sums ? ring : sums;
 }
+
+// Where every block can have an SM of its own it asks for more than half of an
+// SM's shared memory: else the next launch's blocks, which come while this
+// one's still run, gather two by two on the SMs that are free, and so do those
+// of the launch after it.  n 8192, k 8 x 1024, m 8 then took 17.7 us a call
+// instead of 10.9 for as long as calls followed each other, or 10.9, by the
+// order the first blocks came in.
+constexpr int kAloneSmem = 116 * 1024;
 
 // n of BYTES bytes, the rest zero.
 template <int BYTES>
@@ -373,21 +382,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
 }
 
 template <bool BF16, int NT, bool ZERO, int SS>
-cudaError_t launch_t(const W4Args& a, cudaStream_t stream) {
+cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
+    constexpr int kAlone = std::max(w4_smem<NT, SS>(), kAloneSmem);
     auto kern = w4_kernel<BF16, NT, ZERO, SS>;
     static std::atomic<unsigned char> smem_set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, w4_smem<NT, SS>())) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone)) != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.n + kCols - 1) / kCols * a.splits), static_cast<unsigned>((a.m + 8 * NT - 1) / (8 * NT)), 1);
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = w4_smem<NT, SS>();
+    cfg.dynamicSmemBytes = static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y <= sm_count ? kAlone : w4_smem<NT, SS>();
     cfg.stream = stream;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -404,15 +414,15 @@ cudaError_t launch_t(const W4Args& a, cudaStream_t stream) {
 }
 
 template <bool BF16, int NT, bool ZERO>
-cudaError_t launch_s(const W4Args& a, cudaStream_t stream) {
-    if (NT == 1 && a.group % (4 * kStep) == 0) return launch_t<BF16, NT, ZERO, NT == 1 ? 4 : 2>(a, stream);
-    return a.group % (2 * kStep) == 0 ? launch_t<BF16, NT, ZERO, 2>(a, stream) : launch_t<BF16, NT, ZERO, 1>(a, stream);
+cudaError_t launch_s(const W4Args& a, int sm_count, cudaStream_t stream) {
+    if (NT == 1 && a.group % (4 * kStep) == 0) return launch_t<BF16, NT, ZERO, NT == 1 ? 4 : 2>(a, sm_count, stream);
+    return a.group % (2 * kStep) == 0 ? launch_t<BF16, NT, ZERO, 2>(a, sm_count, stream) : launch_t<BF16, NT, ZERO, 1>(a, sm_count, stream);
 }
 template <bool BF16>
-cudaError_t launch_b(const W4Args& a, cudaStream_t stream) {
+cudaError_t launch_b(const W4Args& a, int sm_count, cudaStream_t stream) {
     const bool two = a.m > 8, zero = a.zero[0] != nullptr;
-    if (two) return zero ? launch_s<BF16, 2, true>(a, stream) : launch_s<BF16, 2, false>(a, stream);
-    return zero ? launch_s<BF16, 1, true>(a, stream) : launch_s<BF16, 1, false>(a, stream);
+    if (two) return zero ? launch_s<BF16, 2, true>(a, sm_count, stream) : launch_s<BF16, 2, false>(a, sm_count, stream);
+    return zero ? launch_s<BF16, 1, true>(a, sm_count, stream) : launch_s<BF16, 1, false>(a, sm_count, stream);
 }
 
 }  // namespace
@@ -438,7 +448,7 @@ cudaError_t launch_w4(const W4Args& args, bool bf16, int sm_count, cudaStream_t 
             a.splits = k;
         }
     }
-    return bf16 ? launch_b<true>(a, stream) : launch_b<false>(a, stream);
+    return bf16 ? launch_b<true>(a, sm_count, stream) : launch_b<false>(a, sm_count, stream);
 }
 
 }  // namespace coc

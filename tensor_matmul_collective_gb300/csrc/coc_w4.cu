@@ -432,7 +432,7 @@ cudaError_t launch_b(const W4Args& a, int sm_count, cudaStream_t stream) {
 // halves and quarters, as far as joining them costs less (about 3 steps a
 // block and 2 a further range).  Two blocks on an SM are no faster than one
 // after the other: the SM's instruction rate is the bound.  Measured, ranges 1 /
-// 2 / 4: n 4096, k 4096, m 1 6.4 / 5.6 / 5.9 us; n 8192, k 8 x 1024, m 8 12.3 /
+// 2 / 4: n 4096, k 4096, m 1 6.4 / 5.6 / 5.9 us; n 8192, k 8 x 1024, m 8 11.0 /
 // 14.0 / 20; n 14336, k 8 x 7168, m 16 159 / 130 / 152.
 cudaError_t launch_w4(const W4Args& args, bool bf16, int sm_count, cudaStream_t stream) {
     W4Args a = args;

@@ -86,6 +86,11 @@ __device__ __forceinline__ int value_of(int p) {
     return D >= 128 ? tile / 8 * 128 + g * 16 + tile % 8 * 2 : g * 8 + tile * 2;
 }
 
+// Where the outputs of a token's query head lie.
+__device__ __forceinline__ uint16_t* out_at(const KvAttnArgs& a, int rank, int token, int head) {
+    return a.out[rank] + (static_cast<long long>(token) * a.q_heads + head) * a.d;
+}
+
 // Codes are read once by one lane: no place in L1.
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
     uint4 v;
@@ -204,6 +209,14 @@ struct Limits {
 template <int D, int ROWS>
 constexpr int blocks_per_sm() { return D == 256 || (D == 128 && ROWS == 16) ? 2 : 3; }
 
+// An item's end: each row's maximum and sum over the warps, one over the sum
+// (0 if there is none: no key seen, zero), and its place in the output.
+template <int ROWS>
+struct Ending {
+    float max[ROWS], sum[ROWS], inv[ROWS];
+    uint16_t* out[ROWS];
+};
+
 // EXACT: the head has D values (every offset inside a chunk is a constant);
 // otherwise fewer, and the pieces past them are zero.
 template <bool BF16, int D, bool EXACT, int ROWS>
@@ -219,6 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
     __shared__ long long found[3];
     __shared__ float wm[kWarps][ROWS], wl[kWarps][ROWS];
     __shared__ Limits<ROWS> limits;
+    __shared__ Ending<ROWS> ending;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int group = a.q_heads / a.heads;
@@ -281,26 +295,29 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
     const int page_bytes = a.heads * head_bytes;                       // at most 2^25
     const uint32_t pages = static_cast<uint32_t>(a.pages);
 
-    for (long long u = u0; u < u1;) {
+    // Items follow each other: row tiles, heads, ranks, sequences.  `unit` is
+    // the first of the item's units; those ahead of its first tile go with that
+    // tile.
+    int rt, r, h;
+    long long unit;
+    {
         const int span = sw.tiles + kItemCost;
-        if (u >= base + static_cast<long long>(sw.row_tiles) * span * RH) {
-            base += static_cast<long long>(sw.row_tiles) * span * RH;
-            sw = seq_work<ROWS>(a, ++s);
-            continue;
-        }
-        // item (rank and head, row tile), tiles [t0, t1) of it; the units
-        // ahead of its first tile go with that tile
-        const int item = static_cast<int>((u - base) / span);
-        const long long start = base + static_cast<long long>(item) * span + kItemCost;     // unit of its first tile
-        const int t0 = static_cast<int>(max(0LL, u - start));
+        const long long item = (u0 - base) / span;
+        const int rh = static_cast<int>(item / sw.row_tiles);
+        rt = static_cast<int>(item - static_cast<long long>(rh) * sw.row_tiles);
+        r = rh / a.heads;
+        h = rh - r * a.heads;
+        unit = base + item * span;
+    }
+    for (;;) {
+        const long long start = unit + kItemCost;       // unit of its first tile
+        const int t0 = static_cast<int>(max(0LL, u0 - start));
         if (start + t0 >= u1) break;
         const int t1 = static_cast<int>(min(static_cast<long long>(sw.tiles), u1 - start));
-        const int rh = item / sw.row_tiles, rt = item - rh * sw.row_tiles;
-        const int r = rh / a.heads, h = rh - r * a.heads;
 
         // ---- rows and their limits
-        const int rows = static_cast<int>(min(static_cast<long long>(ROWS), static_cast<long long>(sw.n) * group - rt * ROWS));
-        const int i0 = rt * ROWS / group, i1 = (rt * ROWS + rows - 1) / group;
+        const int row0 = rt * ROWS, rows = static_cast<int>(min(static_cast<long long>(ROWS), static_cast<long long>(sw.n) * group - row0));
+        const int i0 = row0 / group, i1 = (row0 + rows - 1) / group;
         const int shift = sw.len - sw.n + 1;        // token i's keys end at shift + i
         const int room = static_cast<int>(min(static_cast<long long>(0x7fffffff), a.table_width << page_shift));
         auto end_of = [&](int i) { return max(0, min(room, shift + i)); };
@@ -329,7 +346,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
         // a chunk between these is seen whole by every row
         const int clean_lo = from_max, clean_hi = end_min - kSub;
         const int32_t* table = a.table + static_cast<long long>(s) * a.table_width;
-        auto seen = [&](int j) { return j < lim.end && (j >= lim.from || j < lim.sinks); };   // by any row of the tile
+        struct Seen {           // by any row of the tile
+            int end, from, sinks;
+            __device__ bool operator()(int j) const { return j < end && (j >= from || j < sinks); }
+        };
+        auto any_row = [&]() { return Seen{lim.end, lim.from, lim.sinks}; };
         auto wanted = [&](int j) { return j < lim.end && (j + kSub > lim.from || j < lim.sinks); };
         // Place of the chunk whose table entry is read next, the tile it belongs to, and where the sinks' tiles end.
         int ahead = t0, place = (t0 < near ? t0 : far + t0 - near) * kTile + warp * kSub;
@@ -361,6 +382,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
             const uint8_t* kp = k_lane + static_cast<long long>(id) * page_bytes + (j & (a.page - 1)) * d;
             auto go = [&](auto all) {
                 constexpr bool ALL = decltype(all)::value;
+                Seen seen{};
+                if constexpr (!ALL) seen = any_row();
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -377,6 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
             const uint8_t* vp = v_lane + static_cast<long long>(id) * page_bytes + (j & (a.page - 1)) * d;
             auto go = [&](auto all) {
                 constexpr bool ALL = decltype(all)::value;
+                Seen seen{};
+                if constexpr (!ALL) seen = any_row();
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int tok = (y & 1) + 8 * (y >> 1);     // after key 2 c
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
         uint32_t qf[NT][KL * 8];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int rho = rt * ROWS + 8 * n + g;
+            const int rho = row0 + 8 * n + g;
             const bool valid = 8 * n + g < rows;
             const int tok = sw.begin + rho / group;
             const uint16_t* qp = a.q[r] + (valid ? tok * a.q_token + (h * group + rho % group) * a.q_head : 0);
@@ -527,11 +552,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                     see[n] = 0xf;
                     if (!clean) {
                         see[n] = 0;
+                        const int row = 8 * n + 2 * c;
+                        const Seen by[2] = {{lim.row_end[row], lim.row_from[row], lim.sinks}, {lim.row_end[row + 1], lim.row_from[row + 1], lim.sinks}};
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int key = j0 + g + 8 * (x >> 1), row = 8 * n + 2 * c + (x & 1);
-                            see[n] |= static_cast<uint32_t>(key < lim.row_end[row] && (key >= lim.row_from[row] || key < lim.sinks)) << x;
-                        }
+                        for (int x = 0; x < 4; ++x) see[n] |= static_cast<uint32_t>(by[x & 1](j0 + g + 8 * (x >> 1))) << x;
                     }
                     float z[4];             // log2 of the weights
                     auto logs = [&](float a0, float a1) {
@@ -682,11 +706,25 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                 *reinterpret_cast<float2*>(mine_s + x1 * MS + 16 * i + 2 * g) = make_float2(acc[n][i][1] * k1, acc[n][i][3] * k1);
             }
         }
+        if (threadIdx.x < ROWS) {
+            const int row = threadIdx.x, rho = row0 + min(row, rows - 1);
+            float M = wm[0][row], L = 0.f;
+#pragma unroll
+            for (int i = 1; i < kWarps; ++i) M = fmaxf(M, wm[i][row]);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) L += wl[i][row] * exp2_fast(wm[i][row] - M);
+            ending.max[row] = M;
+            ending.sum[row] = L;
+            ending.inv[row] = L == 0.f ? 0.f : 1.f / L;
+            ending.out[row] = out_at(a, r, sw.begin + rho / group, h * group + rho % group);
+        }
         __syncthreads();
         const bool begins = t0 == 0, ends = t1 == sw.tiles;
         float* part = parts + (2LL * blockIdx.x + (begins ? 1 : 0)) * part_floats<D, ROWS>();
-        for (int x = threadIdx.x; x < ROWS * D / 2; x += kWarps * 32) {
-            const int row = x / (D / 2), p = x % (D / 2) * 2;
+        static_assert(kWarps * 32 % (D / 2) == 0 || D / 2 % (kWarps * 32) == 0);
+#pragma unroll
+        for (int x0 = 0; x0 < ROWS * D / 2; x0 += kWarps * 32) {
+            const int x = x0 + threadIdx.x, row = x / (D / 2), p = x % (D / 2) * 2;
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
@@ -694,51 +732,51 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                 sum.x += v.x;
                 sum.y += v.y;
             }
-            float M = wm[0][row];
-#pragma unroll
-            for (int i = 1; i < kWarps; ++i) M = fmaxf(M, wm[i][row]);
-            float L = 0.f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) L += wl[i][row] * exp2_fast(wm[i][row] - M);
             if (begins && ends) {
                 const int e = value_of<D>(p);
-                if (row < rows && e < a.d) {
-                    const int rho = rt * ROWS + row;
-                    const float inv = L == 0.f ? 0.f : 1.f / L;     // no key seen: zero
-                    uint16_t* o = a.out[r] + (static_cast<long long>(sw.begin + rho / group) * a.q_heads + h * group + rho % group) * a.d + e;
-                    *reinterpret_cast<uint32_t*>(o) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
-                }
+                const float inv = ending.inv[row];
+                if (row < rows && e < a.d)
+                    *reinterpret_cast<uint32_t*>(ending.out[row] + e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
             } else {
                 *reinterpret_cast<float2*>(part + row * D + p) = sum;
-                if (p == 0) {
-                    part[ROWS * D + row] = M;
-                    part[ROWS * D + ROWS + row] = L;
-                }
             }
+        }
+        if (!(begins && ends) && threadIdx.x < ROWS) {
+            part[ROWS * D + threadIdx.x] = ending.max[threadIdx.x];
+            part[ROWS * D + ROWS + threadIdx.x] = ending.sum[threadIdx.x];
         }
         if (begins && !ends) {
             left_open = true;
-            if (threadIdx.x == 0) {
-                rec->rows = rows;
-                rec->last_block = static_cast<int>((start + sw.tiles - 1) / quota);
-                rec->head = rh;
-                rec->token = sw.begin;
-                rec->row = rt * ROWS;
+            if (threadIdx.x == 0) *rec = {rows, static_cast<int>((start + sw.tiles - 1) / quota), r * a.heads + h, sw.begin, row0, {0, 0, 0}};
+        }
+        if (!ends) break;       // the run ends inside the item
+        unit = start + sw.tiles;
+        if (++rt == sw.row_tiles) {
+            rt = 0;
+            if (++h == a.heads) {
+                h = 0;
+                if (++r == a.R) {
+                    r = 0;
+                    if (unit >= u1) break;
+                    do sw = seq_work<ROWS>(a, ++s);
+                    while (sw.row_tiles == 0);      // there is one: unit < total
+                }
             }
         }
-        __syncthreads();    // the merge area and wm are read before the next item
-        u = start + t1;
+        __syncthreads();    // the merge area, wm and the limits are read before the next item
     }
     if (threadIdx.x == 0 && !left_open) rec->rows = 0;
+}
+
+// Where the outputs of a row of a merged item lie.
+__device__ __forceinline__ uint16_t* out_at(const KvAttnArgs& a, const Record& rec, int row) {
+    const int group = a.q_heads / a.heads, r = rec.head / a.heads, h = rec.head - r * a.heads, rho = rec.row + row;
+    return out_at(a, r, rec.token + rho / group, h * group + rho % group);
 }
 
 // Merging the parts of the item that block b began and others went on with.
 // Its time is latency, the record's and then the parts': the first values are
 // asked for together with the maxima, before their weights are known.
-__device__ __forceinline__ uint32_t* out_at(const KvAttnArgs& a, const Record& rec, int row, int e) {
-    const int group = a.q_heads / a.heads, r = rec.head / a.heads, h = rec.head - r * a.heads, rho = rec.row + row;
-    return reinterpret_cast<uint32_t*>(a.out[r] + (static_cast<long long>(rec.token + rho / group) * a.q_heads + h * group + rho % group) * a.d + e);
-}
 constexpr int kAtOnce = 8;          // parts whose values a thread has in flight
 
 // Block (b, row).  Group y of the threads adds the parts y, y + kMergeGroups,
@@ -815,7 +853,7 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     for (int i = 0; i < T / 32; ++i) L += red[1][i];
     const int e = value_of<D>(p);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (e < a.d) *out_at(a, rec, row, e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
+    if (e < a.d) *reinterpret_cast<uint32_t*>(out_at(a, rec, row) + e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
 }
 
 // The same with a warp a row and the parts one after another: block b, warp =
@@ -885,10 +923,11 @@ __global__ void __launch_bounds__(ROWS * 32) kv_attention_merge_rows(const __gri
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint16_t* o = out_at(a, rec, row);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
         const int e = value_of<D>(2 * lane + 64 * k);
-        if (e < a.d) *out_at(a, rec, row, e) = pack2<BF16>(__float_as_uint(sum[k].x * inv), __float_as_uint(sum[k].y * inv));
+        if (e < a.d) *reinterpret_cast<uint32_t*>(o + e) = pack2<BF16>(__float_as_uint(sum[k].x * inv), __float_as_uint(sum[k].y * inv));
     }
 }
 

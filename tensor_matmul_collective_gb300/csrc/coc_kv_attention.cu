@@ -54,7 +54,7 @@ constexpr int kTile = kWarps * kSub;       // keys of one block's step
 constexpr float kNoMax = -1.0e38f;         // running maximum before any key
 // What beginning and ending an item costs, in tiles: an item counts as so many
 // units more than it has tiles.
-constexpr int kItemCost = 5;
+constexpr int kItemCost = 3;
 // Weights are 2^(z - m + kOffset), with m at most 2^kSlack behind the true
 // maximum (it moves only when a key exceeds it by more): at most 2^15, and
 // normal fp16 numbers down to 2^-23 of m.

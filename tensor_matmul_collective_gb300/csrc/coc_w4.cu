@@ -98,6 +98,21 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto nothing: no accumulator has to be cleared.
+template <bool BF16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // (x & mask) | bits in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
     uint32_t r;
@@ -126,17 +141,18 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float x0, float x1, f
 }
 
 // code - z of four of a word's 8 codes: the pairs (k, k + 4) for k = 2 H and
-// 2 H + 1.  off: -(1024 + z) twice (fp16) or -(128 + z) (bf16); off16: -(64 + z)
-// (fp16: a code four bits up is 16 times itself, and its product with 1/16
-// costs the addition nothing).
-template <bool BF16, int H>
+// 2 H + 1.  off: -(B + z) twice, B the number whose mantissa takes the code: 128
+// (bf16), 1024, or 1152 where z is an argument (fp16; -(1152 + z) is then the
+// byte z + 128 in -1024's mantissa); off16: -(64 + z) (fp16: a code four bits up
+// is 16 times itself, and its product with 1/16 costs the addition nothing).
+template <bool BF16, bool ZERO, int H>
 __device__ __forceinline__ void codes(uint32_t w, uint32_t off, uint32_t off16, uint32_t& p0, uint32_t& p1) {
     if constexpr (BF16) {
         p0 = add2<true>(and_or(w >> (8 * H), 0x000F000Fu, 0x43004300u), off);
         p1 = add2<true>(and_or(w >> (8 * H + 4), 0x000F000Fu, 0x43004300u), off);
     } else {
         const uint32_t v = w >> (8 * H);
-        p0 = add2<false>(and_or(v, 0x000F000Fu, 0x64006400u), off);
+        p0 = add2<false>(and_or(v, 0x000F000Fu, ZERO ? 0x64806480u : 0x64006400u), off);
         p1 = fma2_half(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, off16);
     }
 }
@@ -155,8 +171,8 @@ __device__ __forceinline__ int part_begin(int all, int i, int ways) {
 
 // Block: 64 columns, 8 NT rows of x (blockIdx.y), kWarps ranges of the
 // contraction; cluster: blocks with the same columns and further ranges.  SS
-// steps make a stage (groups are whole stages).
-template <bool BF16, int NT, bool ZERO, int SS>
+// steps make a stage (groups are whole stages; ONE: a group is one stage).
+template <bool BF16, int NT, bool ZERO, int SS, bool ONE>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constant__ W4Args a) {
     constexpr int SB = stage_bytes<NT, SS>(), kStages = stages<SS>();
     constexpr int XO = SS * 1024, CO = SS * 512 * (2 + NT);      // x, scales in a stage
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                 load((st + kStages - 1) % kStages);
                 cp_wait<kStages - 1>();
                 const uint8_t* slot = ring_p + st * SB;
-                if (fresh) {
+                if (ONE || fresh) {
                     fresh = false;
                     __syncwarp();                   // the lanes 4 g copied it for the others
                     sc = *reinterpret_cast<const uint4*>(slot + CO + g * 16);
@@ -280,10 +296,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                         const uint32_t zv[2] = {z2.x ^ 0x80808080u, z2.y ^ 0x80808080u};      // z + 128
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            // 2^23 + (z + 128) is exact, and so is what is taken off
-                            const float z = __uint_as_float(__byte_perm(zv[i / 4], 0x4B000000u, 0x7650 + (i & 3)));
-                            off[i] = pair<BF16>((BF16 ? 8388608.f : 8388608.f - 896.f) - z);
-                            if constexpr (!BF16) off16[i] = add2<false>(off[i], 0x63806380u);           // + 960
+                            if constexpr (BF16) {
+                                // 2^23 + (z + 128) is exact, and so is what is taken off
+                                off[i] = pair<true>(8388608.f - __uint_as_float(__byte_perm(zv[i / 4], 0x4B000000u, 0x7650 + (i & 3))));
+                            } else {
+                                off[i] = __byte_perm(zv[i / 4], 0xE4E4E4E4u, 0x4040 + 0x0101 * (i & 3));
+                                off16[i] = add2<false>(off[i], 0x64406440u);        // + 1088
+                            }
                         }
                     }
                     __syncwarp();                   // read before a later stage's copy lands in the slot
@@ -308,16 +327,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
                             uint32_t a0, a1, a2, a3;
-                            codes<BF16, H>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], a0, a2);
-                            codes<BF16, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
+                            codes<BF16, ZERO, H>(wv[2 * i], off[ZERO ? 2 * i : 0], off16[ZERO ? 2 * i : 0], a0, a2);
+                            codes<BF16, ZERO, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
+                            for (int t = 0; t < NT; ++t) {
+                                if (ONE && u == 0 && H == 0) mma16816_first<BF16>(part[t][i], a0, a1, a2, a3, b[t][0], b[t][1]);
+                                else mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
+                            }
                         }
                     };
                     half(std::integral_constant<int, 0>{});
                     half(std::integral_constant<int, 1>{});
                 }
-                if (--left == 0 || sb + st + 1 == s1) {
+                if (ONE || --left == 0 || sb + st + 1 == s1) {
                     const uint32_t sv[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -327,7 +349,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], f);
-                                part[t][i][q] = part[t][i][q + 1] = 0.f;
+                                if (!ONE) part[t][i][q] = part[t][i][q + 1] = 0.f;
                             }
                         }
                     left = per_group;
@@ -381,10 +403,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
     if (splits > 1) cluster_sync();     // no block leaves while its sums are read
 }
 
-template <bool BF16, int NT, bool ZERO, int SS>
+template <bool BF16, int NT, bool ZERO, int SS, bool ONE>
 cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
     constexpr int kAlone = std::max(w4_smem<NT, SS>(), kAloneSmem);
-    auto kern = w4_kernel<BF16, NT, ZERO, SS>;
+    auto kern = w4_kernel<BF16, NT, ZERO, SS, ONE>;
     static std::atomic<unsigned char> smem_set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -415,8 +437,13 @@ cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
 
 template <bool BF16, int NT, bool ZERO>
 cudaError_t launch_s(const W4Args& a, int sm_count, cudaStream_t stream) {
-    if (NT == 1 && a.group % (4 * kStep) == 0) return launch_t<BF16, NT, ZERO, NT == 1 ? 4 : 2>(a, sm_count, stream);
-    return a.group % (2 * kStep) == 0 ? launch_t<BF16, NT, ZERO, 2>(a, sm_count, stream) : launch_t<BF16, NT, ZERO, 1>(a, sm_count, stream);
+    auto with = [&](auto steps) {
+        constexpr int SS = decltype(steps)::value;
+        return a.group == SS * kStep ? launch_t<BF16, NT, ZERO, SS, true>(a, sm_count, stream) : launch_t<BF16, NT, ZERO, SS, false>(a, sm_count, stream);
+    };
+    if constexpr (NT == 1)
+        if (a.group % (4 * kStep) == 0) return with(std::integral_constant<int, 4>{});
+    return a.group % (2 * kStep) == 0 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 1>{});
 }
 template <bool BF16>
 cudaError_t launch_b(const W4Args& a, int sm_count, cudaStream_t stream) {

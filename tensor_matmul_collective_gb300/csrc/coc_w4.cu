@@ -11,9 +11,9 @@
 // byte (4 m) are few, but taking codes out of words costs instructions: a
 // shift, a mask and an addition per pair, 88 of the 150 that a warp issues for
 // 2048 weights at up to 8 tokens (205 at 16), and their dependent sequences are
-// the bound: 3.3 TB/s of weights at n 8192, k 8 x 1024, m 8 (11.0 us), 3.4 at
-// n 14336, k 8 x 7168, m 16 with zero points (130 us); with nothing copied at
-// all the two take 9.6 and 109 us.
+// the bound: 3.4 TB/s of weights at n 8192, k 8 x 1024, m 8 (10.5 us), 3.4 at
+// n 14336, k 8 x 7168, m 16 with zero points (127 us); where they took
+// 11.0 and 130, copying nothing at all left 9.6 and 109.
 // W^T is the A operand of mma.sync (16 weight columns x 16 of k) and x^T the B
 // operand (8 tokens).  A word holds 8 codes along k of one column; a mask
 // takes two codes four apart into the halves of a register, so the pairs
@@ -171,7 +171,9 @@ __device__ __forceinline__ int part_begin(int all, int i, int ways) {
 
 // Block: 64 columns, 8 NT rows of x (blockIdx.y), kWarps ranges of the
 // contraction; cluster: blocks with the same columns and further ranges.  SS
-// steps make a stage (groups are whole stages; ONE: a group is one stage).
+// steps make a stage (groups are whole stages; ONE: a group is one stage, which
+// spares the bookkeeping of groups: groups of 32 at n 14336, m 16 take 130 us
+// with it and 179 without, of 128 in stages of 64 take 124).
 template <bool BF16, int NT, bool ZERO, int SS, bool ONE>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constant__ W4Args a) {
     constexpr int SB = stage_bytes<NT, SS>(), kStages = stages<SS>();
@@ -287,6 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                 load((st + kStages - 1) % kStages);
                 cp_wait<kStages - 1>();
                 const uint8_t* slot = ring_p + st * SB;
+                const bool first = fresh;           // of its group
                 if (ONE || fresh) {
                     fresh = false;
                     __syncwarp();                   // the lanes 4 g copied it for the others
@@ -322,8 +325,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                     }
                     const uint32_t wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
                     // all tiles once per half: products into one accumulator do not follow each other
-                    auto half = [&](auto hc) {
+                    auto half = [&](auto hc, auto onto_nothing) {
                         constexpr int H = decltype(hc)::value;
+                        constexpr bool FIRST = decltype(onto_nothing)::value;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {       // columns 2 i and 2 i + 1 of the lane's: rows g and g + 8 of the tile
                             uint32_t a0, a1, a2, a3;
@@ -331,13 +335,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                             codes<BF16, ZERO, H>(wv[2 * i + 1], off[ZERO ? 2 * i + 1 : 0], off16[ZERO ? 2 * i + 1 : 0], a1, a3);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                if (ONE && u == 0 && H == 0) mma16816_first<BF16>(part[t][i], a0, a1, a2, a3, b[t][0], b[t][1]);
+                                if (FIRST) mma16816_first<BF16>(part[t][i], a0, a1, a2, a3, b[t][0], b[t][1]);
                                 else mma16816<BF16>(part[t][i], a0, a1, a2, a3, b[t][2 * H], b[t][2 * H + 1]);
                             }
                         }
                     };
-                    half(std::integral_constant<int, 0>{});
-                    half(std::integral_constant<int, 1>{});
+                    using zeroth = std::integral_constant<int, 0>;
+                    if (u == 0 && (ONE || first)) half(zeroth{}, std::true_type{});
+                    else half(zeroth{}, std::false_type{});
+                    half(std::integral_constant<int, 1>{}, std::false_type{});
                 }
                 if (ONE || --left == 0 || sb + st + 1 == s1) {
                     const uint32_t sv[4] = {sc.x, sc.y, sc.z, sc.w};
@@ -347,10 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
                         for (int q = 0; q < 4; q += 2) {
                             const float f = to_float16bit<BF16>(static_cast<uint16_t>(q ? sv[i] >> 16 : sv[i]));
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], f);
-                                if (!ONE) part[t][i][q] = part[t][i][q + 1] = 0.f;
-                            }
+                            for (int t = 0; t < NT; ++t) fma2(acc[t][i][q], acc[t][i][q + 1], part[t][i][q], part[t][i][q + 1], f);
                         }
                     left = per_group;
                     fresh = true;

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
 }
 
 template <bool BF16, int NT, bool ZERO, int SS, bool ONE>
-cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
+cudaError_t launch_t(const W4Args& a, bool alone, cudaStream_t stream) {
     constexpr int kAlone = std::max(w4_smem<NT, SS>(), kAloneSmem);
     auto kern = w4_kernel<BF16, NT, ZERO, SS, ONE>;
     static std::atomic<unsigned char> smem_set[64];
@@ -422,7 +422,7 @@ cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.n + kCols - 1) / kCols * a.splits), static_cast<unsigned>((a.m + 8 * NT - 1) / (8 * NT)), 1);
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<long long>(cfg.gridDim.x) * cfg.gridDim.y <= sm_count ? kAlone : w4_smem<NT, SS>();
+    cfg.dynamicSmemBytes = alone ? kAlone : w4_smem<NT, SS>();
     cfg.stream = stream;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -439,46 +439,87 @@ cudaError_t launch_t(const W4Args& a, int sm_count, cudaStream_t stream) {
 }
 
 template <bool BF16, int NT, bool ZERO>
-cudaError_t launch_s(const W4Args& a, int sm_count, cudaStream_t stream) {
+cudaError_t launch_s(const W4Args& a, bool alone, cudaStream_t stream) {
     auto with = [&](auto steps) {
         constexpr int SS = decltype(steps)::value;
-        return a.group == SS * kStep ? launch_t<BF16, NT, ZERO, SS, true>(a, sm_count, stream) : launch_t<BF16, NT, ZERO, SS, false>(a, sm_count, stream);
+        return a.group == SS * kStep ? launch_t<BF16, NT, ZERO, SS, true>(a, alone, stream) : launch_t<BF16, NT, ZERO, SS, false>(a, alone, stream);
     };
     if constexpr (NT == 1)
         if (a.group % (4 * kStep) == 0) return with(std::integral_constant<int, 4>{});
     return a.group % (2 * kStep) == 0 ? with(std::integral_constant<int, 2>{}) : with(std::integral_constant<int, 1>{});
 }
 template <bool BF16>
-cudaError_t launch_b(const W4Args& a, int sm_count, cudaStream_t stream) {
+cudaError_t launch_b(const W4Args& a, bool alone, cudaStream_t stream) {
     const bool two = a.m > 8, zero = a.zero[0] != nullptr;
-    if (two) return zero ? launch_s<BF16, 2, true>(a, sm_count, stream) : launch_s<BF16, 2, false>(a, sm_count, stream);
-    return zero ? launch_s<BF16, 1, true>(a, sm_count, stream) : launch_s<BF16, 1, false>(a, sm_count, stream);
+    if (two) return zero ? launch_s<BF16, 2, true>(a, alone, stream) : launch_s<BF16, 2, false>(a, alone, stream);
+    return zero ? launch_s<BF16, 1, true>(a, alone, stream) : launch_s<BF16, 1, false>(a, alone, stream);
+}
+
+// Blocks that run at once in clusters of k, one on an SM: a cluster lies within
+// a part of the GPU whose SMs need not be a multiple of k (152 SMs hold 76, 36
+// and 15 clusters of 2, 4 and 8).
+cudaError_t alone_blocks(int k, int* out) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && (*out = known[dev][k].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    auto kern = w4_kernel<true, 1, false, 1, true>;     // any: the shared memory asked for decides
+    constexpr int kSmem = std::max(w4_smem<1, 1>(), kAloneSmem);
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(k);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(k), 1, 1);
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess) return e;
+    *out = n * k;
+    if (dev >= 0 && dev < 64) known[dev][k].store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 }  // namespace
 
 // Blocks of a cluster (ranges of the contraction) by the steps of the busiest
 // SM: 64-column slabs that do not divide evenly over the SMs are evened out by
-// halves and quarters, as far as joining them costs less (about 3 steps a
-// block and 2 a further range).  Two blocks on an SM are no faster than one
-// after the other: the SM's instruction rate is the bound.  Measured, ranges 1 /
-// 2 / 4: n 4096, k 4096, m 1 6.4 / 5.6 / 5.9 us; n 8192, k 8 x 1024, m 8 11.0 /
-// 14.0 / 20; n 14336, k 8 x 7168, m 16 159 / 130 / 152.
+// halves to eighths, as far as joining them costs less: about 3 steps a block,
+// and for a further range 1 where every block has an SM of its own and 14 where
+// clusters wait for SMs.  (Two blocks on an SM take 1.8 times as long as one.)
+// Measured, ranges 1 / 2 / 4 / 8: n 4096, k 4096, m 1 6.2 / 5.5 / 5.6 us; k 8 x
+// 1024, m 8 at n 2048 10.1 / 8.3 / 7.2, n 4096 10.2 / 8.4 / 9.4, n 8192 10.4 /
+// 12.4 / 17.6, n 10240 17.3 / 18.1 / 21.7, n 22528 25.9 / 28.6 / 39.6; n 704, k
+// 2 x 16256, m 6 35.1 / 20.7 / 12.6 / 9.5; n 1280, k 4 x 4672, m 12 29.7 / 19.0 /
+// 13.1 / 17.0; n 14336, k 8 x 7168, m 16 154 / 126 / 148.
 cudaError_t launch_w4(const W4Args& args, bool bf16, int sm_count, cudaStream_t stream) {
     W4Args a = args;
     const double steps = static_cast<double>(a.k / kStep) * a.R;
     const int rows = a.m > 8 ? 16 : 8;
     const long long tiles = static_cast<long long>((a.n + kCols - 1) / kCols) * ((a.m + rows - 1) / rows);
     double best = 1e300;
-    a.splits = 1;
-    for (int k : {1, 2, 4}) {
-        const double t = static_cast<double>((tiles * k + sm_count - 1) / sm_count) * (steps / (k * kWarps) + 3.0) + 2.0 * (k - 1);
+    bool alone = false;
+    for (int k : {1, 2, 4, 8}) {
+        int room = sm_count;
+        if (k > 1) {
+            const cudaError_t e = alone_blocks(k, &room);
+            if (e != cudaSuccess) return e;
+            if (room < k) continue;
+        }
+        const long long rounds = (tiles * k + room - 1) / room;
+        const double t = static_cast<double>(rounds) * (steps / (k * kWarps) + 3.0) + (rounds == 1 ? 1.0 : 14.0) * (k - 1);
         if (t < best) {
             best = t;
             a.splits = k;
+            alone = rounds == 1;
         }
     }
-    return bf16 ? launch_b<true>(a, sm_count, stream) : launch_b<false>(a, sm_count, stream);
+    return bf16 ? launch_b<true>(a, alone, stream) : launch_b<false>(a, alone, stream);
 }
 
 }  // namespace coc

@@ -150,3 +150,29 @@ def test_w4_nothing_is_written_around_the_outputs(m, n, ks):
     run(xs, codes, scales, zs, 32, outs=[buf[256:256 + m * n].view(m, n)])
     coc.sync_status()
     assert (buf[:256] == 7).all() and (buf[256 + m * n:] == 7).all()
+
+
+@pytest.mark.parametrize("m", [3, 16])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 96, 128, 192, 256, 384])
+def test_w4_group_sizes(group, zeros, m):
+    """Groups of one stage and of several, in both types; ranges that begin inside a group."""
+    for dt in (BF, HF):
+        ks = 768 if group != 256 else 1024
+        xs, codes, scales, zs = make(2, m, 136, ks, group, zeros, dt, seed=group + m)
+        outs = run(xs, codes, scales, zs, group)
+        coc.sync_status()
+        ref, size = reference(xs, codes, scales, zs, group)
+        check(outs, ref, size, group, 2 * ks, dt)
+
+
+@pytest.mark.parametrize("R,m,n,ks", [(1, 1, 64, 8192), (2, 6, 704, 6528), (1, 12, 512, 7168), (4, 2, 1152, 4096), (8, 8, 2432, 512), (1, 8, 10240, 512)])
+def test_w4_few_columns_and_many(R, m, n, ks):
+    """One to eight ranges of the contraction a slab; as many slabs as do not fit the SMs at once."""
+    xs, codes, scales, zs = make(R, m, n, ks, 64, True, BF, seed=n)
+    outs = run(xs, codes, scales, zs, 64)
+    coc.sync_status()
+    ref, size = reference(xs, codes, scales, zs, 64)
+    check(outs, ref, size, 64, R * ks, BF)
+    again = run(xs, codes, scales, zs, 64)
+    assert all(torch.equal(a, b) for a, b in zip(outs, again))

@@ -35,7 +35,7 @@
 // unnormalised parts, which a second kernel adds in order.
 //
 // Measured: 48 sequences of 1 to 8192 keys, 8 ranks of one key head with 8
-// query heads of 128: 75 us, 5.2 TB/s; two of 131071: 95 us, 5.6 TB/s.  With 16
+// query heads of 128: 74 us, 5.4 TB/s; two of 131071: 93 us, 5.8 TB/s.  With 16
 // query heads (16 rows a tile) 48 sequences of 4096 keys take 92 us, 4.4 TB/s:
 // the conversions and products of a byte, at two blocks an SM.
 #include <algorithm>

@@ -9,8 +9,8 @@
 //
 // What bounds it.  k n / 2 bytes of weights, read once: the operations per
 // byte (4 m) are few, but taking codes out of words costs instructions: a
-// shift, a mask and an addition per pair, 88 of the 150 that a warp issues for
-// 2048 weights at up to 8 tokens (205 at 16), and their dependent sequences are
+// shift, a mask and an addition per pair, 88 of the 139 that a warp issues for
+// 2048 weights at up to 8 tokens (197 at 16 with zero points), and their dependent sequences are
 // the bound: 3.4 TB/s of weights at n 8192, k 8 x 1024, m 8 (10.5 us), 3.4 at
 // n 14336, k 8 x 7168, m 16 with zero points (127 us); where they took
 // 11.0 and 130, copying nothing at all left 9.6 and 109.
@@ -32,7 +32,7 @@
 // Tried: codes as the A operand of tcgen05.mma in tensor memory, roles in 16
 // warps.  Writing operands, permuting x and waiting cost more instructions
 // (444 per 2048 weights at 16 tokens) than the registers' way: 221 us at
-// n 14336.
+// n 14336, when that took 150.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

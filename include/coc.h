@@ -576,7 +576,9 @@ coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, in
  *
  *   out = sum_j softmax_j(scale q.k_j) v_j     (k, v = code * scale of the page)
  *
- * in fp32 with one rounding at the end; a row that sees no key is zero.
+ * with scores, maxima and sums in fp32 and one rounding at the end (in the
+ * product with v a softmax weight keeps 11 bits for bf16 outputs, 22 for fp16);
+ * a row that sees no key is zero.
  * Positions that a row does not see take no part in it whatever they hold.
  *
  * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append
@@ -585,8 +587,8 @@ coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, in
  * Other arguments as coc_kv_cache_append.  Pages outside the cache, and
  * positions past the table, are left out, and coc_sync_status reports
  * COC_ERR_INVALID_ARG.  Results do not depend on what else is in the batch's
- * memory or on timing: splits of the keys go by the lengths and the GPU only
- * and are added in a fixed order.
+ * memory or on timing: splits of the keys go by the sizes, the lengths and the
+ * GPU only and are added in a fixed order.
  */
 coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t tokens, int64_t seqs, int q_heads,
                                     const void* const* q, const int64_t* q_strides, void* const* out,

@@ -1041,7 +1041,7 @@ cudaError_t kv_attention_plan(const KvAttnArgs& a, bool bf16, int sm_count, int*
     const long long tiles = table_tiles(a);
     long long resident = static_cast<long long>(n) * sm_count;
     resident = std::min<long long>(resident, kMaxGrid);
-    *grid = static_cast<int>(tiles >= resident ? resident : std::min(resident, items * tiles));
+    *grid = static_cast<int>(tiles >= resident ? resident : std::min(resident, items * (tiles + kItemCost)));
     *scratch = static_cast<size_t>(*grid) * (sizeof(Record) + 2 * rows * (padded_d(a.d) + 2) * sizeof(float));
     return cudaSuccess;
 }

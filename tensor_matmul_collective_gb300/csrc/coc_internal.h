@@ -227,6 +227,7 @@ struct KvAttnArgs {
     long long q_token, q_head, table_width, pages;
     float scale;
     int R, seqs, tokens, heads, q_heads, d, page, window, sinks;
+    int grid;                            // blocks of the attention kernel (set by launch_kv_attention)
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool bf16, cudaStream_t stream);
 cudaError_t kv_attention_plan(const KvAttnArgs& a, bool bf16, int sm_count, int* grid, size_t* scratch);

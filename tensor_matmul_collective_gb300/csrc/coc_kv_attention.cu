@@ -779,9 +779,13 @@ __device__ __forceinline__ uint16_t* out_at(const KvAttnArgs& a, const Record& r
 // asked for together with the maxima, before their weights are known.
 constexpr int kAtOnce = 8;          // parts whose values a thread has in flight
 
-// Block (b, row).  Group y of the threads adds the parts y, y + kMergeGroups,
-// ... in order, then the groups are added in order.
+// Block (x, row): the records from x kMergeSpan on, few of which are of an item
+// (a block for each would be four times the blocks, most of them for nothing:
+// 94.5 instead of 92.6 us for two sequences of 131071).  Group y of the threads
+// adds the parts y, y + kMergeGroups, ... in order, then the groups are added
+// in order.
 constexpr int kMergeGroups = 4;
+constexpr int kMergeSpan = 4;
 constexpr int kMaxGrid = 2048;      // blocks of the attention kernel
 
 template <bool BF16, int D, int ROWS>
@@ -792,76 +796,82 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
     __shared__ float2 sums[kMergeGroups][D / 2];
     grid_dependency_wait();
     const Record* recs = reinterpret_cast<const Record*>(a.scratch);
-    const Record rec = recs[blockIdx.x];
-    const int row = blockIdx.y, first = blockIdx.x, count = rec.last_block - first + 1;
-    if (row >= rec.rows) return;
-    const float* parts = reinterpret_cast<const float*>(recs + gridDim.x);
-    auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
-    const int y = threadIdx.x / (D / 2), x = threadIdx.x % (D / 2), p = 2 * x;
-    float2 v[kAtOnce];
-    auto fetch = [&](int i0) {
+    const int row = blockIdx.y, y = threadIdx.x / (D / 2), x = threadIdx.x % (D / 2), p = 2 * x;
+    const int lane = threadIdx.x & 31, at = blockIdx.x * kMergeSpan + lane;
+    const float* parts = reinterpret_cast<const float*>(recs + a.grid);
+    uint32_t open = __ballot_sync(0xffffffffu, lane < kMergeSpan && at < a.grid && recs[at].rows > row);
+    for (; open != 0; open &= open - 1) {
+        const int first = blockIdx.x * kMergeSpan + __ffs(open) - 1;
+        const Record rec = recs[first];
+        const int count = rec.last_block - first + 1;
+        auto part = [&](int i) { return parts + (2LL * (first + i) + (i == 0 ? 1 : 0)) * part_floats<D, ROWS>(); };
+        float2 v[kAtOnce];
+        auto fetch = [&](int i0) {
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int i = i0 + k * kMergeGroups;
-            v[k] = i < count ? *reinterpret_cast<const float2*>(part(i) + row * D + p) : make_float2(0.f, 0.f);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + k * kMergeGroups;
+                v[k] = i < count ? *reinterpret_cast<const float2*>(part(i) + row * D + p) : make_float2(0.f, 0.f);
+            }
+        };
+        fetch(y);
+        float M = kNoMax, l = 0.f;      // l: of part threadIdx.x
+        for (int i = threadIdx.x; i < count; i += T) {
+            M = fmaxf(M, weight[i] = part(i)[ROWS * D + row]);
+            if (i == threadIdx.x) l = part(i)[ROWS * D + ROWS + row];
         }
-    };
-    fetch(y);
-    float M = kNoMax, l = 0.f;      // l: of part threadIdx.x
-    for (int i = threadIdx.x; i < count; i += T) {
-        M = fmaxf(M, weight[i] = part(i)[ROWS * D + row]);
-        if (i == threadIdx.x) l = part(i)[ROWS * D + ROWS + row];
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = M;
-    __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = M;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < T / 32; ++i) M = fmaxf(M, red[0][i]);
-    float L = 0.f;
-    for (int i = threadIdx.x; i < count; i += T) {
-        const float f = exp2_fast(weight[i] - M);
-        weight[i] = f;
-        L = fmaf(i == threadIdx.x ? l : part(i)[ROWS * D + ROWS + row], f, L);
-    }
+        for (int i = 0; i < T / 32; ++i) M = fmaxf(M, red[0][i]);
+        float L = 0.f;
+        for (int i = threadIdx.x; i < count; i += T) {
+            const float f = exp2_fast(weight[i] - M);
+            weight[i] = f;
+            L = fmaf(i == threadIdx.x ? l : part(i)[ROWS * D + ROWS + row], f, L);
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = L;
-    __syncthreads();
-    float2 sum = make_float2(0.f, 0.f);
-    for (int i0 = y; i0 < count; i0 += kAtOnce * kMergeGroups) {
-        if (i0 != y) fetch(i0);
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if ((threadIdx.x & 31) == 0) red[1][threadIdx.x >> 5] = L;
+        __syncthreads();
+        float2 sum = make_float2(0.f, 0.f);
+        for (int i0 = y; i0 < count; i0 += kAtOnce * kMergeGroups) {
+            if (i0 != y) fetch(i0);
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int i = i0 + k * kMergeGroups;
-            if (i < count) {
-                sum.x = fmaf(v[k].x, weight[i], sum.x);
-                sum.y = fmaf(v[k].y, weight[i], sum.y);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + k * kMergeGroups;
+                if (i < count) {
+                    sum.x = fmaf(v[k].x, weight[i], sum.x);
+                    sum.y = fmaf(v[k].y, weight[i], sum.y);
+                }
             }
         }
-    }
-    sums[y][x] = sum;
-    __syncthreads();
-    if (y != 0) return;
+        sums[y][x] = sum;
+        __syncthreads();
+        if (y == 0) {
 #pragma unroll
-    for (int i = 1; i < kMergeGroups; ++i) {
-        sum.x += sums[i][x].x;
-        sum.y += sums[i][x].y;
-    }
-    L = 0.f;
+            for (int i = 1; i < kMergeGroups; ++i) {
+                sum.x += sums[i][x].x;
+                sum.y += sums[i][x].y;
+            }
+            L = 0.f;
 #pragma unroll
-    for (int i = 0; i < T / 32; ++i) L += red[1][i];
-    const int e = value_of<D>(p);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (e < a.d) *reinterpret_cast<uint32_t*>(out_at(a, rec, row) + e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
+            for (int i = 0; i < T / 32; ++i) L += red[1][i];
+            const int e = value_of<D>(p);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            if (e < a.d) *reinterpret_cast<uint32_t*>(out_at(a, rec, row) + e) = pack2<BF16>(__float_as_uint(sum.x * inv), __float_as_uint(sum.y * inv));
+        }
+        __syncthreads();    // the sums are read before the next item's
+    }
 }
 
 // The same with a warp a row and the parts one after another: block b, warp =
 // row; an eighth of the blocks and no barrier.  It is taken where the blocks
 // share few parts an item, fewer than kFewParts if every sequence has a row
-// tile: the whole call takes 75.4 instead of 79.8 us for 48 sequences of up to
-// 8192 keys on 8 ranks (1.2 blocks an item), but 95.3 instead of 94.1 for two
-// of 131071 (28 blocks an item).
+// tile: the whole call takes 73.5 instead of 80.6 us for 48 sequences of up to
+// 8192 keys on 8 ranks (1.2 blocks an item), but 94.0 instead of 91.8 for two
+// of 131071 (28 blocks an item), 51 instead of 22 for one on one rank.
 constexpr int kFewParts = 4;
 
 template <bool BF16, int D, int ROWS>
@@ -956,7 +966,9 @@ struct Launcher {
         *out = n;
         return cudaSuccess;
     }
-    static cudaError_t launch(const KvAttnArgs& a, int grid, cudaStream_t stream) {
+    static cudaError_t launch(const KvAttnArgs& args, int grid, cudaStream_t stream) {
+        KvAttnArgs a = args;
+        a.grid = grid;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -976,7 +988,7 @@ struct Launcher {
             cfg.blockDim = dim3(ROWS * 32, 1, 1);
             return cudaLaunchKernelEx(&cfg, kv_attention_merge_rows<BF16, D, ROWS>, a);
         }
-        cfg.gridDim = dim3(static_cast<unsigned>(grid), ROWS, 1);
+        cfg.gridDim = dim3(static_cast<unsigned>((grid + kMergeSpan - 1) / kMergeSpan), ROWS, 1);
         cfg.blockDim = dim3(kMergeGroups * D / 2, 1, 1);
         return cudaLaunchKernelEx(&cfg, kv_attention_merge<BF16, D, ROWS>, a);
     }

@@ -36,7 +36,7 @@
 //
 // Measured: 48 sequences of 1 to 8192 keys, 8 ranks of one key head with 8
 // query heads of 128: 74 us, 5.4 TB/s; two of 131071: 93 us, 5.8 TB/s.  With 16
-// query heads (16 rows a tile) 48 sequences of 4096 keys take 92 us, 4.4 TB/s:
+// query heads (16 rows a tile) 48 sequences of 4096 keys take 87 us, 4.6 TB/s:
 // the conversions and products of a byte, at two blocks an SM.
 #include <algorithm>
 #include <mutex>
@@ -995,27 +995,31 @@ struct Launcher {
 };
 
 // Query rows of a tile.  16 rows share one conversion of the codes, at two
-// blocks an SM instead of three for heads of 128 (no room for heads of 256):
-// worth it where the keys, not the items' beginnings and ends, take the time,
-// and tiles of 8 would read them for a quarter of the items again.  How many
-// tokens each sequence has is known on the device only: as many as the others
-// where they divide evenly, else so much on average that a quarter has more
-// than 8 rows.  8 ranks of one key head of 128, 8 against 16 rows: 48 sequences
-// of 4096 keys with 16 query heads 137 and 92 us, with 8 heads and 1 to 8
-// tokens 327 and 235, with 6 heads and 1 or 2 tokens 110 and 92, with 8 heads
-// and one token 75 and 92; 64 sequences of up to 512 keys (4096 tiles) with 8
-// heads and 1 or 2 tokens 27.3 and 30.5, of up to 2048 keys 52.7 and 49.7; 128
-// sequences of up to 256 keys with 16 heads 42.3 and 39.5.
-constexpr long long kManyTiles = 4096;
+// blocks an SM instead of three for heads of 128: worth it where the keys, not
+// the items' beginnings and ends, take the time, and tiles of 8 would read them
+// for a quarter of the items again.  How many tokens each sequence has is known
+// on the device only: as many as the others where they divide evenly, else so
+// much on average that a quarter has more than 8 rows (and the rest half empty
+// tiles: it takes more keys to pay).  8 ranks of one key head of 128, 8 against
+// 16 rows: 48 sequences of 4096 keys with 16 query heads 135 and 87 us, with 8
+// heads and 1 to 8 tokens 325 and 223, with 6 heads and 1 or 2 tokens 110 and
+// 87, with 8 heads and one token 73 and 86; 32 sequences of up to 512 keys (2048
+// tiles) with 16 heads 17.3 and 17.0, of up to 1024 23.8 and 20.7; 64 of up to
+// 1024 keys (8192 tiles) with 8 heads and 1 or 2 tokens 32.5 and 33.7, of up to
+// 2048 49.5 and 48.2.  Heads of 256 have no registers for more than 8 rows (with
+// Q in shared memory 300 and 300), and 32 rows leave no second buffer (heads of
+// 128: 224 and 272 with 1 to 8 tokens).
+constexpr long long kManyTiles = 2048, kManyRaggedTiles = 8192;
 
 long long table_tiles(const KvAttnArgs& a) { return std::max<long long>(1, (a.table_width * a.page + kTile - 1) / kTile); }
 
 int tile_rows(const KvAttnArgs& a) {
     const int group = a.q_heads / a.heads;
-    const long long tokens = a.tokens, seqs = a.seqs;
-    const bool many_rows = tokens % seqs == 0 ? tokens / seqs * group > 8 : 2 * tokens * group >= 15 * seqs && 4 * tokens >= 5 * seqs;
-    const bool many_tiles = table_tiles(a) >= kManyTiles || table_tiles(a) * a.seqs * a.R * a.heads >= kManyTiles;
-    return a.d <= 128 && many_rows && many_tiles ? 16 : 8;
+    const long long tokens = a.tokens, seqs = a.seqs, tiles = table_tiles(a);
+    const bool even = tokens % seqs == 0;
+    const bool many_rows = even ? tokens / seqs * group > 8 : 2 * tokens * group >= 15 * seqs && 4 * tokens >= 5 * seqs;
+    const long long many = even ? kManyTiles : kManyRaggedTiles;
+    return a.d <= 128 && many_rows && (tiles >= many || tiles * seqs * a.R * a.heads >= many) ? 16 : 8;
 }
 
 // Head sizes 64, 128 and 256 have instances of their own; the others take the

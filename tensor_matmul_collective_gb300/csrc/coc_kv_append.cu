@@ -19,7 +19,7 @@
 // values of four heads, whose cosines it loads once.
 //
 // Measured (8 ranks, 8 query heads and one key head of 128 each): 128 tokens,
-// one a sequence, 4.8 us; 7686 tokens of 7 prompts 61 us, 5.0 TB/s
+// one a sequence, 4.0 us; 7686 tokens of 7 prompts 59 us, 5.1 TB/s
 // (two blocks an SM instead of three: 73; two heads a thread: 61 to 69).
 #include "coc_kv.cuh"
 #include "coc_ptx.cuh"
@@ -188,16 +188,13 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int
     if (p0 < a.table_width) page_id = __ldg(a.table + static_cast<long long>(s) * a.table_width + p0);
     const int start = p0 * a.page;
     const int first = max(past, start), last = min(len, start + a.page);   // new positions in this page
-    if (page_id < 0 || page_id >= a.pages || (a.cos != nullptr && last > a.positions)) {
+    if (a.cos != nullptr && last > a.positions) {
         if (tid == 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
         return;
     }
     const bool rot = which == 0 && a.cos != nullptr;
     const uint16_t* src = (which ? a.v[r] : a.k[r]) + (begin + first - past) * (which ? a.v_token : a.k_token) + h * (which ? a.v_head : a.k_head);
     const long long stride = which ? a.v_token : a.k_token;
-    uint8_t* codes = (which ? a.cv[r] : a.ck[r]) + (static_cast<long long>(page_id) * a.heads + h) * a.page * a.d;
-    float* scale = (which ? a.sv[r] : a.sk[r]) + static_cast<long long>(page_id) * a.heads + h;
-    const float old = first > start ? *scale : 0.f;
     const int per_row = a.d / 16, tasks = (last - first) * per_row;
 
     auto values = [&](int i, float (&v)[16], Task& k, int& row) {
@@ -240,6 +237,14 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int
             amax = largest(v, amax);
         }
     }
+    // nothing so far has waited for the page's number
+    if (page_id < 0 || page_id >= a.pages) {
+        if (tid == 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
+        return;
+    }
+    uint8_t* codes = (which ? a.cv[r] : a.ck[r]) + (static_cast<long long>(page_id) * a.heads + h) * a.page * a.d;
+    float* scale = (which ? a.sv[r] : a.sk[r]) + static_cast<long long>(page_id) * a.heads + h;
+    const float old = first > start ? *scale : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if constexpr (TPU > 32) {
@@ -307,6 +312,15 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
     const int heads = min(kHeads, a.q_heads - g0);
     const uint16_t* x = a.q[r] + t * a.q_token + g0 * a.q_head;
     uint16_t* o = a.q_out[r] + (static_cast<long long>(t) * a.q_heads + g0) * a.d;
+    // the values first: they wait for nothing
+    Task k = task_of(a, task, a.cos != nullptr);
+    uint4 p0[kHeads], p1[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+        if (h < heads) {
+            p0[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e0));
+            p1[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e1));
+        }
     int s = t, pos = 0;
     bool rot = a.cos != nullptr;
     if (rot) {
@@ -326,14 +340,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
         rot = t >= b && t < e && pos >= 0 && pos < a.positions;
         if (pos >= a.positions) atomicOr(a.status, DEV_ERR_BAD_PAGE);
     }
-    const Task k = task_of(a, task, rot);
-    uint4 p0[kHeads], p1[kHeads];
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-        if (h < heads) {
-            p0[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e0));
-            p1[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e1));
-        }
+    if (!rot) k.turn = kCopy;       // the same pieces as they are
     Angles g;
     angles_of(a, k, pos, g);
 #pragma unroll

@@ -576,9 +576,10 @@ coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, in
  *
  *   out = sum_j softmax_j(scale q.k_j) v_j     (k, v = code * scale of the page)
  *
- * with scores, maxima and sums in fp32 and one rounding at the end (in the
- * product with v a softmax weight keeps 11 bits for bf16 outputs, 22 for fp16);
- * a row that sees no key is zero.
+ * with scores, maxima and sums in fp32 and one rounding at the end; in the
+ * product with v a softmax weight keeps 22 bits.  q enters its product as it
+ * is, but values of a bf16 row below 2^-29 of its largest lose bits.  A row
+ * that sees no key is zero.
  * Positions that a row does not see take no part in it whatever they hold.
  *
  * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append

@@ -25,8 +25,11 @@
 // on 8 ranks: the copies and their reads fill the memory pipe twice.)
 // Q is fp16 (exact for fp16; a bf16 row is scaled by a power of two to the top
 // of fp16's range first, so that it keeps its 8 bits down to 2^-29 of the
-// row's largest value).  Weights are rounded to fp16 (11 bits); with fp16
-// outputs a second product adds what that rounding left.
+// row's largest value).  A weight is two fp16 numbers, itself rounded to 11 bits
+// and what that left, and V is multiplied by both: 22 bits.  (One product with
+// 11 bits moved bf16 outputs by up to 2^-12 of sum p |v|, more than their own
+// rounding where values cancel; the second costs 0 to 1 us of a batch's 76 us,
+// 6 of 93 with 16 rows a tile.)
 //
 // Split.  The tiles of 64 keys of all (sequence, head, row tile) items form
 // one list, in which every item also counts kItemCost tiles for its beginning
@@ -602,12 +605,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                     const uint32_t plo = pack_half2(z[0], z[1]), phi = pack_half2(z[2], z[3]);
                     p0[n] = transposed(plo);
                     p1[n] = transposed(phi);
-                    if constexpr (!BF16) {
-                        const float2 rl = __half22float2(*reinterpret_cast<const __half2*>(&plo));
-                        const float2 rh2 = __half22float2(*reinterpret_cast<const __half2*>(&phi));
-                        e0[n] = transposed(pack_half2(z[0] - rl.x, z[1] - rl.y));
-                        e1[n] = transposed(pack_half2(z[2] - rh2.x, z[3] - rh2.y));
-                    }
+                    const float2 rl = __half22float2(*reinterpret_cast<const __half2*>(&plo));
+                    const float2 rh2 = __half22float2(*reinterpret_cast<const __half2*>(&phi));
+                    e0[n] = transposed(pack_half2(z[0] - rl.x, z[1] - rl.y));
+                    e1[n] = transposed(pack_half2(z[2] - rh2.x, z[3] - rh2.y));
                 }
                 // O^T += V^T P^T
                 if (!clean) {
@@ -661,10 +662,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                     for (int n = 0; n < NT; ++n) {
                         mma16816(acc[n][2 * i], fa, p0[n], p1[n]);
                         mma16816(acc[n][2 * i + 1], fb, p0[n], p1[n]);
-                        if constexpr (!BF16) {
-                            mma16816(acc[n][2 * i], fa, e0[n], e1[n]);
-                            mma16816(acc[n][2 * i + 1], fb, e0[n], e1[n]);
-                        }
+                        mma16816(acc[n][2 * i], fa, e0[n], e1[n]);
+                        mma16816(acc[n][2 * i + 1], fb, e0[n], e1[n]);
                     }
                 }
                 if (BUF == 1 && id >= 0) load_v(j, id, nxt);

@@ -1,6 +1,5 @@
 // Shared by the paged 8-bit key/value cache kernels (coc_kv_append.cu,
-// coc_kv_attention.cu): the cache as the kernels see it, the lookup of a new
-// token's sequence, and the scale rule.
+// coc_kv_attention.cu): conversions and the scale rule.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "coc_internal.h"
+#include "coc_kv_units.h"
 
 namespace coc {
 namespace {
@@ -37,19 +37,6 @@ __device__ __forceinline__ float scale_for(float amax) {
     const int e = static_cast<int>(b >> 23) - 127;
     const int s = e - ((b & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
     return __uint_as_float(static_cast<uint32_t>((s < kMinScaleExp ? kMinScaleExp : s) + 127) << 23);
-}
-
-// First and one-past-last new token of sequence s (cu NULL: one token each).
-// Offsets outside [0, tokens] or descending are clamped, so that no lookup
-// leaves the caller's buffers whatever the device array holds.
-__device__ __forceinline__ void seq_tokens(const int32_t* cu, int s, int tokens, int& begin, int& end) {
-    if (cu == nullptr) {
-        begin = s;
-        end = s + 1;
-        return;
-    }
-    begin = min(max(__ldg(cu + s), 0), tokens);
-    end = min(max(__ldg(cu + s + 1), begin), tokens);
 }
 
 }  // namespace

@@ -165,35 +165,17 @@ template <bool BF16, int TPU>
 __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int tid, float* red) {
     const int which = item & 1, r = (item >> 1) % a.R, rest = (item >> 1) / a.R;
     const int h = rest % a.heads, unit = rest / a.heads;
-    int s = unit, lo = 0;
-    if (a.cu != nullptr) {      // the last s whose first unit, cu[s] / page + 2 s, is <= unit
-        int hi = a.seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            int b, e;
-            seq_tokens(a.cu, mid, a.tokens, b, e);
-            if (b / a.page + 2 * mid <= unit) lo = mid;
-            else hi = mid;
-        }
-        s = lo;
-    }
-    int begin, end;
-    seq_tokens(a.cu, s, a.tokens, begin, end);
-    const int n = end - begin;
-    const int len = __ldg(a.lens + s);
-    const int past = len - n;
-    const int p0 = max(past, 0) / a.page + (a.cu != nullptr ? unit - (begin / a.page + 2 * s) : 0);   // this unit's page of the sequence
-    if (n <= 0 || len <= 0 || p0 > (len - 1) / a.page) return;
+    AppendUnit u;
+    if (!append_unit_of(a.cu, a.lens, a.seqs, a.tokens, a.page, unit, u)) return;
     int page_id = -1;
-    if (p0 < a.table_width) page_id = __ldg(a.table + static_cast<long long>(s) * a.table_width + p0);
-    const int start = p0 * a.page;
-    const int first = max(past, start), last = min(len, start + a.page);   // new positions in this page
+    if (u.page < a.table_width) page_id = __ldg(a.table + static_cast<long long>(u.s) * a.table_width + u.page);
+    const int start = u.start, first = u.first, last = u.last;
     if (a.cos != nullptr && last > a.positions) {
         if (tid == 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
         return;
     }
     const bool rot = which == 0 && a.cos != nullptr;
-    const uint16_t* src = (which ? a.v[r] : a.k[r]) + (begin + first - past) * (which ? a.v_token : a.k_token) + h * (which ? a.v_head : a.k_head);
+    const uint16_t* src = (which ? a.v[r] : a.k[r]) + (u.token + first) * (which ? a.v_token : a.k_token) + h * (which ? a.v_head : a.k_head);
     const long long stride = which ? a.v_token : a.k_token;
     const int per_row = a.d / 16, tasks = (last - first) * per_row;
 

@@ -637,8 +637,8 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
         raise TypeError("cache must be a KVCache")
     native = _native or _marshal()
     if native:
-        done = native[0].append(native[1], cache._ref, ks, vs, block_table, lens, cos, sin, qs, q_outs, cu_new, interleaved,
-                                None if stream is None else _stream(stream))
+        done = native[0].append(native[1], cache._ref, cache.device.index, ks, vs, block_table, lens, cos, sin, qs, q_outs, cu_new,
+                                interleaved, None if stream is None else _stream(stream))
         if done is not None:
             if done[0] != OK:
                 _check(done[0])
@@ -693,7 +693,7 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
         raise TypeError("cache must be a KVCache")
     native = _native or _marshal()
     if native:
-        done = native[0].attend(native[2], cache._ref, qs, block_table, lens, cu_new,
+        done = native[0].attend(native[2], cache._ref, cache.device.index, qs, block_table, lens, cu_new,
                                 cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks), outs,
                                 None if stream is None else _stream(stream))
         if done is not None:

@@ -56,8 +56,8 @@ struct Ranks {
 
 const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// The first tensor of a list, on the current CUDA device and of a 16-bit type.
-const at::Tensor* first_of(PyObject* o, int64_t* R) {
+// The first tensor of a list, on CUDA device `index` if that is the current one, and of a 16-bit type.
+const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index) {
     PyObject* x = nullptr;
     if (PyList_Check(o) && PyList_GET_SIZE(o) > 0) {
         *R = PyList_GET_SIZE(o);
@@ -67,7 +67,7 @@ const at::Tensor* first_of(PyObject* o, int64_t* R) {
         x = PyTuple_GET_ITEM(o, 0);
     }
     const at::Tensor* t = x != nullptr ? tensor_of(x) : nullptr;
-    if (t == nullptr || *R > COC_MAX_RANKS || !t->is_cuda() || t->device().index() != c10::cuda::current_device()) return nullptr;
+    if (t == nullptr || *R > COC_MAX_RANKS || !t->is_cuda() || t->device().index() != index || index != c10::cuda::current_device()) return nullptr;
     return t->scalar_type() == at::kHalf || t->scalar_type() == at::kBFloat16 ? t : nullptr;
 }
 
@@ -142,29 +142,31 @@ PyObject* result(coc_status_t st, PyObject* list) {
     return r;
 }
 
-// (entry point, cache, ks, vs, block_table, lens, cos, sin, qs, q_outs, cu_new, interleaved, stream)
+// (entry point, cache, its device's index, ks, vs, block_table, lens, cos, sin, qs, q_outs, cu_new, interleaved, stream)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 13) return none();
+    if (n != 14) return none();
     const auto fn = reinterpret_cast<decltype(&coc_kv_cache_append)>(PyLong_AsVoidPtr(a[0]));
     const auto* cache = static_cast<const coc_kv_cache_t*>(PyLong_AsVoidPtr(a[1]));
+    const int64_t index = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred()) return nullptr;
     if (fn == nullptr || cache == nullptr) return none();
     int64_t R = 0;
-    const at::Tensor* k0 = first_of(a[2], &R);
+    const at::Tensor* k0 = first_of(a[3], &R, index);
     if (k0 == nullptr || R != cache->R || k0->dim() != 3) return none();
     const int64_t T = k0->size(0), d = cache->head_dim;
     const at::ScalarType dt = k0->scalar_type();
     const at::Device dev = k0->device();
     Ranks k, v, q;
     int64_t hk, hv, hq = 0, ks[2], vs[2], qs[2] = {0, 0};
-    if (!k.take(a[2], R, dt, dev) || !k.heads(R, T, d, &hk, ks) || !v.take(a[3], R, dt, dev) || !v.heads(R, T, d, &hv, vs)) return none();
+    if (!k.take(a[3], R, dt, dev) || !k.heads(R, T, d, &hk, ks) || !v.take(a[4], R, dt, dev) || !v.heads(R, T, d, &hv, vs)) return none();
     if (hk != cache->kv_heads || hv != hk) return none();
     Index ix;
-    if (!ix.take(a[4], a[5], a[10], T, dev)) return none();
+    if (!ix.take(a[5], a[6], a[11], T, dev)) return none();
     const float *cos = nullptr, *sin = nullptr;
     int64_t positions = 0, rot = 0;
-    if (a[6] != Py_None || a[7] != Py_None) {
-        const at::Tensor *c = tensor_of(a[6]), *s = tensor_of(a[7]);
+    if (a[7] != Py_None || a[8] != Py_None) {
+        const at::Tensor *c = tensor_of(a[7]), *s = tensor_of(a[8]);
         if (c == nullptr || s == nullptr || c->dim() != 2 || c->sizes() != s->sizes()) return none();
         for (const at::Tensor* t : {c, s})
             if (t->scalar_type() != at::kFloat || t->device() != dev || !t->is_contiguous()) return none();
@@ -175,15 +177,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (rot > d) return none();
     }
     coc_stream_t stream;
-    if (!stream_of(a[12], &stream)) return nullptr;
-    const int interleaved = PyObject_IsTrue(a[11]);
+    if (!stream_of(a[13], &stream)) return nullptr;
+    const int interleaved = PyObject_IsTrue(a[12]);
     PyObject* list = nullptr;
     void* qo[COC_MAX_RANKS] = {};
-    if (a[8] != Py_None) {
-        if (!q.take(a[8], R, dt, dev) || !q.heads(R, T, d, &hq, qs)) return none();
-        if (!outputs(a[9], R, {T, hq, d}, *k0, &list, qo)) return PyErr_Occurred() ? nullptr : none();
+    if (a[9] != Py_None) {
+        if (!q.take(a[9], R, dt, dev) || !q.heads(R, T, d, &hq, qs)) return none();
+        if (!outputs(a[10], R, {T, hq, d}, *k0, &list, qo)) return PyErr_Occurred() ? nullptr : none();
     } else {
-        if (a[9] != Py_None) return none();
+        if (a[10] != Py_None) return none();
         list = none();
     }
     coc_status_t st;
@@ -195,30 +197,32 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (entry point, cache, qs, block_table, lens, cu_new, scale, window, sinks, outs, stream)
+// (entry point, cache, its device's index, qs, block_table, lens, cu_new, scale, window, sinks, outs, stream)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 11) return none();
+    if (n != 12) return none();
     const auto fn = reinterpret_cast<decltype(&coc_kv_cache_attention)>(PyLong_AsVoidPtr(a[0]));
     const auto* cache = static_cast<const coc_kv_cache_t*>(PyLong_AsVoidPtr(a[1]));
+    const int64_t index = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred()) return nullptr;
     if (fn == nullptr || cache == nullptr) return none();
     int64_t R = 0;
-    const at::Tensor* q0 = first_of(a[2], &R);
+    const at::Tensor* q0 = first_of(a[3], &R, index);
     if (q0 == nullptr || R != cache->R || q0->dim() != 3) return none();
     const int64_t T = q0->size(0), d = cache->head_dim;
     Ranks q;
     int64_t hq, qs[2];
-    if (!q.take(a[2], R, q0->scalar_type(), q0->device()) || !q.heads(R, T, d, &hq, qs)) return none();
+    if (!q.take(a[3], R, q0->scalar_type(), q0->device()) || !q.heads(R, T, d, &hq, qs)) return none();
     Index ix;
-    if (!ix.take(a[3], a[4], a[5], T, q0->device())) return none();
-    const double scale = PyFloat_AsDouble(a[6]);
-    const int64_t window = PyLong_AsLongLong(a[7]), sinks = PyLong_AsLongLong(a[8]);
+    if (!ix.take(a[4], a[5], a[6], T, q0->device())) return none();
+    const double scale = PyFloat_AsDouble(a[7]);
+    const int64_t window = PyLong_AsLongLong(a[8]), sinks = PyLong_AsLongLong(a[9]);
     if (PyErr_Occurred()) return nullptr;
     coc_stream_t stream;
-    if (!stream_of(a[10], &stream)) return nullptr;
+    if (!stream_of(a[11], &stream)) return nullptr;
     PyObject* list = nullptr;
     void* out[COC_MAX_RANKS];
-    if (!outputs(a[9], R, {T, hq, d}, *q0, &list, out)) return PyErr_Occurred() ? nullptr : none();
+    if (!outputs(a[10], R, {T, hq, d}, *q0, &list, out)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(cache, T, ix.seqs, static_cast<int>(hq), q.p, qs, out, ix.table, ix.width, ix.lens, ix.cu, static_cast<float>(scale), window,
@@ -235,7 +239,7 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto fn = reinterpret_cast<decltype(&coc_matmul_all_reduce_w4a16)>(PyLong_AsVoidPtr(a[0]));
     if (fn == nullptr) return none();
     int64_t R = 0;
-    const at::Tensor* x0 = first_of(a[1], &R);
+    const at::Tensor* x0 = first_of(a[1], &R, c10::cuda::current_device());
     const int64_t group = PyLong_AsLongLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
     if (x0 == nullptr || x0->dim() != 2 || group < 1) return none();

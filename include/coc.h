@@ -87,7 +87,12 @@
  *     their scratch as stream-ordered allocations from a device pool, which
  *     become memory nodes of the graph, so graph replays allocate nothing
  *     either.  coc_shutdown() frees all of it.  Calls on different streams
- *     use different workspaces and may overlap freely.
+ *     use different workspaces and may overlap freely.  Threads that call on
+ *     one stream take turns, a whole call at a time.  The per-thread default
+ *     stream has one workspace, which goes from thread to thread in stream
+ *     order.  A stream with the handle of a destroyed one takes over its
+ *     workspace in stream order; where the destroyed stream's last call was
+ *     cached attention, the new one's first call waits for the device.
  *     coc_matmul_all_reduce_noalloc takes none of this memory.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  Outputs must not alias inputs or each other.
@@ -671,7 +676,7 @@ coc_status_t coc_debug_clock_read(int slot, int64_t* cycles, int64_t* ns);
 
 /* Frees the per-device status buffers, the per-stream workspaces and the
  * graph-capture pool; forgets the allocation-free entry point's set-up.
- * Further calls re-create what they need. */
+ * Further calls re-create what they need.  No other call may run meanwhile. */
 coc_status_t coc_shutdown(void);
 
 #ifdef __cplusplus

@@ -39,17 +39,22 @@ std::atomic<long long> g_alloc_calls{0};   // device allocations made by the lib
 // Scratch owned by the library for the calls made on one stream: the
 // rank-split fp32 parts, the MoE routing tables, the w8A16 pre-pass weight.
 // Allocated at the first call on the stream that needs it and grown only when
-// a call needs more, so steady-state calls allocate nothing.  `last_use` is
-// recorded after every call that used it and waited on by the next one; short
-// calls leave both out (an event between two kernels costs them microseconds
-// and their programmatic launch) and go by the stream's id, which, unlike its
-// handle, is never given again: a workspace found under a handle that now is
-// another stream is taken over only when the device has finished.
+// a call needs more, so steady-state calls allocate nothing.  A call holds `mu`
+// from taking the scratch to its last launch: calls that two threads make on
+// one stream do not mix their launches.  `last_use` is recorded after a call
+// that used it and waited on by the next one, so that a stream handle that names
+// another stream by then (reused after cudaStreamDestroy, or the per-thread
+// default stream) never overlaps the earlier stream's kernels.  Short calls
+// leave both out (an event between two kernels costs them microseconds and
+// their programmatic launch) and go by the stream's id, which, unlike its handle,
+// is never given again.
 struct Workspace {
+    std::mutex mu;
     void* ptr = nullptr;
     size_t bytes = 0;
     cudaEvent_t last_use = nullptr;
-    unsigned long long stream_id = 0;
+    bool unmarked = false;              // the last call recorded no event: it was on stream `id`
+    unsigned long long id = ~0ull;
 };
 
 struct DeviceState {
@@ -309,6 +314,7 @@ struct Scratch {
     bool captured = false;
     bool by_stream = false;     // ordered by the stream alone: no event
     Workspace* w = nullptr;
+    std::unique_lock<std::mutex> held;      // w's
 };
 constexpr size_t kWorkspaceCap = size_t(4) << 30;   // largest scratch one call may take
 coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out, bool by_stream = false);
@@ -725,7 +731,6 @@ coc_status_t device_pool(DeviceState* ds, cudaMemPool_t* out) {
 
 coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes, Scratch* out, bool by_stream) {
     *out = Scratch{};
-    out->by_stream = by_stream;
     if (bytes == 0) return COC_OK;
     if (bytes > kWorkspaceCap)
         return fail(COC_ERR_SHAPE, "the call needs %zu bytes of scratch, above the %zu-byte cap", bytes, kWorkspaceCap);
@@ -743,21 +748,37 @@ coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes,
         out->captured = true;
         return COC_OK;
     }
-    std::lock_guard<std::mutex> lk(g_mu);
-    Workspace& w = ds->ws[stream];
+    // this handle is another stream in every thread: only events order its users
+    if (stream == cudaStreamPerThread) by_stream = false;
+    Workspace* found = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        found = &ds->ws[stream];
+    }
+    Workspace& w = *found;
+    std::unique_lock<std::mutex> held(w.mu);
     if (w.last_use == nullptr && (e = cudaEventCreateWithFlags(&w.last_use, cudaEventDisableTiming)) != cudaSuccess) {
         w.last_use = nullptr;
         return cuda_fail(e, "cudaEventCreateWithFlags (workspace)");
     }
-    unsigned long long id = 0;
-    if ((e = cudaStreamGetId(stream, &id)) != cudaSuccess) return cuda_fail(e, "cudaStreamGetId (workspace)");
-    if (w.ptr != nullptr && w.stream_id != id && (e = cudaDeviceSynchronize()) != cudaSuccess)
-        return cuda_fail(e, "cudaDeviceSynchronize (workspace of a stream that is gone)");
-    w.stream_id = id;
+    bool wait = !by_stream;             // for last_use
+    if (by_stream || w.unmarked) {
+        unsigned long long id = 0;
+        if ((e = cudaStreamGetId(stream, &id)) != cudaSuccess) return cuda_fail(e, "cudaStreamGetId (workspace)");
+        if (id != w.id) {
+            // the handle was another stream's; if that one's last call left no event, its end cannot be told from the device's
+            if (w.unmarked && (e = cudaDeviceSynchronize()) != cudaSuccess)
+                return cuda_fail(e, "cudaDeviceSynchronize (workspace of a stream that is gone)");
+            w.unmarked = false;
+            wait = true;
+        }
+        w.id = id;
+    }
     if (w.bytes < bytes) {
         // grow: the previous buffer is freed once every kernel that used it is done
         if (w.ptr != nullptr) {
-            if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize (workspace)");
+            e = w.unmarked ? cudaStreamSynchronize(stream) : cudaEventSynchronize(w.last_use);
+            if (e != cudaSuccess) return cuda_fail(e, "waiting for the workspace's last use");
             if ((e = cudaFree(w.ptr)) != cudaSuccess) return cuda_fail(e, "cudaFree (workspace)");
             w.ptr = nullptr;
             w.bytes = 0;
@@ -770,18 +791,20 @@ coc_status_t scratch_acquire(DeviceState* ds, cudaStream_t stream, size_t bytes,
         }
         w.bytes = want;
     }
-    // after the previous user of this workspace (this stream, or a destroyed
-    // stream whose handle this one reuses)
-    if (!by_stream && (e = cudaStreamWaitEvent(stream, w.last_use, 0)) != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent (workspace)");
+    // after the previous user of this workspace (this stream, or another that had its handle)
+    if (wait && (e = cudaStreamWaitEvent(stream, w.last_use, 0)) != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent (workspace)");
+    if (by_stream) w.unmarked = true;
     out->ptr = w.ptr;
+    out->by_stream = by_stream;
     out->w = &w;
+    out->held = std::move(held);
     return COC_OK;
 }
 
 coc_status_t scratch_release(cudaStream_t stream, Scratch& sc, coc_status_t st) {
     cudaError_t e = cudaSuccess;
     if (sc.captured && sc.ptr != nullptr) e = cudaFreeAsync(sc.ptr, stream);
-    else if (sc.w != nullptr && !sc.by_stream) e = cudaEventRecord(sc.w->last_use, stream);
+    else if (sc.w != nullptr && !sc.by_stream && (e = cudaEventRecord(sc.w->last_use, stream)) == cudaSuccess) sc.w->unmarked = false;
     sc = Scratch{};
     if (st == COC_OK && e != cudaSuccess) st = cuda_fail(e, "releasing the call's scratch");
     return st;

@@ -535,7 +535,9 @@ typedef struct {
  * Sequence s has the new tokens [cu_new[s], cu_new[s+1]) of `tokens` (cu_new
  * NULL: one each, token s) and holds lens[s] tokens with them, so its new
  * token i of n is at position p = lens[s] - n + i (p < 0: not appended, its q
- * is copied).
+ * is copied).  cu_new does not descend; it may begin above 0 and end below
+ * `tokens` (a part of a batch, a batch padded to a fixed size): the tokens
+ * outside belong to no sequence, are not appended, and their q is copied.
  *
  *   rotation     of the first rot_dim values of a head, pairs (a, b) = values
  *                (j, j + rot_dim/2), or (2j, 2j+1) if `interleaved`:
@@ -584,7 +586,7 @@ coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, in
  * with scores, maxima and sums in fp32 and one rounding at the end; in the
  * product with v a softmax weight keeps 22 bits.  q enters its product as it
  * is, but values of a bf16 row below 2^-29 of its largest lose bits.  A row
- * that sees no key is zero.
+ * that sees no key is zero, and so are the rows of tokens of no sequence.
  * Positions that a row does not see take no part in it whatever they hold.
  *
  * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append

@@ -629,7 +629,8 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
     strides free); qs[r]: tokens x q_heads x head_dim or None.  Sequence s has
     the new tokens cu_new[s] .. cu_new[s+1]-1 (cu_new None: one each) and
     lens[s] tokens in the cache with them; block_table[s, p // page_size] is
-    the page of its position p.  cos, sin: float32 positions x rot_dim/2, or
+    the page of its position p.  Tokens ahead of cu_new[0] and past its last
+    entry belong to no sequence: they are not appended, their q is copied.  cos, sin: float32 positions x rot_dim/2, or
     None for no rotation; interleaved pairs values 2j, 2j+1 instead of
     j, j + rot_dim/2.  Returns the rotated q of every rank (tokens x q_heads x
     head_dim), None without qs."""
@@ -688,7 +689,8 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
     kv_cache_append.  New token i of n sees the first E = lens[s] - (n-1-i)
     positions; with window > 0 only the last `window` of them and the first
     `sinks`.  scale defaults to head_dim ** -0.5.  Returns outs, one tokens x
-    q_heads x head_dim tensor per rank; a row that sees no key is zero."""
+    q_heads x head_dim tensor per rank; a row that sees no key, or whose token
+    belongs to no sequence, is zero."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     native = _native or _marshal()

@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
         }
         seq_tokens(a.cu, s, a.tokens, b, e);
         pos = __ldg(a.lens + s) - (e - t);
-        rot = t >= b && t < e && pos >= 0 && pos < a.positions;
-        if (pos >= a.positions) atomicOr(a.status, DEV_ERR_BAD_PAGE);
+        const bool owned = t >= b && t < e;     // else the token is no sequence's and has no position
+        rot = owned && pos >= 0 && pos < a.positions;
+        if (owned && pos >= a.positions) atomicOr(a.status, DEV_ERR_BAD_PAGE);
     }
     if (!rot) k.turn = kCopy;       // the same pieces as they are
     Angles g;

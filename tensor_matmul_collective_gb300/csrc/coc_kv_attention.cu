@@ -245,6 +245,25 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
     grid_dependency_wait();
     grid_dependents_launch();
 
+    // ---- rows of the new tokens that no sequence has, ahead of the first offset and past the last: zero
+    if (a.cu != nullptr) {
+        int first, last, unused;
+        seq_tokens(a.cu, 0, a.tokens, first, unused);
+        seq_tokens(a.cu, a.seqs - 1, a.tokens, unused, last);
+        const int spare = first + a.tokens - last;
+        if (spare > 0) {
+            const int pieces = a.d / 8;         // of 16 bytes, in a head
+            const long long each = static_cast<long long>(spare) * a.q_heads * pieces;
+            for (int r = 0; r < a.R; ++r)
+                for (long long i = blockIdx.x * static_cast<long long>(kWarps * 32) + threadIdx.x; i < each; i += static_cast<long long>(gridDim.x) * (kWarps * 32)) {
+                    const long long row = i / pieces, x = row / a.q_heads;
+                    const int token = static_cast<int>(x < first ? x : x - first + last);
+                    uint16_t* o = out_at(a, r, token, static_cast<int>(row - x * a.q_heads));
+                    *reinterpret_cast<uint4*>(o + (i - row * pieces) * 8) = make_uint4(0, 0, 0, 0);
+                }
+        }
+    }
+
     // ---- this block's run of units: each thread adds a contiguous range of
     // sequences; the scan of the threads' sums gives the total and the start
     const int per = (a.seqs + kWarps * 32 - 1) / (kWarps * 32);

@@ -234,8 +234,10 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TPU / 32; ++i) amax = fmaxf(amax, red[i]);
+    } else {
+        __syncwarp();       // the shuffles order no memory
     }
-    const float now = fmaxf(scale_for(amax), old);      // every thread has read the old scale by now
+    const float now = fmaxf(scale_for(amax), old);      // behind the barrier: every thread has read the old scale
     if (tid == 0) *scale = now;
     const float inv = __frcp_rn(now);
     if (first > start && now != old) {

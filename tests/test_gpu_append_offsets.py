@@ -42,3 +42,25 @@ def test_part_of_a_batch(R, hq, hkv, d, rot, page, news, past, a, b, dt):
                  [t[mine] for t in qkv], cos, sin, False, dt)
     for o, x in zip(out, dev):
         assert torch.equal(o[:cu[a]], x[0][:cu[a]]) and torch.equal(o[cu[b]:], x[0][cu[b]:])
+
+
+def test_every_lane_has_the_scale_from_before():
+    """A warp a unit, each new token far above what its page holds: all codes of the page shrink by the same factor, none by 1."""
+    page, d, hkv, seqs = 16, 256, 2, 200
+    g = torch.Generator().manual_seed(5)
+    lens = [2 + s % 15 for s in range(seqs)]
+    table, pages = kv.make_table(lens, page, gen=g)
+    rk, rv = kv.random_cache(1, pages, hkv, page, d, g), kv.random_cache(1, pages, hkv, page, d, g)
+    new = [(8.0 * torch.randn(seqs, hkv, d, generator=g)).to(BF)]
+    cache = to_cache(rk, rv)
+    coc.kv_cache_append([new[0].to(DEV)], [new[0].to(DEV)], cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV))
+    coc.sync_status()
+    for (codes0, scale0), codes1, scale1 in ((rk[0], cache.k[0], cache.k_scale[0]), (rv[0], cache.v[0], cache.v_scale[0])):
+        grown = 0
+        for s, n in enumerate(lens):
+            j = table[s, 0].item()
+            f = scale0[j].double() / scale1[j].cpu().double()
+            grown += int((f < 1).sum())
+            old = codes0[j, :, :n - 1].view(kv.E4M3).double() * f[:, None, None]
+            assert torch.equal(codes1[j, :, :n - 1].float().cpu().double(), kv.e4m3(old))
+        assert grown > seqs

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_kernel(const __grid_constan
         const int n0 = col0 + 4 * g < a.n ? 16 : 0, n1 = col0 + 32 + 4 * g < a.n ? 16 : 0;       // bytes copied: none past the columns
         const uint32_t ring = smem_u32(smem) + warp * kStages * SB;
         const uint8_t* ring_p = smem + warp * kStages * SB;
-        const uint32_t rows_w = 16u * static_cast<uint32_t>(a.n);       // bytes of a step's word rows
+        const size_t rows_w = size_t(16) * a.n;                         // bytes of a step's word rows
         // The 8 pieces of a word row stay together in shared memory (a copy writes a row at a time; scattered by lane, the
         // copies' writes alone took 73 cycles per 2048 weights), permuted so that the lanes' reads meet no bank twice.
         const uint32_t wslot = c * 128 + ((g ^ (2 * c)) << 4);

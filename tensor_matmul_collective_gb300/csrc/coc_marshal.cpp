@@ -56,8 +56,8 @@ struct Ranks {
 
 const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// The first tensor of a list, on CUDA device `index` if that is the current one, and of a 16-bit type.
-const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index) {
+// The first tensor of a list, on the current CUDA device, which is `index` where that is given, and of a 16-bit type.
+const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1) {
     PyObject* x = nullptr;
     if (PyList_Check(o) && PyList_GET_SIZE(o) > 0) {
         *R = PyList_GET_SIZE(o);
@@ -67,7 +67,8 @@ const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index) {
         x = PyTuple_GET_ITEM(o, 0);
     }
     const at::Tensor* t = x != nullptr ? tensor_of(x) : nullptr;
-    if (t == nullptr || *R > COC_MAX_RANKS || !t->is_cuda() || t->device().index() != index || index != c10::cuda::current_device()) return nullptr;
+    if (t == nullptr || *R > COC_MAX_RANKS || !t->is_cuda() || t->device().index() != c10::cuda::current_device()) return nullptr;
+    if (index >= 0 && t->device().index() != index) return nullptr;
     return t->scalar_type() == at::kHalf || t->scalar_type() == at::kBFloat16 ? t : nullptr;
 }
 
@@ -239,7 +240,7 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto fn = reinterpret_cast<decltype(&coc_matmul_all_reduce_w4a16)>(PyLong_AsVoidPtr(a[0]));
     if (fn == nullptr) return none();
     int64_t R = 0;
-    const at::Tensor* x0 = first_of(a[1], &R, c10::cuda::current_device());
+    const at::Tensor* x0 = first_of(a[1], &R);
     const int64_t group = PyLong_AsLongLong(a[4]);
     if (PyErr_Occurred()) return nullptr;
     if (x0 == nullptr || x0->dim() != 2 || group < 1) return none();

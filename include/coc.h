@@ -589,7 +589,8 @@ coc_status_t coc_kv_cache_append(const coc_kv_cache_t* cache, int64_t tokens, in
  * that sees no key is zero, and so are the rows of tokens of no sequence.
  * Positions that a row does not see take no part in it whatever they hold.
  *
- * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append
+ * q[r]    tokens x q_heads x head_dim in `dt`, strides as in the append;
+ *         tokens * q_heads / kv_heads <= 2^30
  * out[r]  tokens x q_heads x head_dim, packed
  * window  0: every earlier key; sinks needs a window.
  * Other arguments as coc_kv_cache_append.  Pages outside the cache, and

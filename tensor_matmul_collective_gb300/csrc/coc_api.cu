@@ -1666,6 +1666,9 @@ COC_API coc_status_t coc_kv_cache_attention(const coc_kv_cache_t* cache, int64_t
     if (st != COC_OK) return st;
     if (q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads != 0)
         return fail(COC_ERR_SHAPE, "q_heads = %d; must be a multiple of the %d key/value heads, up to 65535", q_heads, cache->kv_heads);
+    if (tokens * (q_heads / cache->kv_heads) > (int64_t(1) << 30))
+        return fail(COC_ERR_SHAPE, "%lld tokens of %d query heads a key head: at most 2^30 rows", (long long)tokens,
+                    q_heads / cache->kv_heads);
     if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
         return fail(COC_ERR_INVALID_ARG, "window = %lld, sinks = %lld: neither negative, sinks only with a window",
                     (long long)window, (long long)sinks);

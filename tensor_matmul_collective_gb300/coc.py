@@ -506,13 +506,23 @@ def moe_topk_grouped_matmul_combine(xs, idxs, gates, w, experts_per_rank: int, x
     return y_tok, y, xd, counts, offsets
 
 
+class _Held(list):
+    """Tensors whose addresses are stored elsewhere: a list that stays as it is."""
+
+    def _fixed(self, *args, **kwargs):
+        raise TypeError("a KVCache's tensors are fixed: make a KVCache of the others")
+    __setitem__ = __delitem__ = __iadd__ = __imul__ = _fixed
+    append = extend = insert = pop = remove = clear = sort = reverse = _fixed
+
+
 class KVCache:
     """The ranks' paged key/value caches in 8 bits, as kv_cache_append and kv_cache_attention take them.
 
     k[r], v[r]: (pages, kv_heads, page_size, head_dim) float8_e4m3fn codes;
     k_scale[r], v_scale[r]: (pages, kv_heads) float32, the value of a code is
     code * scale.  The tensors stay the caller's (``empty`` allocates them);
-    the object holds references and their addresses, checked once here."""
+    the object holds references and their addresses, checked once here: it
+    stays with these tensors, and they keep their memory (no resize_ or set_)."""
 
     def __init__(self, k, v, k_scale, v_scale):
         if not isinstance(k, (list, tuple)) or not 1 <= len(k) <= MAX_RANKS:
@@ -527,7 +537,7 @@ class KVCache:
         _check_list(v, "v", c.shape, torch.float8_e4m3fn, c.device)
         _check_list(k_scale, "k_scale", c.shape[:2], torch.float32, c.device)
         _check_list(v_scale, "v_scale", c.shape[:2], torch.float32, c.device)
-        self.k, self.v, self.k_scale, self.v_scale = list(k), list(v), list(k_scale), list(v_scale)
+        self._k, self._v, self._k_scale, self._v_scale = _Held(k), _Held(v), _Held(k_scale), _Held(v_scale)
         self.R, self.device = len(k), c.device
         self.pages, self.kv_heads, self.page_size, self.head_dim = c.shape
         d = _KVCacheDesc(R=self.R, page_size=self.page_size, kv_heads=self.kv_heads, head_dim=self.head_dim, pages=self.pages)
@@ -536,6 +546,11 @@ class KVCache:
                 getattr(d, field)[r] = t.data_ptr()
         self._desc = d
         self._ref = ctypes.addressof(d)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     @classmethod
     def empty(cls, R: int, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):

@@ -37,3 +37,23 @@ def test_cache_of_another_device_is_refused(monkeypatch, native):
     with pytest.raises(ValueError):
         coc.kv_cache_attention(x, cache, tb, ln)
     coc.sync_status()
+
+
+def test_cache_tensors_are_fixed():
+    """The addresses are stored: neither the lists nor their entries can be exchanged under them."""
+    cache, x, tb, ln = small()
+    for name in ("k", "v", "k_scale", "v_scale"):
+        ts = getattr(cache, name)
+        other = torch.empty_like(ts[0])
+        held = list(ts)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, [other, other])
+        for change in (lambda: ts.__setitem__(0, other), lambda: ts.__setitem__(slice(0, 1), [other]), lambda: ts.append(other),
+                       lambda: ts.pop(), lambda: ts.__delitem__(0), lambda: ts.reverse(), lambda: ts.extend([other]), lambda: ts.clear(),
+                       lambda: ts.insert(0, other), lambda: ts.__iadd__([other]), lambda: ts.__imul__(2), lambda: ts.remove(other)):
+            with pytest.raises(TypeError):
+                change()
+        assert len(getattr(cache, name)) == 2 and all(a is b for a, b in zip(getattr(cache, name), held))
+        assert [*held] + ts == held + held          # otherwise a list
+    coc.kv_cache_append(x, x, cache, tb, ln)
+    coc.sync_status()

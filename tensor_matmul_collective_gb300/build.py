@@ -24,6 +24,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-re
 
 MARSHAL_SRC = os.path.join(CSRC, "coc_marshal.cpp")
 MARSHAL = os.path.join(HERE, "_coc_marshal.so")
+MARSHAL_FOR = os.path.join(BUILD, "marshal_for.txt")      # what it was built against
 
 
 def _marshal_command():
@@ -37,6 +38,18 @@ def _marshal_command():
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
             *[f"-isystem{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), py, cuda)], MARSHAL_SRC, "-o", MARSHAL,
             f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
+def _marshal_target() -> str:
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version}"
+
+
+def _marshal_stale() -> bool:
+    if _stale(MARSHAL, [MARSHAL_SRC, os.path.join(CSRC, HEADERS[-1])]) or not os.path.exists(MARSHAL_FOR):
+        return True
+    with open(MARSHAL_FOR) as f:
+        return f.read() != _marshal_target()
 
 
 def nvcc() -> str:
@@ -57,7 +70,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, h) for h in HEADERS]
     objs, procs = [], []
-    marshal = _marshal_command() if force or _stale(MARSHAL, [MARSHAL_SRC, headers[-1]]) else None
+    marshal = _marshal_command() if force or _marshal_stale() else None
     if marshal is not None:
         marshal = (marshal, subprocess.Popen(marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT))
     for src in SOURCES:
@@ -84,6 +97,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         out, _ = marshal[1].communicate()
         if marshal[1].returncode != 0:
             raise RuntimeError(f"g++ failed: {' '.join(marshal[0])}\n{out.decode(errors='replace')}")
+        with open(MARSHAL_FOR, "w") as f:
+            f.write(_marshal_target())
     return LIB
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 from array import array
 
 import torch
@@ -132,15 +133,18 @@ _native = None
 
 
 def _marshal():
-    """_coc_marshal with the entry points' addresses, or False where it was not
-    built: then the checks below do its work, more slowly."""
+    """_coc_marshal with the entry points' addresses, or False (with a warning)
+    where it was not built or does not load: then the checks below do its work,
+    more slowly."""
     global _native
     if _native is None:
         L = lib()
         try:
             from . import _coc_marshal as m
-        except ImportError:
+        except ImportError as e:
             m = None
+            warnings.warn(f"_coc_marshal does not load ({e}): the decode-step calls take the slower checks in Python; build() makes it",
+                          RuntimeWarning, stacklevel=3)
         _native = False if m is None else (
             m, *(ctypes.cast(f, ctypes.c_void_p).value for f in (L.coc_kv_cache_append, L.coc_kv_cache_attention,
                                                                 L.coc_matmul_all_reduce_w4a16)))

@@ -83,11 +83,11 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor
         for (int64_t r = 0; r < R; ++r) p[r] = const_cast<void*>(o.p[r]);
         return *list != nullptr;
     }
-    *list = PyList_New(R);
-    if (*list == nullptr) return false;
+    // (what may throw comes before the list)
     const at::TensorOptions opt = at::TensorOptions().dtype(like.scalar_type()).device(like.device());
     if (R == 1) {
         at::Tensor t = at::empty(shape, opt);
+        if ((*list = PyList_New(1)) == nullptr) return false;
         p[0] = t.data_ptr();
         PyList_SET_ITEM(*list, 0, THPVariable_Wrap(std::move(t)));
         return true;
@@ -97,6 +97,7 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor
     int64_t n = 1;
     for (const int64_t x : shape) n *= x;
     const at::Tensor all = at::empty({R * n}, opt);
+    if ((*list = PyList_New(R)) == nullptr) return false;
     for (int64_t r = 0; r < R; ++r) {
         at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), all.dtype());
         t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
@@ -180,6 +181,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     coc_stream_t stream;
     if (!stream_of(a[13], &stream)) return nullptr;
     const int interleaved = PyObject_IsTrue(a[12]);
+    if (interleaved < 0) return nullptr;
     PyObject* list = nullptr;
     void* qo[COC_MAX_RANKS] = {};
     if (a[9] != Py_None) {

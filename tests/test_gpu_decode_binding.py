@@ -57,3 +57,12 @@ def test_cache_tensors_are_fixed():
         assert [*held] + ts == held + held          # otherwise a list
     coc.kv_cache_append(x, x, cache, tb, ln)
     coc.sync_status()
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_an_argument_without_a_truth_value_is_the_callers_error(monkeypatch, native):
+    plain(monkeypatch, native)
+    cache, x, tb, ln = small()
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        coc.kv_cache_append(x, x, cache, tb, ln, interleaved=torch.zeros(2))
+    coc.sync_status()

@@ -1753,8 +1753,6 @@ COC_API coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, in
     a.n = static_cast<int>(n);
     a.k = static_cast<int>(k_shard);
     a.group = static_cast<int>(group_size);
-    a.status = ds->status;
-    a.inject_timeout = g_inject.load();
     const cudaError_t e = launch_w4(a, dt == COC_BF16, ds->sm_count, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? COC_OK : cuda_fail(e, "w4A16 launch");
 }

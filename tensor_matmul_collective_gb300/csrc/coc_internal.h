@@ -242,9 +242,7 @@ struct W4Args {
     const int8_t* zero[COC_MAX_RANKS];   // NULL: 8 everywhere
     uint16_t* out[COC_MAX_RANKS];        // m x n
     int R, m, n, k, group;
-    unsigned* status;
     int splits;                          // blocks of a cluster (set by launch_w4)
-    int inject_timeout;
 };
 cudaError_t launch_w4(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 

@@ -12,20 +12,14 @@
 namespace coc {
 namespace {
 
-// Largest e4m3 value, and the least exponent a page's scale takes (an all-zero
-// page would otherwise have none; 2^-100 keeps code * scale a normal fp32).
-constexpr float kE4M3Max = 448.f;
+// The least exponent a page's scale takes (an all-zero page would otherwise
+// have none; 2^-100 keeps code * scale a normal fp32).
 constexpr int kMinScaleExp = -100;
 
 template <bool BF16>
 __device__ __forceinline__ float to_float16bit(uint16_t v) {
     if constexpr (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
     else return __half2float(__ushort_as_half(v));
-}
-template <bool BF16>
-__device__ __forceinline__ uint16_t from_float16bit(float f) {
-    if constexpr (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
-    else return __half_as_ushort(__float2half_rn(f));
 }
 
 // Least power of two s with amax <= 448 s, at least 2^kMinScaleExp.  amax =

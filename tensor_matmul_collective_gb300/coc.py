@@ -612,9 +612,9 @@ def _check_heads(ts, name, R, tokens, d, dtype, device):
 
 
 def _head_outs(outs, name, R, shape, dtype, device):
-    """R packed outputs, given or new, and their pointers."""
+    """R packed outputs, given or new (parts of one allocation, which costs the host a call instead of R), and their pointers."""
     if outs is None:
-        outs = [torch.empty(shape, dtype=dtype, device=device) for _ in range(R)]
+        outs = list(torch.empty((R, *shape), dtype=dtype, device=device).unbind(0))
     else:
         _check_list(outs, name, shape, dtype, device)
         if len(outs) != R:
@@ -652,7 +652,8 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
     entry belong to no sequence: they are not appended, their q is copied.  cos, sin: float32 positions x rot_dim/2, or
     None for no rotation; interleaved pairs values 2j, 2j+1 instead of
     j, j + rot_dim/2.  Returns the rotated q of every rank (tokens x q_heads x
-    head_dim), None without qs."""
+    head_dim), None without qs; new ones are parts of one allocation, which
+    lasts as long as any of them."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     native = _native or _marshal()
@@ -709,7 +710,7 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
     positions; with window > 0 only the last `window` of them and the first
     `sinks`.  scale defaults to head_dim ** -0.5.  Returns outs, one tokens x
     q_heads x head_dim tensor per rank; a row that sees no key, or whose token
-    belongs to no sequence, is zero."""
+    belongs to no sequence, is zero.  New outs are parts of one allocation."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     native = _native or _marshal()
@@ -745,7 +746,8 @@ def matmul_all_reduce_w4a16(xs, wqs, scales, group_size: int, zeros=None, outs=N
 
     xs[q]: m x k_shard (fp16/bf16); wqs[q]: (k_shard/8) x n int32, eight 4-bit
     codes along k in a word (w4_pack); scales[q]: (k_shard/group_size) x n in
-    the activations' type; zeros: None (z = 8) or int8 tensors like scales."""
+    the activations' type; zeros: None (z = 8) or int8 tensors like scales.  New
+    outs are parts of one allocation."""
     native = _native or _marshal()
     if native:
         done = native[0].w4(native[3], xs, wqs, scales, int(group_size), zeros, outs, None if stream is None else _stream(stream))

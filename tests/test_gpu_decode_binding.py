@@ -66,3 +66,19 @@ def test_an_argument_without_a_truth_value_is_the_callers_error(monkeypatch, nat
     with pytest.raises(RuntimeError, match="ambiguous"):
         coc.kv_cache_append(x, x, cache, tb, ln, interleaved=torch.zeros(2))
     coc.sync_status()
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_new_outputs_of_the_ranks_share_one_allocation(monkeypatch, native):
+    """As the calls' documentation says, whichever way the arguments are looked at."""
+    plain(monkeypatch, native)
+    cache, x, tb, ln = small()
+    turned = coc.kv_cache_append(x, x, cache, tb, ln, qs=x)
+    outs = coc.kv_cache_attention(x, cache, tb, ln)
+    w = coc.matmul_all_reduce_w4a16([t.view(3, 128) for t in x], [torch.zeros(16, 24, dtype=torch.int32, device=DEV)] * 2,
+                                    [torch.ones(2, 24, dtype=BF, device=DEV)] * 2, 64)
+    for ts in (turned, outs, w):
+        a, b = ts
+        assert a.untyped_storage().data_ptr() == b.untyped_storage().data_ptr()
+        assert b.data_ptr() - a.data_ptr() == a.numel() * 2 and a.is_contiguous() and b.is_contiguous()
+    coc.sync_status()

@@ -8,7 +8,11 @@
 // The page scale of V goes into the weight, w_j = 2^(z_j + log2 s_vj - m): it
 // then needs no multiplication of its own, and m, the running maximum, is
 // taken over z + log2 s_v, so that the products w c of all pages stay in the
-// range of a 16-bit type whatever the scales are.  The denominator adds w / s_v.
+// range of a 16-bit type whatever the scales are.  The denominator adds w / s_v;
+// where pages differ by more than 2^kFarScale that weight may be below fp32's
+// range while the key still counts (its values do not): 2^(z_j - m) is taken
+// instead.  A sum that moves to another maximum is scaled in two steps, by the
+// square root of a factor that may be below that range itself.
 //
 // What bounds it.  2 d bytes of codes per key and key head are read once for
 // up to 8 or 16 rows: 16 to 32 operations a byte, far below the tensor cores' rate,
@@ -63,6 +67,10 @@ constexpr int kItemCost = 3;
 // normal fp16 numbers down to 2^-23 of m.
 constexpr float kOffset = 9.f;
 constexpr float kSlack = 6.f;
+// Binary digits between a page's scale of V and the largest so far, up to which
+// w / s_v may be added: a key whose w is below 2^-126 there has less than 2^-70
+// of the weight of the key that the maximum stands for.
+constexpr float kFarScale = 60.f;
 
 // Shared memory: the warps' sums, joined at the end of an item.
 template <int D>
@@ -518,6 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
             qs1[n] = __shfl_sync(0xffffffffu, qscale, 8 * c + 4);
         }
 
+        float ev_top = -INFINITY;   // log2 of the largest scale of V so far
         for (int tb = t0; tb < tn; tb += BUF) {
 #pragma unroll
             for (int cur = 0; cur < BUF; ++cur) {
@@ -561,6 +570,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                 if (BUF == 1 && id >= 0) load_k(j, id, nxt);
                 const float ev = log2_fast(fmaxf(sv0, 1.2e-38f));
                 const float inv = exp2_fast(-ev);
+                ev_top = fmaxf(ev_top, ev);
+                const bool far = ev < ev_top - kFarScale;       // the same in all lanes
                 const bool clean = j0 >= clean_lo && j0 <= clean_hi;
                 uint32_t see[NT];                       // bit x: the row of sc[x] sees its key
                 uint32_t p0[NT], p1[NT], e0[NT], e1[NT];    // weights, and what their rounding left
@@ -603,11 +614,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                         }
                         n0 = kOffset - n0;
                         n1 = kOffset - n1;
-                        const float c0 = exp2_fast(n0 - b0[n]), c1 = exp2_fast(n1 - b1[n]);
+                        const float h0 = exp2_fast(0.5f * (n0 - b0[n])), h1 = exp2_fast(0.5f * (n1 - b1[n]));
+                        const float c0 = h0 * h0, c1 = h1 * h1;
                         b0[n] = n0;
                         b1[n] = n1;
-                        l0[n] *= c0;
-                        l1[n] *= c1;
+                        l0[n] = l0[n] * h0 * h0;
+                        l1[n] = l1[n] * h1 * h1;
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             acc[n][i][0] *= c0;
@@ -617,10 +629,16 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                         }
                         logs(ev + b0[n], ev + b1[n]);
                     }
+                    if (far) {
+                        l0[n] += exp2_fast(z[0] - ev) + exp2_fast(z[2] - ev);
+                        l1[n] += exp2_fast(z[1] - ev) + exp2_fast(z[3] - ev);
+                    }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) z[x] = exp2_fast(z[x]);
-                    l0[n] = fmaf(z[0] + z[2], inv, l0[n]);
-                    l1[n] = fmaf(z[1] + z[3], inv, l1[n]);
+                    if (!far) {
+                        l0[n] = fmaf(z[0] + z[2], inv, l0[n]);
+                        l1[n] = fmaf(z[1] + z[3], inv, l1[n]);
+                    }
                     const uint32_t plo = pack_half2(z[0], z[1]), phi = pack_half2(z[2], z[3]);
                     p0[n] = transposed(plo);
                     p1[n] = transposed(phi);
@@ -730,7 +748,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
 #pragma unroll
             for (int i = 1; i < kWarps; ++i) M = fmaxf(M, wm[i][row]);
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) L += wl[i][row] * exp2_fast(wm[i][row] - M);
+            for (int i = 0; i < kWarps; ++i) {
+                const float h = exp2_fast(0.5f * (wm[i][row] - M));
+                L += wl[i][row] * h * h;
+            }
             ending.max[row] = M;
             ending.sum[row] = L;
             ending.inv[row] = L == 0.f ? 0.f : 1.f / L;
@@ -845,9 +866,9 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
         for (int i = 0; i < T / 32; ++i) M = fmaxf(M, red[0][i]);
         float L = 0.f;
         for (int i = threadIdx.x; i < count; i += T) {
-            const float f = exp2_fast(weight[i] - M);
-            weight[i] = f;
-            L = fmaf(i == threadIdx.x ? l : part(i)[ROWS * D + ROWS + row], f, L);
+            const float h = exp2_fast(0.5f * (weight[i] - M));
+            weight[i] = h * h;
+            L = fmaf((i == threadIdx.x ? l : part(i)[ROWS * D + ROWS + row]) * h, h, L);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -933,8 +954,9 @@ __global__ void __launch_bounds__(ROWS * 32) kv_attention_merge_rows(const __gri
                 m = part(i0 + lane)[ROWS * D + row];
                 l = part(i0 + lane)[ROWS * D + ROWS + row];
             }
-            f = i0 + lane < count ? exp2_fast(m - M) : 0.f;
-            L = fmaf(l, f, L);
+            const float h = i0 + lane < count ? exp2_fast(0.5f * (m - M)) : 0.f;
+            f = h * h;
+            L = fmaf(l * h, h, L);
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {

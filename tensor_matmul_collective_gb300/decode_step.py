@@ -4,9 +4,10 @@ sequence-parallel input), append to the 8-bit key/value cache with the position
 rotation, attention over the cache, and the output projection with 4-bit
 weights (w4A16 MATMUL_ALL_REDUCE).
 
-``python -m tensor_matmul_collective_gb300.decode_step`` runs prompts and then
-a number of single-token steps of one layer with random weights and prints the
-time of a step (``--ranks 8 --hidden 8192 --heads 64 --kv-heads 8 --batch 64``
+``python -m tensor_matmul_collective_gb300.decode_step`` appends the keys and
+values of prompts to the cache (their own attention is not part of it) and then
+runs a number of single-token steps of one layer with random weights and prints
+the time of a step (``--ranks 8 --hidden 8192 --heads 64 --kv-heads 8 --batch 64``
 by default; the step is captured into a CUDA graph).
 """
 from __future__ import annotations
@@ -92,7 +93,7 @@ def main() -> None:
     block = random_block(R, a.hidden, a.heads, a.kv_heads, a.head_dim, B * per_seq, a.page, a.prompt + a.steps + 1)
     table = torch.randperm(B * per_seq, device=dev).to(torch.int32).view(B, per_seq).contiguous()
     lens = torch.full((B,), a.prompt, dtype=torch.int32, device=dev)
-    # prompts: all tokens of every sequence in one call
+    # prompts: keys and values of all tokens of every sequence in one call
     tokens = B * a.prompt
     xs = [torch.randn(tokens // R, a.hidden, device=dev).to(torch.bfloat16) for _ in range(R)]
     cu = torch.arange(0, tokens + 1, a.prompt, dtype=torch.int32, device=dev)

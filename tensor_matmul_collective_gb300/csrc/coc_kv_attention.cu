@@ -37,14 +37,15 @@
 //
 // Split.  The tiles of 64 keys of all (sequence, head, row tile) items form
 // one list, in which every item also counts kItemCost tiles for its beginning
-// and end, cut into equal contiguous runs, one per resident block: lengths may
-// be as unlike as they are, no SM idles.  An item that spans blocks leaves
+// and end, cut into equal contiguous runs, one per resident block: whatever the
+// lengths, no SM idles in this kernel.  An item that spans blocks leaves
 // unnormalised parts, which a second kernel adds in order.
 //
 // Measured: 48 sequences of 1 to 8192 keys, 8 ranks of one key head with 8
-// query heads of 128: 74 us, 5.4 TB/s; two of 131071: 93 us, 5.8 TB/s.  With 16
-// query heads (16 rows a tile) 48 sequences of 4096 keys take 87 us, 4.6 TB/s:
-// the conversions and products of a byte, at two blocks an SM.
+// query heads of 128: 73 to 79 us by their lengths, 5.1 to 5.4 TB/s; two of
+// 131071: 93 us, 5.8 TB/s.  With 16 query heads (16 rows a tile) 48 sequences of
+// 4096 keys take 94 us, 4.3 TB/s: the conversions and products of a byte, at
+// two blocks an SM.  24 of 4096 keys with 8 query heads of 256: 80 us, 5.1 TB/s.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -908,9 +909,12 @@ __global__ void __launch_bounds__(kMergeGroups * D / 2) kv_attention_merge(const
 // The same with a warp a row and the parts one after another: block b, warp =
 // row; an eighth of the blocks and no barrier.  It is taken where the blocks
 // share few parts an item, fewer than kFewParts if every sequence has a row
-// tile: the whole call takes 73.5 instead of 80.6 us for 48 sequences of up to
-// 8192 keys on 8 ranks (1.2 blocks an item), but 94.0 instead of 91.8 for two
-// of 131071 (28 blocks an item), 51 instead of 22 for one on one rank.
+// tile: the whole call takes 75.7 instead of 82.7 us for 48 sequences of up to
+// 8192 keys on 8 ranks (1.2 blocks an item), but 95.6 instead of 93.5 for two
+// of 131071 (28 blocks an item), 51 instead of 22 for one on one rank.  The rule
+// knows the sizes, not the lengths: of 128 sequences on one rank one of 131072
+// keys beside 127 of 16 takes 45 us, a warp a row adding its hundreds of parts,
+// where that one alone takes 21.
 constexpr int kFewParts = 4;
 
 template <bool BF16, int D, int ROWS>
@@ -1041,15 +1045,15 @@ struct Launcher {
 // on the device only: as many as the others where they divide evenly, else so
 // much on average that a quarter has more than 8 rows (and the rest half empty
 // tiles: it takes more keys to pay).  8 ranks of one key head of 128, 8 against
-// 16 rows: 48 sequences of 4096 keys with 16 query heads 135 and 87 us, with 8
-// heads and 1 to 8 tokens 325 and 223, with 6 heads and 1 or 2 tokens 110 and
-// 87, with 8 heads and one token 73 and 86; 32 sequences of up to 512 keys (2048
-// tiles) with 16 heads 17.3 and 17.0, of up to 1024 23.8 and 20.7; 64 of up to
-// 1024 keys (8192 tiles) with 8 heads and 1 or 2 tokens 32.5 and 33.7, of up to
-// 2048 49.5 and 48.2.  Heads of 256 have no registers for more than 8 rows (with
+// 16 rows: 48 sequences of 4096 keys with 16 query heads 138 and 94 us, with 8
+// heads and 1 to 8 tokens 330 and 243, with 6 heads and 1 or 2 tokens 111 and
+// 94, with 8 heads and one token 75 and 93; 32 sequences of up to 512 keys (2048
+// tiles) with 16 heads 18.0 and 18.1, of up to 1024 23.6 and 22.1; 64 of up to
+// 1024 keys (8192 tiles) with 8 heads and 1 or 2 tokens 33.3 and 36.4, of up to
+// 2048 51.3 and 51.5.  Heads of 256 have no registers for more than 8 rows (with
 // Q in shared memory 300 and 300), and 32 rows leave no second buffer (heads of
 // 128: 224 and 272 with 1 to 8 tokens).
-constexpr long long kManyTiles = 2048, kManyRaggedTiles = 8192;
+constexpr long long kManyTiles = 2048, kManyRaggedTiles = 12288;
 
 long long table_tiles(const KvAttnArgs& a) { return std::max<long long>(1, (a.table_width * a.page + kTile - 1) / kTile); }
 

@@ -22,6 +22,23 @@ __device__ __forceinline__ float to_float16bit(uint16_t v) {
     else return __half2float(__ushort_as_half(v));
 }
 
+// Loads of what an earlier kernel on the stream may have written (see load_index).
+__device__ __forceinline__ float load_float(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 load_float4(const float* p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 load_uint4(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // Least power of two s with amax <= 448 s, at least 2^kMinScaleExp.  amax =
 // 1.f x 2^e gives 2^(e - 8) for 1.f <= 1.75 (448 = 1.75 x 2^8), else 2^(e - 7).
 // A power of two makes x / s and a later change of scale exact up to e4m3's

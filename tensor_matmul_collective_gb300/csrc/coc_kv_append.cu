@@ -42,8 +42,8 @@ __device__ __noinline__ float rotated(const KvAppendArgs& a, const uint16_t* x, 
     const bool first = a.interleaved ? (e & 1) == 0 : e < half;
     const int pe = a.interleaved ? (e ^ 1) : (first ? e + half : e - half);
     const float w = to_float16bit<BF16>(x[pe]);
-    const float c = __ldg(a.cos + static_cast<long long>(pos) * half + j);
-    const float s = __ldg(a.sin + static_cast<long long>(pos) * half + j);
+    const float c = load_float(a.cos + static_cast<long long>(pos) * half + j);
+    const float s = load_float(a.sin + static_cast<long long>(pos) * half + j);
     return first ? __fsub_rn(__fmul_rn(v, c), __fmul_rn(w, s)) : __fadd_rn(__fmul_rn(v, c), __fmul_rn(w, s));
 }
 
@@ -91,11 +91,11 @@ struct Angles {
 };
 __device__ __forceinline__ void load4(const float* p, float* f, bool vec) {
     if (vec) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 v = load_float4(p);
         f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __ldg(p + i);
+        for (int i = 0; i < 4; ++i) f[i] = load_float(p + i);
     }
 }
 __device__ __forceinline__ void angles_of(const KvAppendArgs& a, const Task& k, int pos, Angles& g) {
@@ -168,7 +168,7 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int
     AppendUnit u;
     if (!append_unit_of(a.cu, a.lens, a.seqs, a.tokens, a.page, unit, u)) return;
     int page_id = -1;
-    if (u.page < a.table_width) page_id = __ldg(a.table + static_cast<long long>(u.s) * a.table_width + u.page);
+    if (u.page < a.table_width) page_id = load_index(a.table + static_cast<long long>(u.s) * a.table_width + u.page);
     const int start = u.start, first = u.first, last = u.last;
     if (a.cos != nullptr && last > a.positions) {
         if (tid == 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
@@ -183,7 +183,7 @@ __device__ __forceinline__ void append_unit(const KvAppendArgs& a, int item, int
         row = i / per_row;
         k = task_of(a, i - row * per_row, rot);
         const uint16_t* x = src + row * stride;
-        const uint4 p0v = __ldg(reinterpret_cast<const uint4*>(x + k.e0)), p1v = __ldg(reinterpret_cast<const uint4*>(x + k.e1));
+        const uint4 p0v = load_uint4(x + k.e0), p1v = load_uint4(x + k.e1);
         Angles g;
         angles_of(a, k, first + row, g);
         turned<BF16>(a, x, p0v, p1v, k, g, first + row, v);
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
 #pragma unroll
     for (int h = 0; h < kHeads; ++h)
         if (h < heads) {
-            p0[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e0));
-            p1[h] = __ldg(reinterpret_cast<const uint4*>(x + h * a.q_head + k.e1));
+            p0[h] = load_uint4(x + h * a.q_head + k.e0);
+            p1[h] = load_uint4(x + h * a.q_head + k.e1);
         }
     int s = t, pos = 0;
     bool rot = a.cos != nullptr;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const __grid_con
             s = lo;
         }
         seq_tokens(a.cu, s, a.tokens, b, e);
-        pos = __ldg(a.lens + s) - (e - t);
+        pos = load_index(a.lens + s) - (e - t);
         const bool owned = t >= b && t < e;     // else the token is no sequence's and has no position
         rot = owned && pos >= 0 && pos < a.positions;
         if (owned && pos >= a.positions) atomicOr(a.status, DEV_ERR_BAD_PAGE);

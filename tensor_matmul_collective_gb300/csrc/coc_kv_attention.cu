@@ -106,12 +106,12 @@ __device__ __forceinline__ uint16_t* out_at(const KvAttnArgs& a, int rank, int t
 // Codes are read once by one lane: no place in L1.
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint2 load8(const uint8_t* p) {
     uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
 
@@ -119,7 +119,7 @@ __device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool in) {
     uint4 v;
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
         : "l"(p), "r"(static_cast<int>(in)));
     return v;
@@ -128,7 +128,7 @@ __device__ __forceinline__ uint2 load8_if(const uint8_t* p, bool in) {
     uint2 v;
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+        "@p ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
         : "=&r"(v.x), "=&r"(v.y)
         : "l"(p), "r"(static_cast<int>(in)));
     return v;
@@ -185,7 +185,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttnArgs& a, int s) {
     int end;
     seq_tokens(a.cu, s, a.tokens, w.begin, end);
     w.n = end - w.begin;
-    w.len = max(0, __ldg(a.lens + s));
+    w.len = max(0, load_index(a.lens + s));
     const long long room = a.table_width * a.page;
     if (w.len > room && w.n > 0) atomicOr(a.status, DEV_ERR_BAD_PAGE);
     const int group = a.q_heads / a.heads;
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
             if (place == skip_at) place += skip;
         };
         // Nothing looks at an entry before the next step, so that the load's latency is not waited for.
-        auto entry_here = [&]() { return ahead < tn && place < end_max ? __ldg(table + (place >> page_shift)) : -1; };
+        auto entry_here = [&]() { return ahead < tn && place < end_max ? load_index(table + (place >> page_shift)) : -1; };
         // Entries outside the cache are left out, and reported where a row sees a key of the chunk.
         auto checked = [&](int id, int j, bool in) {
             if (static_cast<uint32_t>(id) >= pages) {
@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
         int id = checked(entry0, j, t0 < tn);   // this chunk's page
         float sk = 0.f, sv = 0.f;
         if (id >= 0) {
-            sk = __ldg(sk_head + static_cast<long long>(id) * a.heads);
-            sv = __ldg(sv_head + static_cast<long long>(id) * a.heads);
+            sk = load_float(sk_head + static_cast<long long>(id) * a.heads);
+            sv = load_float(sv_head + static_cast<long long>(id) * a.heads);
             load_k(j, id, 0);
             load_v(j, id, 0);
         }
@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm<D, ROWS>()) kv_atte
                 j1 = place;
                 entry = entry_here();
                 if (id >= 0) {
-                    sk = __ldg(sk_head + static_cast<long long>(id) * a.heads);
-                    sv = __ldg(sv_head + static_cast<long long>(id) * a.heads);
+                    sk = load_float(sk_head + static_cast<long long>(id) * a.heads);
+                    sv = load_float(sv_head + static_cast<long long>(id) * a.heads);
                     if (BUF == 2) {
                         load_k(j, id, nxt);
                         load_v(j, id, nxt);

@@ -14,9 +14,14 @@
 namespace coc {
 namespace {
 
+// (On the device not by __ldg: these kernels begin while the one that writes the
+// array may still run, and a load from memory that is said to be read-only need
+// not stay behind the wait for it.)
 COC_HD int load_index(const int32_t* p) {
 #ifdef __CUDA_ARCH__
-    return __ldg(p);
+    int v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
 #else
     return *p;
 #endif

@@ -611,10 +611,26 @@ def _check_heads(ts, name, R, tokens, d, dtype, device):
     return shape[1], [stride[0], stride[1]], ptrs
 
 
-def _head_outs(outs, name, R, shape, dtype, device):
-    """R packed outputs, given or new (parts of one allocation, which costs the host a call instead of R), and their pointers."""
+def _as_stream(stream):
+    """A torch stream of what the calls take as `stream`: one already, or a handle."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _head_outs(outs, name, R, shape, dtype, device, stream):
+    """R packed outputs, given or new (parts of one allocation, which costs the host a call instead of R), and their pointers.
+
+    New ones of a call on another than the current stream are that stream's
+    memory (what the current stream has freed may still be in use there), and
+    the current stream, on which the caller goes on with them, is noted as a user."""
     if outs is None:
-        outs = list(torch.empty((R, *shape), dtype=dtype, device=device).unbind(0))
+        now = torch.cuda.current_stream()
+        if stream is None or _stream(stream) == now.cuda_stream:
+            new = torch.empty((R, *shape), dtype=dtype, device=device)
+        else:
+            with torch.cuda.stream(_as_stream(stream)):
+                new = torch.empty((R, *shape), dtype=dtype, device=device)
+            new.record_stream(now)
+        outs = list(new.unbind(0))
     else:
         _check_list(outs, name, shape, dtype, device)
         if len(outs) != R:
@@ -679,7 +695,7 @@ def kv_cache_append(ks, vs, cache, block_table, lens, cos=None, sin=None, qs=Non
     hq, qstr, qp, qop = 0, [], [], []
     if qs is not None:
         hq, qstr, qp = _check_heads(qs, "qs", R, T, d, dt, dev)
-        q_outs, qop = _head_outs(q_outs, "q_outs", R, (T, hq, d), dt, dev)
+        q_outs, qop = _head_outs(q_outs, "q_outs", R, (T, hq, d), dt, dev, stream)
     elif q_outs is not None:
         raise ValueError("q_outs without qs")
     cp = sp = None
@@ -731,7 +747,7 @@ def kv_cache_attention(qs, cache, block_table, lens, scale=None, cu_new=None, wi
     T = q0.shape[0]
     hq, qstr, qp = _check_heads(qs, "qs", R, T, d, dt, dev)
     seqs, width = _check_seqs(cache, T, block_table, lens, cu_new)
-    outs, op = _head_outs(outs, "outs", R, (T, hq, d), dt, dev)
+    outs, op = _head_outs(outs, "outs", R, (T, hq, d), dt, dev, stream)
     buf, at = _words(qp, qstr, op)
     st = lib().coc_kv_cache_attention(cache._ref, T, seqs, hq, at[0], at[1], at[2], block_table.data_ptr(), width,
                                       lens.data_ptr(), None if cu_new is None else cu_new.data_ptr(),
@@ -770,7 +786,7 @@ def matmul_all_reduce_w4a16(xs, wqs, scales, group_size: int, zeros=None, outs=N
         if len(views) != R:
             raise ValueError(f"need one {name} tensor per rank")
         _check_list(views, name, (ks // group_size, n), want, dev)
-    outs, op = _head_outs(outs, "outs", R, (m, n), dt, dev)
+    outs, op = _head_outs(outs, "outs", R, (m, n), dt, dev, stream)
     buf, at = _words([t.data_ptr() for t in xs], [t.data_ptr() for t in wqs], [t.data_ptr() for t in scales],
                      [] if zeros is None else [t.data_ptr() for t in zeros], op)
     st = lib().coc_matmul_all_reduce_w4a16(R, m, n, ks, at[0], at[1], at[2], None if zeros is None else at[3], int(group_size),

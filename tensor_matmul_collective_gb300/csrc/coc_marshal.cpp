@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -75,7 +76,11 @@ const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1) {
 coc_dtype_t code_of(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 ? COC_BF16 : COC_FP16; }
 
 // Outputs: the given list's tensors, or R new ones; `list` is a new reference.
-bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor& like, PyObject** list, void* (&p)[COC_MAX_RANKS]) {
+// New ones of a call on another than the current stream are that stream's
+// memory (what the current stream has freed may still be in use there), and the
+// current stream, on which the caller goes on with them, is noted as a user.
+bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor& like, coc_stream_t stream, PyObject** list,
+             void* (&p)[COC_MAX_RANKS]) {
     if (given != Py_None) {
         Ranks o;
         if (!o.take(given, R, like.scalar_type(), like.device()) || !o.packed(R, shape)) return false;
@@ -84,9 +89,14 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor
         return *list != nullptr;
     }
     // (what may throw comes before the list)
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream();
+    const bool other = reinterpret_cast<cudaStream_t>(stream) != now.stream();
+    c10::cuda::OptionalCUDAStreamGuard on;
+    if (other) on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), like.device().index()));
     const at::TensorOptions opt = at::TensorOptions().dtype(like.scalar_type()).device(like.device());
     if (R == 1) {
         at::Tensor t = at::empty(shape, opt);
+        if (other) t.record_stream(now);
         if ((*list = PyList_New(1)) == nullptr) return false;
         p[0] = t.data_ptr();
         PyList_SET_ITEM(*list, 0, THPVariable_Wrap(std::move(t)));
@@ -97,6 +107,7 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor
     int64_t n = 1;
     for (const int64_t x : shape) n *= x;
     const at::Tensor all = at::empty({R * n}, opt);
+    if (other) all.record_stream(now);
     if ((*list = PyList_New(R)) == nullptr) return false;
     for (int64_t r = 0; r < R; ++r) {
         at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), all.dtype());
@@ -186,7 +197,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* qo[COC_MAX_RANKS] = {};
     if (a[9] != Py_None) {
         if (!q.take(a[9], R, dt, dev) || !q.heads(R, T, d, &hq, qs)) return none();
-        if (!outputs(a[10], R, {T, hq, d}, *k0, &list, qo)) return PyErr_Occurred() ? nullptr : none();
+        if (!outputs(a[10], R, {T, hq, d}, *k0, stream, &list, qo)) return PyErr_Occurred() ? nullptr : none();
     } else {
         if (a[10] != Py_None) return none();
         list = none();
@@ -225,7 +236,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[11], &stream)) return nullptr;
     PyObject* list = nullptr;
     void* out[COC_MAX_RANKS];
-    if (!outputs(a[10], R, {T, hq, d}, *q0, &list, out)) return PyErr_Occurred() ? nullptr : none();
+    if (!outputs(a[10], R, {T, hq, d}, *q0, stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(cache, T, ix.seqs, static_cast<int>(hq), q.p, qs, out, ix.table, ix.width, ix.lens, ix.cu, static_cast<float>(scale), window,
@@ -260,7 +271,7 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[7], &stream)) return nullptr;
     PyObject* list = nullptr;
     void* out[COC_MAX_RANKS];
-    if (!outputs(a[6], R, {m, cols}, *x0, &list, out)) return PyErr_Occurred() ? nullptr : none();
+    if (!outputs(a[6], R, {m, cols}, *x0, stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(R), m, cols, k, x.p, w.p, s.p, zero ? z.p : nullptr, group, out, code_of(*x0), stream);

@@ -37,18 +37,25 @@ class AttentionBlock:
     def __call__(self, xs, block_table, lens, cu_new=None, outs=None, stream=None):
         """xs[r]: rank r's rows of the new tokens' activations (tokens/R x
         hidden, tokens/R a multiple of 8); lens, block_table, cu_new as in
-        coc.kv_cache_append.  Returns tokens x hidden on every rank."""
+        coc.kv_cache_append.  Returns tokens x hidden on every rank.  With a
+        stream everything that is allocated on the way is that stream's."""
+        if stream is not None and coc._stream(stream) != torch.cuda.current_stream().cuda_stream:
+            now = torch.cuda.current_stream()
+            with torch.cuda.stream(coc._as_stream(stream)):
+                new = self(xs, block_table, lens, cu_new=cu_new, outs=outs)
+            if outs is None:
+                new[0].record_stream(now)       # all ranks' are one allocation
+            return new
         hq, hk, d = self.q_heads, self.kv_heads, self.head_dim
-        qkv = coc.all_gather_matmul(xs, self.w_qkv, stream=stream)
+        qkv = coc.all_gather_matmul(xs, self.w_qkv)
         tokens = qkv[0].shape[0]
         q = [t[:, :hq * d].view(tokens, hq, d) for t in qkv]
         k = [t[:, hq * d:(hq + hk) * d].view(tokens, hk, d) for t in qkv]
         v = [t[:, (hq + hk) * d:].view(tokens, hk, d) for t in qkv]
-        q = coc.kv_cache_append(k, v, self.cache, block_table, lens, self.cos, self.sin, qs=q, cu_new=cu_new, stream=stream)
-        ctx = coc.kv_cache_attention(q, self.cache, block_table, lens, cu_new=cu_new, window=self.window, sinks=self.sinks,
-                                     stream=stream)
+        q = coc.kv_cache_append(k, v, self.cache, block_table, lens, self.cos, self.sin, qs=q, cu_new=cu_new)
+        ctx = coc.kv_cache_attention(q, self.cache, block_table, lens, cu_new=cu_new, window=self.window, sinks=self.sinks)
         return coc.matmul_all_reduce_w4a16([c.view(tokens, hq * d) for c in ctx], self.w_out, self.scales, self.group,
-                                           zeros=self.zeros, outs=outs, stream=stream)
+                                           zeros=self.zeros, outs=outs)
 
 
 def rotation_tables(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):

@@ -549,7 +549,9 @@ typedef struct {
  *                a page that holds earlier tokens not below its scale S0
  *                before.  A power of two costs e4m3 no precision and changes
  *                of scale stay exact down to its underflow.
- *   codes        e4m3(value / S), from the fp32 value, round-to-nearest-even;
+ *   codes        e4m3(value / S), from the fp32 value, round-to-nearest-even
+ *                (times the rounded 1 / S where a caller's S0 that is no power
+ *                of two stays);
  *                the page's earlier codes c become e4m3(c S0 / S) where S grew.
  *                NaN stays NaN, infinities become +-448 (neither counts in amax).
  *   q_out[r]     tokens x q_heads x head_dim, packed: the rotated q, rounded once.

@@ -52,7 +52,7 @@ def busy():
     """(stream, event at its end) of some hundred milliseconds of work on a stream of its own."""
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(400_000_000)
+        torch.cuda._sleep(1_000_000_000)
         end = torch.cuda.Event()
         end.record()
     return side, end

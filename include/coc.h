@@ -25,6 +25,14 @@
  *   attention over that cache                           coc_kv_cache_attention
  *   MATMUL_ALL_REDUCE with 4-bit weights                coc_matmul_all_reduce_w4a16
  *
+ * and the feed-forward block in 8-bit floating point (extension):
+ *   rows to codes and scales                            coc_quantize_f8
+ *   residual addition, RMS norm, codes and scales       coc_add_rms_norm_f8
+ *   the AllReduce, ReduceScatter and AllGather
+ *     operators on 8-bit activations and weights        coc_fused_matmul_f8
+ *   ALL_GATHER_MATMUL of gate and up projection,
+ *     silu(gate) * up, codes and scales                 coc_all_gather_gated_matmul_f8
+ *
  * The same page's section 问题分析 ("problem analysis") places them in the
  * Megatron ColumnParallelLinear / RowParallelLinear layers: the matmul is
  * followed by AllReduce without sequence parallelism, by AllGather or
@@ -629,6 +637,89 @@ coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, int64_t k_
                                          const void* const* scale, const void* const* zero,
                                          int64_t group_size, void* const* out,
                                          coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * 8-bit floating point.  A matrix is held as e4m3 codes (1 byte; 448 is the
+ * largest value) with power-of-two scales (e8m0: 1 byte, the value 2^(byte -
+ * 127); 255 is NaN): the value of a code is code * scale.
+ *
+ *   activations  rows x k codes, rows x ceil(k/128) scales: one for each row
+ *                and 128 columns (the last ones may be fewer)
+ *   weights      n x k codes (Megatron's [out, in]), ceil(n/128) x ceil(k/128)
+ *                scales: one for 128 x 128
+ *
+ * Codes are 16-byte aligned, rows of codes a multiple of 16 bytes; scales have
+ * no alignment.  Where a call makes codes of values y, the scale S of 128 of
+ * them is the least power of two with max|y| <= 448 S, at least 2^-100, and
+ * code = e4m3(y / S), round-to-nearest-even from the fp32 value; NaN stays
+ * NaN, infinities become +-448 (neither counts in the maximum).
+ *
+ * Products are summed in fp32 on the tensor cores, which apply the scales
+ * (kind::mxf8f6f4): k ascending, rank after rank.  Few rows (up to 128) and
+ * tiles that leave SMs free split the contraction into up to 8 ranges, whose
+ * sums are added in order; the split depends on the sizes and the GPU only,
+ * so results are bitwise reproducible.
+ */
+
+/*
+ * Rows of 16-bit values to codes and scales.
+ *
+ * R in {1, 2, 4, 8}; x[r] rows x hidden in `dt`, codes[r] rows x hidden,
+ * scale[r] rows x ceil(hidden/128).  hidden % 16 == 0; x and codes 16-byte
+ * aligned.  One kernel, no scratch; rows == 0 or hidden == 0 is a no-op.
+ */
+coc_status_t coc_quantize_f8(int R, int64_t rows, int64_t hidden, const void* const* x, void* const* codes,
+                             void* const* scale, coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * Residual addition and root-mean-square norm with the result in 8 bits.
+ *
+ *   s = x[r] + residual[r]  (fp32; residual NULL: s = x[r]);  sum[r] = rne(s)
+ *   y = s / sqrt(mean(s^2) + eps) * weight;  codes[r], scale[r] = y as above
+ *
+ * The norm takes the unrounded s.  Each rank has its own rows (sequence
+ * parallelism); weight is one vector of `hidden` values in `dt`.
+ * hidden % 16 == 0, at most 65536; eps in [1e-20, 1e20]; residual and sum are
+ * given together or not at all; sum[r] may be residual[r] or x[r] itself.
+ * Other arguments as coc_quantize_f8.
+ */
+coc_status_t coc_add_rms_norm_f8(int R, int64_t rows, int64_t hidden, const void* const* x, const void* const* residual,
+                                 const void* weight, float eps, void* const* sum, void* const* codes,
+                                 void* const* scale, coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * The fused operators on 8-bit activations and weights.
+ *
+ * op       COC_OP_ALL_REDUCE / _REDUCE_SCATTER: (rows, cols, inner) = (m, n,
+ *          k_shard), x[r] m x k_shard, w[r] n x k_shard, out[r] m x n in `dt`
+ *          (AR) or (m/R) x n (RS; m % R == 0).  COC_OP_ALL_GATHER: (m_shard,
+ *          n_shard, k), x[r] m_shard x k, w[r] n_shard x k, out[r] (R m_shard)
+ *          x n_shard.  Any number of rows.
+ * inner % 16 == 0, cols % 8 == 0; codes and outputs 16-byte aligned.
+ * rows == 0 or cols == 0 is a no-op, inner == 0 writes zeros.
+ * AllGather shards (codes and scales) that do not follow each other in
+ * memory are first stacked by a copy into the call's scratch.
+ */
+coc_status_t coc_fused_matmul_f8(coc_op_t op, int R, int64_t rows, int64_t cols, int64_t inner, const void* const* x,
+                                 const void* const* x_scale, const void* const* w, const void* const* w_scale,
+                                 void* const* out, coc_dtype_t dt, coc_stream_t stream);
+
+/*
+ * ALL_GATHER_MATMUL of a gated feed-forward layer's two projections with the
+ * activation: Xg = the gathered rows,
+ *
+ *   g = Xg Wg_r^T, u = Xg Wu_r^T (fp32);  h = g / (1 + e^-g) * u
+ *   codes[r], scale[r] = h in 8 bits, a scale for each row and 128 columns
+ *
+ * x[r]     m_shard x k
+ * w[r]     (2 f_shard) x k: the rows of Wg_r, then those of Wu_r; w_scale[r]
+ *          (2 ceil(f_shard/128)) x ceil(k/128): Wg_r's blocks, then Wu_r's
+ * codes[r] (R m_shard) x f_shard, scale[r] (R m_shard) x ceil(f_shard/128)
+ * f_shard % 16 == 0, k % 16 == 0; otherwise as coc_fused_matmul_f8.
+ */
+coc_status_t coc_all_gather_gated_matmul_f8(int R, int64_t m_shard, int64_t f_shard, int64_t k, const void* const* x,
+                                            const void* const* x_scale, const void* const* w, const void* const* w_scale,
+                                            void* const* codes, void* const* scale, coc_stream_t stream);
 
 /*
  * Waits for `stream`, then returns and clears the device-side status of

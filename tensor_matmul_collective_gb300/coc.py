@@ -33,7 +33,8 @@ EXPORTS = (
     "coc_fused_matmul", "coc_matmul_all_reduce_w8a16_ex", "coc_moe_dispatch_grouped_matmul", "coc_moe_capacity",
     "coc_moe_dispatch_grouped_matmul_combine", "coc_moe_topk_grouped_matmul_combine", "coc_debug_alloc_count",
     "coc_debug_clock_probe", "coc_debug_clock_read", "coc_kv_cache_append", "coc_kv_cache_attention",
-    "coc_matmul_all_reduce_w4a16",
+    "coc_matmul_all_reduce_w4a16", "coc_quantize_f8", "coc_add_rms_norm_f8", "coc_fused_matmul_f8",
+    "coc_all_gather_gated_matmul_f8",
 )
 
 OP_ALL_REDUCE, OP_REDUCE_SCATTER, OP_ALL_GATHER, OP_ALL_GATHER_V2, OP_WEIGHT_GRAD = range(5)
@@ -109,6 +110,14 @@ def lib() -> ctypes.CDLL:
             L.coc_kv_cache_attention.restype = i32
             L.coc_matmul_all_reduce_w4a16.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, i64, vp, i32, vp]
             L.coc_matmul_all_reduce_w4a16.restype = i32
+            L.coc_quantize_f8.argtypes = [i32, i64, i64, vp, vp, vp, i32, vp]
+            L.coc_quantize_f8.restype = i32
+            L.coc_add_rms_norm_f8.argtypes = [i32, i64, i64, vp, vp, vp, ctypes.c_float, vp, vp, vp, i32, vp]
+            L.coc_add_rms_norm_f8.restype = i32
+            L.coc_fused_matmul_f8.argtypes = [i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, i32, vp]
+            L.coc_fused_matmul_f8.restype = i32
+            L.coc_all_gather_gated_matmul_f8.argtypes = [i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+            L.coc_all_gather_gated_matmul_f8.restype = i32
             L.coc_sync_status.argtypes = [vp]
             L.coc_sync_status.restype = i32
             L.coc_status_string.argtypes = [i32]
@@ -805,6 +814,169 @@ def w4_pack(codes):
     bits = torch.arange(0, 32, 4, device=codes.device, dtype=torch.int64)[None, :, None]
     words = ((codes.to(torch.int64) & 15).view(k // 8, 8, n) << bits).sum(1)
     return torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
+
+
+# ---- 8-bit floating point: codes (float8_e4m3fn) with power-of-two scales
+# (float8_e8m0fnu) for 128 columns of a row, or 128 x 128 of a weight
+
+F8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def _addresses(ts):
+    return [t.data_ptr() for t in ts]
+
+
+def _f8_rows_shape(xs):
+    """(ranks, rows, hidden, dtype, device) of the 16-bit rows, checked."""
+    if not isinstance(xs, (list, tuple)) or not 1 <= len(xs) <= MAX_RANKS or not isinstance(xs[0], torch.Tensor) or xs[0].dim() != 2:
+        raise ValueError(f"xs must be a list of 1..{MAX_RANKS} rows x hidden tensors, one per rank")
+    x0 = xs[0]
+    _check_device(x0)
+    _dtype_code(x0.dtype)
+    _check_list(xs, "xs", x0.shape, x0.dtype, x0.device)
+    return len(xs), x0.shape[0], x0.shape[1], x0.dtype, x0.device
+
+
+def quantize_f8(xs, outs=None, scales=None, stream=None):
+    """Rows of 16-bit values to 8 bits: (codes, scales) of every rank.
+
+    xs[r]: rows x hidden (fp16/bf16), hidden a multiple of 16; codes[r]: rows x
+    hidden float8_e4m3fn, scales[r]: rows x ceil(hidden/128) float8_e8m0fnu,
+    the least power of two that keeps 128 values within e4m3 (at least 2**-100).
+    New ones are parts of one allocation each."""
+    R, rows, hidden, dt, dev = _f8_rows_shape(xs)
+    outs, op = _head_outs(outs, "outs", R, (rows, hidden), torch.float8_e4m3fn, dev, stream)
+    scales, sp = _head_outs(scales, "scales", R, (rows, _blocks(hidden)), torch.float8_e8m0fnu, dev, stream)
+    buf, at = _words(_addresses(xs), op, sp)
+    _check(lib().coc_quantize_f8(R, rows, hidden, at[0], at[1], at[2], _dtype_code(dt), _stream(stream)))
+    return outs, scales
+
+
+def add_rms_norm_f8(xs, weight, residuals=None, eps: float = 1e-6, outs=None, scales=None, sums=None, stream=None):
+    """Residual addition and root-mean-square norm with the result in 8 bits: (codes, scales, sums) of every rank.
+
+    s = xs[r] + residuals[r] (fp32; without residuals xs[r]); sums[r] = s
+    rounded to the type of xs (None without residuals; residuals[r] itself may
+    be given as sums[r]); codes[r], scales[r] = s / sqrt(mean(s**2) + eps) * weight
+    as quantize_f8 gives them.  weight: hidden values in the type of xs, the
+    same for every rank; hidden up to 65536."""
+    R, rows, hidden, dt, dev = _f8_rows_shape(xs)
+    _check_list([weight], "weight", (hidden,), dt, dev)
+    if residuals is None:
+        if sums is not None:
+            raise ValueError("sums without residuals")
+        rp, up = [], []
+    else:
+        _check_list(residuals, "residuals", (rows, hidden), dt, dev)
+        if len(residuals) != R:
+            raise ValueError("need one residual per rank")
+        rp = _addresses(residuals)
+        sums, up = _head_outs(sums, "sums", R, (rows, hidden), dt, dev, stream)
+    outs, op = _head_outs(outs, "outs", R, (rows, hidden), torch.float8_e4m3fn, dev, stream)
+    scales, sp = _head_outs(scales, "scales", R, (rows, _blocks(hidden)), torch.float8_e8m0fnu, dev, stream)
+    buf, at = _words(_addresses(xs), rp, up, op, sp)
+    _check(lib().coc_add_rms_norm_f8(R, rows, hidden, at[0], at[1] if rp else None, weight.data_ptr(), float(eps), at[2] if rp else None,
+                                     at[3], at[4], _dtype_code(dt), _stream(stream)))
+    return outs, scales, sums
+
+
+def _f8_prep(xs, x_scales, ws, w_scales, halves: int = 1):
+    """(ranks, rows, inner, columns of a half) of an 8-bit product's operands, checked."""
+    R, x0, w0 = _prep(xs, ws)
+    rows, k = x0.shape
+    dev = x0.device
+    n = w0.shape[0]
+    if n % halves:
+        raise ValueError("ws must be the gate's rows and as many of the up projection")
+    n //= halves
+    for name, ts, shape, dt in (("xs", xs, (rows, k), torch.float8_e4m3fn), ("x_scales", x_scales, (rows, _blocks(k)), torch.float8_e8m0fnu),
+                                ("ws", ws, (halves * n, k), torch.float8_e4m3fn),
+                                ("w_scales", w_scales, (halves * _blocks(n), _blocks(k)), torch.float8_e8m0fnu)):
+        _check_list(ts, name, shape, dt, dev)
+        if len(ts) != R:
+            raise ValueError(f"need one {name} tensor per rank")
+    return R, rows, k, n, dev
+
+
+def _fused_f8(code, xs, x_scales, ws, w_scales, outs, dtype, stream):
+    R, rows, k, n, dev = _f8_prep(xs, x_scales, ws, w_scales)
+    if dtype is None:
+        dtype = torch.bfloat16 if not outs or not isinstance(outs[0], torch.Tensor) else outs[0].dtype
+    dt = _dtype_code(dtype)
+    if code == OP_REDUCE_SCATTER and rows % R:
+        raise CocError(ERR_SHAPE, "COC_ERR_SHAPE", f"m = {rows} is not a multiple of R = {R}")
+    m = rows // R if code == OP_REDUCE_SCATTER else R * rows if code == OP_ALL_GATHER else rows
+    outs, op = _head_outs(outs, "outs", R, (m, n), dtype, dev, stream)
+    buf, at = _words(_addresses(xs), _addresses(x_scales), _addresses(ws), _addresses(w_scales), op)
+    _check(lib().coc_fused_matmul_f8(code, R, rows, n, k, *at, dt, _stream(stream)))
+    return outs
+
+
+def matmul_all_reduce_f8(xs, x_scales, ws, w_scales, outs=None, dtype=None, stream=None):
+    """MATMUL_ALL_REDUCE in 8 bits: outs[r] = sum_q X_q @ W_q^T for every rank r.
+
+    xs[q], x_scales[q]: m x k_shard codes with m x ceil(k_shard/128) scales
+    (quantize_f8, add_rms_norm_f8, all_gather_gated_matmul_f8); ws[q],
+    w_scales[q]: n x k_shard codes with a scale for 128 x 128 (f8_pack).  outs
+    are `dtype` (fp16/bf16; bf16 where neither it nor outs is given); new ones are
+    parts of one allocation.  Any m; k_shard a multiple of 16, n of 8."""
+    return _fused_f8(OP_ALL_REDUCE, xs, x_scales, ws, w_scales, outs, dtype, stream)
+
+
+def matmul_reduce_scatter_f8(xs, x_scales, ws, w_scales, outs=None, dtype=None, stream=None):
+    """MATMUL_REDUCE_SCATTER in 8 bits: outs[r] = rows [r*m/R, (r+1)*m/R) of sum_q X_q @ W_q^T.  Arguments as matmul_all_reduce_f8."""
+    return _fused_f8(OP_REDUCE_SCATTER, xs, x_scales, ws, w_scales, outs, dtype, stream)
+
+
+def all_gather_matmul_f8(xs, x_scales, ws, w_scales, outs=None, dtype=None, stream=None):
+    """ALL_GATHER_MATMUL in 8 bits: outs[r] = cat(X, dim=0) @ W_r^T.
+
+    xs[i], x_scales[i]: m_shard rows, any number; otherwise as
+    matmul_all_reduce_f8.  Shards that are parts of one allocation, as this
+    module's calls return them, are read as they lie; others are copied together first."""
+    return _fused_f8(OP_ALL_GATHER, xs, x_scales, ws, w_scales, outs, dtype, stream)
+
+
+def all_gather_gated_matmul_f8(xs, x_scales, ws, w_scales, outs=None, scales=None, stream=None):
+    """Both projections of a gated feed-forward layer, silu(gate) * up, in 8 bits: (codes, scales) of every rank.
+
+    xs[i], x_scales[i] as in all_gather_matmul_f8; ws[r]: (2 f_shard) x k
+    codes, the gate's rows, then the up projection's, w_scales[r]
+    (2 ceil(f_shard/128)) x ceil(k/128) (f8_pack with parts=2); f_shard a multiple of 16.
+    codes[r]: (R m_shard) x f_shard, scales[r]: (R m_shard) x ceil(f_shard/128)."""
+    R, rows, k, f, dev = _f8_prep(xs, x_scales, ws, w_scales, halves=2)
+    outs, op = _head_outs(outs, "outs", R, (R * rows, f), torch.float8_e4m3fn, dev, stream)
+    scales, sp = _head_outs(scales, "scales", R, (R * rows, _blocks(f)), torch.float8_e8m0fnu, dev, stream)
+    buf, at = _words(_addresses(xs), _addresses(x_scales), _addresses(ws), _addresses(w_scales), op, sp)
+    _check(lib().coc_all_gather_gated_matmul_f8(R, rows, f, k, *at, _stream(stream)))
+    return outs, scales
+
+
+def f8_pack(w, parts: int = 1):
+    """A weight (n x k, out x in) in 8 bits: n x k float8_e4m3fn codes and float8_e8m0fnu scales, one for 128 x 128.
+
+    parts: equal groups of rows (gate and up: 2) whose blocks of 128 rows begin anew."""
+    if w.dim() != 2 or parts < 1 or w.shape[0] % parts:
+        raise ValueError("w must be n x k, n a multiple of parts")
+    n, k = w.shape[0] // parts, w.shape[1]
+    codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    scales = torch.empty((parts * _blocks(n), _blocks(k)), dtype=torch.uint8, device=w.device)
+    for p in range(parts):
+        for b in range(_blocks(n)):
+            rows = slice(p * n + b * F8_BLOCK, p * n + min(n, (b + 1) * F8_BLOCK))
+            t = torch.nn.functional.pad(w[rows].float(), (0, _blocks(k) * F8_BLOCK - k)).view(-1, _blocks(k), F8_BLOCK)
+            mag = t.abs()
+            m, e = torch.frexp(torch.where(mag.isfinite(), mag, torch.zeros_like(mag)).amax((0, 2)))
+            e = torch.where(m > 0, e + torch.where(m > 0.875, -8, -9), torch.full_like(e, -100)).clamp(min=-100)
+            scales[p * _blocks(n) + b] = (e + 127).to(torch.uint8)
+            inverse = ((127 - e).to(torch.int32) << 23).view(torch.float32)      # 2**-e, exact
+            t = (t * inverse[None, :, None]).view(-1, _blocks(k) * F8_BLOCK)[:, :k]
+            codes[rows] = t.clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return codes, scales.view(torch.float8_e8m0fnu)
 
 
 def matmul(xs, ws, out=None, stream=None):

@@ -1757,6 +1757,177 @@ COC_API coc_status_t coc_matmul_all_reduce_w4a16(int R, int64_t m, int64_t n, in
     return e == cudaSuccess ? COC_OK : cuda_fail(e, "w4A16 launch");
 }
 
+// Scales have no alignment: only that they are there.
+static coc_status_t check_scales(const void* const* arr, int R, const char* name) {
+    if (arr == nullptr) return fail(COC_ERR_INVALID_ARG, "%s is NULL", name);
+    for (int r = 0; r < R; ++r)
+        if (arr[r] == nullptr) return fail(COC_ERR_INVALID_ARG, "%s[%d] is NULL", name, r);
+    return COC_OK;
+}
+
+static coc_status_t f8_rows(bool norm, int R, int64_t rows, int64_t hidden, const void* const* x, const void* const* residual,
+                            const void* weight, float eps, void* const* sum, void* const* codes, void* const* scale, coc_dtype_t dt,
+                            coc_stream_t stream) {
+    coc_status_t st = check_common(R, 1, dt, 0);
+    if (st != COC_OK) return st;
+    if ((st = check_dims(rows, hidden, 0)) != COC_OK) return st;
+    if (hidden % 16 != 0) return fail(COC_ERR_ALIGN, "hidden = %lld: rows of codes must span a multiple of 16 bytes", (long long)hidden);
+    if (norm) {
+        if (hidden > kF8MaxHidden) return fail(COC_ERR_SHAPE, "hidden = %lld above %d", (long long)hidden, kF8MaxHidden);
+        if (!(eps >= 1e-20f && eps <= 1e20f)) return fail(COC_ERR_INVALID_ARG, "eps = %g outside [1e-20, 1e20]", static_cast<double>(eps));
+    }
+    if (rows * ((hidden + 127) / 128) > kMaxDim) return fail(COC_ERR_SHAPE, "%lld rows of %lld: above 2^31 scales", (long long)rows, (long long)hidden);
+    const bool needed = rows > 0 && hidden > 0;
+    if ((st = check_ptrs(x, R, needed, "x")) != COC_OK || (st = check_ptrs(codes, R, needed, "codes")) != COC_OK) return st;
+    if (needed && (st = check_scales(scale, R, "scale")) != COC_OK) return st;
+    if (norm && needed) {
+        if (weight == nullptr) return fail(COC_ERR_INVALID_ARG, "weight is NULL");
+        if (!aligned16(weight)) return fail(COC_ERR_ALIGN, "weight not 16-byte aligned");
+        if ((residual == nullptr) != (sum == nullptr)) return fail(COC_ERR_INVALID_ARG, "residual and sum are given together or not at all");
+        if (residual != nullptr && ((st = check_ptrs(residual, R, true, "residual")) != COC_OK || (st = check_ptrs(sum, R, true, "sum")) != COC_OK))
+            return st;
+    }
+    if (!needed) return COC_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != COC_OK) return st;
+    F8RowsArgs a;
+    std::memset(&a, 0, sizeof a);
+    for (int r = 0; r < R; ++r) {
+        a.x[r] = static_cast<const uint16_t*>(x[r]);
+        a.codes[r] = static_cast<uint8_t*>(codes[r]);
+        a.scale[r] = static_cast<uint8_t*>(scale[r]);
+        if (norm && residual != nullptr) {
+            a.residual[r] = static_cast<const uint16_t*>(residual[r]);
+            a.sum[r] = static_cast<uint16_t*>(sum[r]);
+        }
+    }
+    a.weight = static_cast<const uint16_t*>(weight);
+    a.eps = eps;
+    a.R = R;
+    a.rows = static_cast<int>(rows);
+    a.hidden = static_cast<int>(hidden);
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = norm ? launch_f8_norm(a, dt == COC_BF16, ds->sm_count, str) : launch_f8_quantize(a, dt == COC_BF16, str);
+    return e == cudaSuccess ? COC_OK : cuda_fail(e, "row quantisation launch");
+}
+
+COC_API coc_status_t coc_quantize_f8(int R, int64_t rows, int64_t hidden, const void* const* x, void* const* codes,
+                                     void* const* scale, coc_dtype_t dt, coc_stream_t stream) {
+    return f8_rows(false, R, rows, hidden, x, nullptr, nullptr, 0.f, nullptr, codes, scale, dt, stream);
+}
+
+COC_API coc_status_t coc_add_rms_norm_f8(int R, int64_t rows, int64_t hidden, const void* const* x, const void* const* residual,
+                                         const void* weight, float eps, void* const* sum, void* const* codes,
+                                         void* const* scale, coc_dtype_t dt, coc_stream_t stream) {
+    return f8_rows(true, R, rows, hidden, x, residual, weight, eps, sum, codes, scale, dt, stream);
+}
+
+// op OP_AR / OP_RS: rows = m; OP_AG: rows = m_shard.  out_scale: the gated form's.
+static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n, int64_t k, const void* const* x,
+                              const void* const* x_scale, const void* const* w, const void* const* w_scale, void* const* out,
+                              void* const* out_scale, coc_dtype_t dt, coc_stream_t stream) {
+    coc_status_t st = check_common(R, 1, dt, 0);
+    if (st != COC_OK) return st;
+    if ((st = check_dims(rows, n, k)) != COC_OK) return st;
+    const bool ag = op == OP_AG;
+    const int64_t m = ag ? R * rows : rows;
+    if (m > kMaxDim || (gated && 2 * n > kMaxDim)) return fail(COC_ERR_SHAPE, "%lld gathered rows, %lld columns: above 2^31", (long long)m, (long long)n);
+    if (k % 16 != 0) return fail(COC_ERR_ALIGN, "k = %lld: rows of codes must span a multiple of 16 bytes", (long long)k);
+    if (n % (gated ? 16 : 8) != 0) return fail(COC_ERR_ALIGN, "n = %lld: rows of the outputs must span a multiple of 16 bytes", (long long)n);
+    if (op == OP_RS && rows % R != 0) return fail(COC_ERR_SHAPE, "m = %lld is not a multiple of R = %d", (long long)rows, R);
+    const int64_t kblocks = (k + 127) / 128, n_tiles = (n + 127) / 128;
+    if (((m + 15) / 16) * n_tiles * R > kMaxDim / 8) return fail(COC_ERR_SHAPE, "%lld x %lld outputs: too many tiles", (long long)m, (long long)n);
+    if (kblocks * R > kMaxDim) return fail(COC_ERR_SHAPE, "k = %lld is too long", (long long)k);
+    const bool any = m > 0 && n > 0, needed = any && k > 0;
+    if ((st = check_ptrs(x, R, needed, "x")) != COC_OK || (st = check_ptrs(w, R, needed, "w")) != COC_OK ||
+        (st = check_ptrs(out, R, any, "out")) != COC_OK)
+        return st;
+    if (needed && ((st = check_scales(x_scale, R, "x_scale")) != COC_OK || (st = check_scales(w_scale, R, "w_scale")) != COC_OK)) return st;
+    if (gated && any && (st = check_scales(out_scale, R, "out_scale")) != COC_OK) return st;
+    if (!any) return COC_OK;
+    DeviceState* ds = nullptr;
+    if ((st = device_state(&ds)) != COC_OK) return st;
+    cudaStream_t str = reinterpret_cast<cudaStream_t>(stream);
+
+    F8Args a;
+    std::memset(&a, 0, sizeof a);
+    Scratch sc;
+    const uint8_t* x0 = nullptr;
+    const uint8_t* s0 = nullptr;
+    if (needed && ag) {
+        // the gathered rows as one matrix: as they lie where the shards follow each other, else stacked by a copy
+        x0 = static_cast<const uint8_t*>(x[0]);
+        s0 = static_cast<const uint8_t*>(x_scale[0]);
+        bool apart = false;
+        for (int r = 1; r < R; ++r)
+            apart = apart || x[r] != x0 + r * rows * k || x_scale[r] != s0 + r * rows * kblocks;
+        if (apart) {
+            const size_t codes = static_cast<size_t>(m) * k;
+            if ((st = scratch_acquire(ds, str, codes + static_cast<size_t>(m) * kblocks, &sc, true)) != COC_OK) return st;
+            F8StackArgs g;
+            std::memset(&g, 0, sizeof g);
+            for (int r = 0; r < R; ++r) {
+                g.x[r] = static_cast<const uint8_t*>(x[r]);
+                g.scale[r] = static_cast<const uint8_t*>(x_scale[r]);
+            }
+            g.x_dst = static_cast<uint8_t*>(sc.ptr);
+            g.scale_dst = g.x_dst + codes;
+            g.vecs = rows * k / 16;
+            g.scale_bytes = rows * kblocks;
+            g.R = R;
+            const cudaError_t e = launch_f8_stack(g, ds->sm_count, str);
+            if (e != cudaSuccess) return scratch_release(str, sc, cuda_fail(e, "activation stack launch"));
+            x0 = g.x_dst;
+            s0 = g.scale_dst;
+        }
+    }
+    for (int r = 0; r < R && needed && st == COC_OK; ++r) {
+        const uint64_t w_rows = static_cast<uint64_t>(gated ? 2 * n : n);
+        st = encode(&a.tm_w[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, w[r], k, w_rows, k, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        a.w_scale[r] = static_cast<const uint8_t*>(w_scale[r]);
+        if (st == COC_OK && (!ag || r == 0)) {
+            st = encode(&a.tm_x[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, ag ? x0 : x[r], k, m, k, 128, static_cast<uint32_t>(f8_slab_rows(m)),
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+            a.x_scale[r] = ag ? s0 : static_cast<const uint8_t*>(x_scale[r]);
+        }
+    }
+    if (st != COC_OK) return scratch_release(str, sc, st);
+    for (int r = 0; r < R; ++r) {
+        a.out[r] = out[r];
+        a.out_scale[r] = gated ? static_cast<uint8_t*>(out_scale[r]) : nullptr;
+    }
+    a.status = ds->status;
+    a.inject_timeout = g_inject.load();
+    a.op = op;
+    a.R = R;
+    a.m = static_cast<int>(m);
+    a.n = static_cast<int>(n);
+    a.shards = ag ? 1 : R;
+    a.kblocks = static_cast<int>(kblocks);
+    a.n_tiles = static_cast<int>(n_tiles);
+    a.rows_per_rank = op == OP_RS ? static_cast<int>(m / R) : static_cast<int>(m);
+    const cudaError_t e = launch_f8_slab(a, gated, dt == COC_BF16, ds->sm_count, str);
+    if (e != cudaSuccess) st = cuda_fail(e, "8-bit product launch");
+    return scratch_release(str, sc, st);
+}
+
+COC_API coc_status_t coc_fused_matmul_f8(coc_op_t op, int R, int64_t rows, int64_t cols, int64_t inner, const void* const* x,
+                                         const void* const* x_scale, const void* const* w, const void* const* w_scale,
+                                         void* const* out, coc_dtype_t dt, coc_stream_t stream) {
+    switch (op) {
+        case COC_OP_ALL_REDUCE: return f8_matmul(OP_AR, false, R, rows, cols, inner, x, x_scale, w, w_scale, out, nullptr, dt, stream);
+        case COC_OP_REDUCE_SCATTER: return f8_matmul(OP_RS, false, R, rows, cols, inner, x, x_scale, w, w_scale, out, nullptr, dt, stream);
+        case COC_OP_ALL_GATHER: return f8_matmul(OP_AG, false, R, rows, cols, inner, x, x_scale, w, w_scale, out, nullptr, dt, stream);
+        default: return fail(COC_ERR_INVALID_ARG, "op = %d is none of the 8-bit products", static_cast<int>(op));
+    }
+}
+
+COC_API coc_status_t coc_all_gather_gated_matmul_f8(int R, int64_t m_shard, int64_t f_shard, int64_t k, const void* const* x,
+                                                    const void* const* x_scale, const void* const* w, const void* const* w_scale,
+                                                    void* const* codes, void* const* scale, coc_stream_t stream) {
+    return f8_matmul(OP_AG, true, R, m_shard, f_shard, k, x, x_scale, w, w_scale, codes, scale, COC_BF16, stream);
+}
+
 // Status words of the current device's library state, read and cleared; all
 // zero (and nothing created) when no allocating call has run on the device.
 static coc_status_t take_library_status(unsigned (&words)[STATUS_WORDS]) {

@@ -1,0 +1,116 @@
+// Shared by the 8-bit floating-point kernels (coc_f8_rows.cu, coc_f8_slab.cu,
+// coc_f8_tile.cu): quantisation of a block of 128 values, and the
+// block-scaled tcgen05 products.
+//
+// Values are e4m3 codes with power-of-two scales (e8m0 bytes: exponent + 127)
+// for 128 columns of a row (activations) or 128 x 128 (weights).  A power of
+// two costs e4m3 no precision, and the tensor cores apply it inside the
+// product (kind::mxf8f6f4), so accumulators stay in tensor memory over the
+// whole contraction: nothing has to be read back, scaled and added per block.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "coc_kv.cuh"
+#include "coc_ptx.cuh"
+
+namespace coc {
+namespace {
+
+// The scale byte of a block whose largest finite magnitude is amax (scale_for's
+// power of two), and the factor 1 / S, which is exact: S lies in [2^-100, 2^120].
+__device__ __forceinline__ uint32_t f8_scale_byte(float amax) { return __float_as_uint(scale_for(amax)) >> 23; }
+__device__ __forceinline__ float f8_inverse(uint32_t scale_byte) { return __uint_as_float((254u - scale_byte) << 23); }
+
+// |v| where it is finite, else 0: what counts in a block's largest magnitude.
+__device__ __forceinline__ float f8_magnitude(float v) {
+    const float a = fabsf(v);
+    return a <= 3.4028234663852886e38f ? a : 0.f;
+}
+
+// Four codes, e4m3(v * f), round-to-nearest-even; beyond 448 (infinities) +-448, NaN stays NaN.
+__device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d, float f) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * f, b * f), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * f, d * f), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// silu(g) u = g u / (1 + e^-g).  For g -> -inf the quotient goes to -0 as
+// e^-g overflows to infinity; NaN comes through.
+__device__ __forceinline__ float f8_gated(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// ---- block-scaled products ----
+
+// Instruction descriptor, kind::mxf8f6f4 with e4m3 operands, both K-major, ue8m0
+// scales (bit 23); N >> 3 at bit 17, M >> 4 at bit 24; which byte of the scale
+// words is meant at bits 4 (B) and 29 (A).
+__host__ __device__ constexpr uint32_t f8_idesc(int M, int N) {
+    return (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t f8_idesc_byte(uint32_t idesc, uint32_t byte) { return idesc | (byte << 4) | (byte << 29); }
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale,
+                                          uint32_t b_scale, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale,
+                                               uint32_t b_scale, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+        : "memory");
+}
+
+// Scale words of 128 rows, shared memory -> 4 columns of tensor memory (in all
+// four lane quadrants): row i + 32 j's word, whose byte b is the scale of the
+// row's k-block 4 g + b, lies at bytes 16 i + 4 j of the 512.
+constexpr int kScaleBlock = 512;
+__device__ __forceinline__ uint32_t scale_word_at(uint32_t row) { return (row & 31u) * 16u + (row >> 5) * 4u; }
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    // no swizzle; eight-row groups of 16 bytes follow each other at 128 bytes
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t saddr) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(saddr)) : "memory");
+}
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(saddr)) : "memory");
+}
+
+// One byte that an earlier kernel on the stream may have written.
+__device__ __forceinline__ uint32_t load_byte(const uint8_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+// The scale word of a row: bytes [kb, kb + 4) of its `blocks` scale bytes, zero past them.
+__device__ __forceinline__ uint32_t load_scale_word(const uint8_t* row, int kb, int blocks) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (kb + b < blocks) v |= load_byte(row + kb + b) << (8 * b);
+    return v;
+}
+
+// The k-blocks of all shards one after another, taken from `begin` in runs that
+// share a scale word: up to 4 blocks of one shard, from a multiple of 4 of it.
+struct F8Run {
+    int shard, kb, count;      // blocks kb .. kb + count - 1 of the shard; kb & ~3 is the word's first
+};
+__device__ __forceinline__ F8Run f8_run(int at, int end, int kblocks) {
+    F8Run r;
+    r.shard = at / kblocks;
+    r.kb = at - r.shard * kblocks;
+    r.count = min(min(4 - (r.kb & 3), kblocks - r.kb), end - at);
+    return r;
+}
+
+}  // namespace
+}  // namespace coc

@@ -1,0 +1,229 @@
+// Rows of 16-bit values to e4m3 codes with a power-of-two scale for every 128
+// columns, as they are or behind the residual's addition and a
+// root-mean-square norm.
+//
+// Mathematics.  s = x + residual; y = s / sqrt(mean(s^2) + eps) * weight; for
+// each row and 128 columns S = the least power of two with max|y| <= 448 S and
+// code = e4m3(y / S).  All in fp32, each result rounded once.
+//
+// What bounds it.  Every value is read and written once: 7 bytes a value with
+// residual and sum, 3 without.  A row stays in registers between the sum of
+// squares and the scaling.
+//
+// Layout.  16 lanes hold a block of 128 (8 values, 16 bytes each), so its
+// largest magnitude is four shuffles away and codes go out 8 bytes a lane.
+#include "coc_f8.cuh"
+
+namespace coc {
+namespace {
+
+constexpr float kDown = 8.271806125530277e-25f;     // 2^-80
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = to_float16bit<BF16>(static_cast<uint16_t>(w[i] & 0xFFFFu));
+        f[2 * i + 1] = to_float16bit<BF16>(static_cast<uint16_t>(w[i] >> 16));
+    }
+}
+
+// The 16 lanes' block: its scale byte, and this lane's 8 codes.
+__device__ __forceinline__ uint32_t block_codes(const float (&y)[8], uint2& codes) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, f8_magnitude(y[j]));
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const uint32_t byte = f8_scale_byte(top);
+    const float f = f8_inverse(byte);
+    codes = make_uint2(f8_codes4(y[0], y[1], y[2], y[3], f), f8_codes4(y[4], y[5], y[6], y[7], f));
+    return byte;
+}
+
+// Half a warp a block of 128, kBlocksEach blocks of it in flight.
+constexpr int kQuantThreads = 256;
+constexpr int kBlocksEach = 4;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kQuantThreads) f8_quantize_kernel(const __grid_constant__ F8RowsArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int r = blockIdx.y;
+    const int blocks = (a.hidden + 127) / 128, lane16 = threadIdx.x & 15;
+    const long long all = static_cast<long long>(a.rows) * blocks;
+    const long long first = static_cast<long long>(blockIdx.x) * (kQuantThreads / 16 * kBlocksEach) + (threadIdx.x >> 4);
+    uint4 v[kBlocksEach];
+    long long row[kBlocksEach];
+    int block[kBlocksEach];
+#pragma unroll
+    for (int i = 0; i < kBlocksEach; ++i) {
+        const long long at = first + i * (kQuantThreads / 16);
+        row[i] = at / blocks;
+        block[i] = static_cast<int>(at - row[i] * blocks);
+        const int col = block[i] * 128 + lane16 * 8;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < all && col < a.hidden) v[i] = load_uint4(a.x[r] + row[i] * a.hidden + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kBlocksEach; ++i) {
+        float y[8];
+        unpack8<BF16>(v[i], y);
+        uint2 codes;
+        const uint32_t byte = block_codes(y, codes);
+        const int col = block[i] * 128 + lane16 * 8;
+        if (row[i] < a.rows && col < a.hidden) {
+            *reinterpret_cast<uint2*>(a.codes[r] + row[i] * a.hidden + col) = codes;
+            if (lane16 == 0) a.scale[r][row[i] * blocks + block[i]] = static_cast<uint8_t>(byte);
+        }
+    }
+}
+
+// blockDim.x threads a row (a multiple of 32), blockDim.y rows a block; VPT
+// pieces of 8 values a thread.
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F8RowsArgs a) {
+    __shared__ float sums[32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int r = blockIdx.y, T = blockDim.x, t = threadIdx.x;
+    const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < a.rows;
+    const int pieces = a.hidden / 8;
+    const long long base = row * a.hidden;
+
+    float s[VPT][8];
+    {
+        uint4 xv[VPT], rv[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int p = t + i * T;
+            xv[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (live && p < pieces) {
+                xv[i] = load_uint4(a.x[r] + base + 8 * p);
+                if (a.residual[r] != nullptr) rv[i] = load_uint4(a.residual[r] + base + 8 * p);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float f[8];
+            unpack8<BF16>(xv[i], s[i]);
+            if (a.residual[r] != nullptr) {
+                unpack8<BF16>(rv[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i][j] += f[j];
+                const int p = t + i * T;
+                if (live && p < pieces) {
+                    uint4 o;
+                    o.x = pack2<BF16>(__float_as_uint(s[i][0]), __float_as_uint(s[i][1]));
+                    o.y = pack2<BF16>(__float_as_uint(s[i][2]), __float_as_uint(s[i][3]));
+                    o.z = pack2<BF16>(__float_as_uint(s[i][4]), __float_as_uint(s[i][5]));
+                    o.w = pack2<BF16>(__float_as_uint(s[i][6]), __float_as_uint(s[i][7]));
+                    *reinterpret_cast<uint4*>(a.sum[r] + base + 8 * p) = o;
+                }
+            }
+        }
+    }
+
+    // the row's sum of (s f)^2, in the same order every time
+    const int warp = (threadIdx.y * T + t) >> 5, warps = T >> 5;
+    auto total = [&](float f) {
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = s[i][j] * f;
+                q = fmaf(v, v, q);
+            }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) q += __shfl_xor_sync(0xffffffffu, q, d);
+        if (warps > 1) {
+            __syncthreads();
+            if ((t & 31) == 0) sums[warp] = q;
+            __syncthreads();
+            q = 0.f;
+            for (int w = 0; w < warps; ++w) q += sums[threadIdx.y * warps + w];
+        }
+        return q;
+    };
+    float f = 1.f, q = total(1.f);
+    // Squares of values from 2^64 on overflow; the row is then taken 2^-80 times
+    // (what underflows is nothing beside them).  Every thread of a block goes in
+    // or none: the barriers inside are the block's.
+    if (__syncthreads_or(!(q <= 3.4028234663852886e38f))) {
+        const float scaled = total(kDown);
+        if (!(q <= 3.4028234663852886e38f)) {
+            f = kDown;
+            q = scaled;
+        }
+    }
+    const float eps = f == 1.f ? a.eps : a.eps * kDown * kDown;
+    const float inv = rsqrtf(q / static_cast<float>(a.hidden) + eps);
+
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int p = t + i * T;
+        float w[8], y[8];
+        const bool in = live && p < pieces;
+        unpack8<BF16>(in ? load_uint4(a.weight + 8 * p) : make_uint4(0u, 0u, 0u, 0u), w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = in ? s[i][j] * f * inv * w[j] : 0.f;
+        uint2 codes;
+        const uint32_t byte = block_codes(y, codes);
+        if (in) {
+            *reinterpret_cast<uint2*>(a.codes[r] + base + 8 * p) = codes;
+            if ((t & 15) == 0) a.scale[r][row * ((pieces + 15) / 16) + p / 16] = static_cast<uint8_t>(byte);
+        }
+    }
+}
+
+cudaError_t launch_rows(const void* kern, const F8RowsArgs& a, dim3 grid, dim3 block, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (pdl_launch()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    }
+    void* args[] = {const_cast<F8RowsArgs*>(&a)};
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+template <bool BF16>
+const void* norm_kernel(int vpt) {
+    switch (vpt) {
+        case 1: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 1>);
+        case 2: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 2>);
+        case 4: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 4>);
+        default: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 8>);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_f8_quantize(const F8RowsArgs& a, bool bf16, cudaStream_t stream) {
+    const long long all = static_cast<long long>(a.rows) * ((a.hidden + 127) / 128);
+    const int each = kQuantThreads / 16 * kBlocksEach;
+    const dim3 grid(static_cast<unsigned>((all + each - 1) / each), static_cast<unsigned>(a.R));
+    return launch_rows(bf16 ? reinterpret_cast<const void*>(f8_quantize_kernel<true>) : reinterpret_cast<const void*>(f8_quantize_kernel<false>), a,
+                       grid, dim3(kQuantThreads), stream);
+}
+
+cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStream_t stream) {
+    const int pieces = a.hidden / 8;
+    int vpt = 4;
+    while (vpt < 8 && (pieces + vpt - 1) / vpt > 1024) vpt *= 2;
+    while (vpt > 1 && static_cast<long long>(a.rows) * a.R <= sm_count && (pieces + vpt / 2 - 1) / (vpt / 2) <= 1024) vpt /= 2;
+    const int T = ((pieces + vpt - 1) / vpt + 31) / 32 * 32;
+    const int rows = T >= 128 ? 1 : 128 / T;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.rows) + rows - 1) / rows), static_cast<unsigned>(a.R));
+    return launch_rows(bf16 ? norm_kernel<true>(vpt) : norm_kernel<false>(vpt), a, grid, dim3(T, rows), stream);
+}
+
+}  // namespace coc

@@ -1,0 +1,398 @@
+// Products of 8-bit activations and weights for few rows: the weights' rows are
+// the M side of the tensor core tile, the activations' rows its N side.
+//
+// Mathematics.  Y(i, j) = sum over the shards' k-blocks b of
+// 2^(sx(i, b) + sw(j / 128, b)) sum_{t in b} x(i, t) w(j, t), accumulated in
+// fp32 in tensor memory; the gated form takes two weight tiles (gate, up) over
+// the same activations, h = silu(g) u, and quantises h per row and 128 columns,
+// which is one tile.
+//
+// What bounds it.  n k bytes of weights, read once.  A tile is 128 weight rows
+// by NT activation rows, so few rows cost the tensor cores little.
+//
+// Split.  Where the tiles do not fill the GPU, the blocks of a cluster take
+// contiguous ranges of the k-blocks; the parts meet in shared memory and are
+// added in their order.
+//
+// Roles: warp 0 copies tiles (TMA), warp 1 issues products and owns tensor
+// memory, warps 2 and 3 gather scale words, alternating; then all four warps
+// read the accumulators.
+#include <algorithm>
+#include <atomic>
+
+#include "coc_f8.cuh"
+
+namespace coc {
+namespace {
+
+constexpr int kWTile = 128 * 128;       // bytes of 128 weight rows' k-block
+constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight
+constexpr int kSfCols = 16;             // columns of a set of scale words in tensor memory
+
+template <int NT, bool GATED>
+struct SlabCfg {
+    static constexpr int WT = GATED ? 2 : 1;
+    static constexpr int STAGE = WT * kWTile + NT * 128;
+    // two blocks on an SM where a ring of at least 3 stages fits in half its shared memory
+    static constexpr int SF_BYTES = kSfStages * (WT + 1) * kScaleBlock;
+    static constexpr int HALF = 112 * 1024 - 2048 - SF_BYTES, FULL = 224 * 1024 - 2048 - SF_BYTES;
+    static constexpr bool TWO = HALF / STAGE >= 3;
+    static constexpr int S = (TWO ? HALF : FULL) / STAGE;
+    static constexpr int SUMS = WT * NT * 128 * 4;
+    static constexpr int SMEM = 1024 + S * STAGE + SF_BYTES + 256;
+    static constexpr int COLS = WT * NT + 2 * kSfCols;
+    static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(S >= 2 && S <= 16 && SUMS <= S * STAGE && SMEM <= kSlabSmemCap, "shared memory");
+    static_assert(!TWO || TMEM <= 256, "tensor memory of two blocks");
+};
+
+// 32 lanes x 16 consecutive columns: thread t receives lane (base + t).
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ float4 load_part(uint32_t addr, bool cluster) {
+    float4 v;
+    if (cluster)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int NT, bool GATED, bool BF16>
+__global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8Args p) {
+    using C = SlabCfg<NT, GATED>;
+    constexpr int WT = C::WT, S = C::S;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sf = smem + S * C::STAGE;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sf + C::SF_BYTES);
+    uint64_t* full = bars;                  // [S] tiles landed
+    uint64_t* empty = full + S;             // [S] tiles read by the products
+    uint64_t* sf_full = empty + S;          // [kSfStages] a run's scale words written
+    uint64_t* sf_empty = sf_full + kSfStages;   // [kSfStages] the run's products are done
+    uint64_t* done = sf_empty + kSfStages;  // all products are done
+    uint64_t* never = done + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
+    uint32_t* abort_word = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Ctl ctl{abort_word, p.status};
+    const int splits = p.splits, split = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int tile = static_cast<int>(blockIdx.x) / splits;
+    const int mt = tile % p.m_tiles, col_tile = tile / p.m_tiles;
+    const int nt = col_tile % p.n_tiles, r = col_tile / p.n_tiles;      // r: the AllGather's rank
+    const int row0 = mt * NT;
+    const int total = p.shards * p.kblocks;
+    const int b0 = static_cast<int>(static_cast<long long>(total) * split / splits);
+    const int b1 = static_cast<int>(static_cast<long long>(total) * (split + 1) / splits);
+    const bool ag = p.op == OP_AG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < kSfStages; ++s) {
+            mbar_init(smem_u32(&sf_full[s]), 1);
+            mbar_init(smem_u32(&sf_empty[s]), 1);
+        }
+        mbar_init(smem_u32(done), 1);
+        mbar_init(smem_u32(never), 1);
+        *abort_word = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    if (p.inject_timeout) ok = warp_wait(smem_u32(never), 0, ctl, 0x700u);
+
+    if (warp == 0) {
+        uint32_t stage = 0, phase = 0, filled = 0, parity = 0;
+        const uint64_t pol_w = make_l2_policy(p.m_tiles > 1 ? 0 : 1), pol_x = make_l2_policy(2);
+        for (int i = b0; ok && i < b1; ++i) {
+            ok = warp_wait(smem_u32(&empty[stage]), phase ^ 1u, ctl, 0x710u + stage);
+            if (!ok) break;
+            if (lane == 0) {
+                const int shard = i / p.kblocks, kc = (i - shard * p.kblocks) * 128;
+                const CUtensorMap* wm = &p.tm_w[ag ? r : shard];
+                const uint32_t fb = smem_u32(&full[stage]), dst = smem_u32(smem) + stage * C::STAGE;
+                mbar_expect_tx(fb, C::STAGE);
+                tma_load_2d_hint(dst, wm, kc, nt * 128, fb, pol_w);
+                if constexpr (GATED) tma_load_2d_hint(dst + kWTile, wm, kc, p.n + nt * 128, fb, pol_w);
+                tma_load_2d_hint(dst + WT * kWTile, &p.tm_x[ag ? 0 : shard], kc, row0, fb, pol_x);
+                filled |= 1u << stage;
+                parity = (parity & ~(1u << stage)) | (phase << stage);
+            }
+            __syncwarp();
+            if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok && lane == 0)       // no copy stays in flight into shared memory
+            for (int s = 0; s < S; ++s)
+                if (filled & (1u << s)) drain_wait(smem_u32(&full[s]), (parity >> s) & 1u, kDrainNs);
+        __syncwarp();
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = f8_idesc(128, NT);
+        uint32_t stage = 0, phase = 0;
+        int run_i = 0;
+        for (int at = b0; ok && at < b1; ++run_i) {
+            const F8Run run = f8_run(at, b1, p.kblocks);
+            const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
+            ok = warp_wait(smem_u32(&sf_full[ss]), sph, ctl, 0x720u + ss);
+            // the words two runs ago, in the same columns, have been used
+            if (ok && run_i >= 2) {
+                const int was = run_i - 2;
+                ok = warp_wait(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x730u);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sc = tmem + WT * NT + (run_i & 1) * kSfCols;
+            if (lane == 0) {
+                const uint32_t src = smem_u32(sf) + ss * (WT + 1) * kScaleBlock;
+#pragma unroll
+                for (int w = 0; w < WT + 1; ++w) tc_copy_scales(sc + 4 * w, src + w * kScaleBlock);
+            }
+            __syncwarp();
+            for (int j = 0; j < run.count; ++j, ++at) {
+                ok = warp_wait(smem_u32(&full[stage]), phase, ctl, 0x740u + stage);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t base = smem_u32(smem) + stage * C::STAGE;
+                    const uint64_t xd = make_sdesc(base + WT * kWTile, 16, 1024);
+                    const uint32_t id = f8_idesc_byte(idesc, (run.kb + j) & 3);
+#pragma unroll
+                    for (int w = 0; w < WT; ++w) {
+                        const uint64_t wd = make_sdesc(base + w * kWTile, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)      // 32 of k: 32 bytes of the swizzled row
+                            tc_mma_f8(tmem + w * NT, wd + 2 * kk, xd + 2 * kk, id, sc + 4 * w, sc + 4 * WT, (at > b0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc_commit(smem_u32(&empty[stage]));
+                    if (j == run.count - 1) tc_commit(smem_u32(&sf_empty[ss]));
+                }
+                __syncwarp();
+                if (++stage == S) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (lane == 0) {
+            tc_commit(smem_u32(done));
+            if (!ok) drain_wait(smem_u32(done), 0, kDrainNs);
+        }
+        __syncwarp();
+    } else {
+        // scale words: the weights' are one for all of a tile's rows, the activations' one a row
+        int run_i = 0;
+        for (int at = b0; ok && at < b1; ++run_i) {
+            const F8Run run = f8_run(at, b1, p.kblocks);
+            at += run.count;
+            if ((run_i & 1) != warp - 2) continue;
+            const int kb = run.kb & ~3;
+            const uint8_t* ws = p.w_scale[ag ? r : run.shard];
+            uint32_t wv[WT], xv[NT > 32 ? NT / 32 : 1];
+#pragma unroll
+            for (int w = 0; w < WT; ++w) wv[w] = load_scale_word(ws + static_cast<long long>(nt + w * p.n_tiles) * p.kblocks, kb, p.kblocks);
+#pragma unroll
+            for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) {
+                const int row = row0 + lane + 32 * i;
+                xv[i] = row < p.m && lane + 32 * i < NT
+                            ? load_scale_word(p.x_scale[ag ? 0 : run.shard] + static_cast<long long>(row) * p.kblocks, kb, p.kblocks) : 0u;
+            }
+            const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
+            ok = warp_wait(smem_u32(&sf_empty[ss]), sph ^ 1u, ctl, 0x750u + ss);
+            if (!ok) break;
+            uint8_t* dst = sf + ss * (WT + 1) * kScaleBlock;
+#pragma unroll
+            for (int w = 0; w < WT; ++w)
+                *reinterpret_cast<uint4*>(dst + w * kScaleBlock + lane * 16) = make_uint4(wv[w], wv[w], wv[w], wv[w]);
+#pragma unroll
+            for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) *reinterpret_cast<uint32_t*>(dst + WT * kScaleBlock + scale_word_at(lane + 32 * i)) = xv[i];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sf_full[ss]));
+        }
+    }
+
+    // ---- accumulators to shared memory: sums[weight tile][activation row][weight row]
+    if (ok) ok = warp_wait(smem_u32(done), 0, ctl, 0x760u);
+    tc_fence_after();
+    // every warp is through with the ring (an abort's products too: warp 1 waited for them)
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);
+    for (int c = 0; c < WT * NT; c += 16) {
+        uint32_t v[16];
+        if (b1 > b0) {
+            tmem_ld_16cols(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, v);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + 32 * warp + lane] = __uint_as_float(v[i]);
+    }
+    tc_fence_before();
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+
+    // ---- 16 threads an activation row, 8 columns each; the cluster's blocks share the rows
+    const uint32_t sums_at = smem_u32(sums);
+    for (int x = threadIdx.x + split * 128; x < NT * 16; x += 128 * splits) {
+        const int i = x >> 4, row = row0 + i, c8 = (x & 15) * 8, col = nt * 128 + c8;
+        float y[WT][8];
+#pragma unroll
+        for (int w = 0; w < WT; ++w) {
+            const uint32_t at = sums_at + ((w * NT + i) * 128 + c8) * 4;
+            for (int b = 0; b < splits; ++b) {
+                const uint32_t src = splits > 1 ? map_to_rank(at, b) : at;
+                const float4 lo = load_part(src, splits > 1), hi = load_part(src + 16, splits > 1);
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[w][j] = b == 0 ? v[j] : y[w][j] + v[j];
+            }
+        }
+        const bool in = row < p.m && col < p.n;
+        if constexpr (GATED) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[0][j] = in ? f8_gated(y[0][j], y[1][j]) : 0.f;
+                top = fmaxf(top, f8_magnitude(y[0][j]));
+            }
+#pragma unroll
+            for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const uint32_t byte = f8_scale_byte(top);
+            const float f = f8_inverse(byte);
+            if (in) {
+                uint8_t* out = static_cast<uint8_t*>(p.out[r]);
+                *reinterpret_cast<uint2*>(out + static_cast<long long>(row) * p.n + col) =
+                    make_uint2(f8_codes4(y[0][0], y[0][1], y[0][2], y[0][3], f), f8_codes4(y[0][4], y[0][5], y[0][6], y[0][7], f));
+                if (c8 == 0) p.out_scale[r][static_cast<long long>(row) * p.n_tiles + nt] = static_cast<uint8_t>(byte);
+            }
+        } else if (in) {
+            uint4 o;
+            o.x = pack2<BF16>(__float_as_uint(y[0][0]), __float_as_uint(y[0][1]));
+            o.y = pack2<BF16>(__float_as_uint(y[0][2]), __float_as_uint(y[0][3]));
+            o.z = pack2<BF16>(__float_as_uint(y[0][4]), __float_as_uint(y[0][5]));
+            o.w = pack2<BF16>(__float_as_uint(y[0][6]), __float_as_uint(y[0][7]));
+            if (p.op == OP_AR) {
+                for (int q = 0; q < p.R; ++q) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[q]) + static_cast<long long>(row) * p.n + col) = o;
+            } else {
+                const int q = ag ? r : row / p.rows_per_rank;
+                const long long at = ag ? row : row - q * p.rows_per_rank;
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[q]) + at * p.n + col) = o;
+            }
+        }
+    }
+    if (splits > 1) cluster_sync();     // no block leaves while its sums are read
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+template <int NT, bool GATED, bool BF16>
+cudaError_t launch_t(const F8Args& a, cudaStream_t stream) {
+    using C = SlabCfg<NT, GATED>;
+    auto kern = f8_slab_kernel<NT, GATED, BF16>;
+    static std::atomic<unsigned char> smem_set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1) * a.splits), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    if (pdl_launch()) {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <bool GATED, bool BF16>
+cudaError_t launch_n(const F8Args& a, int nt, cudaStream_t stream) {
+    switch (nt) {
+        case 16: return launch_t<16, GATED, BF16>(a, stream);
+        case 32: return launch_t<32, GATED, BF16>(a, stream);
+        case 64: return launch_t<64, GATED, BF16>(a, stream);
+        default: return launch_t<128, GATED, BF16>(a, stream);
+    }
+}
+
+}  // namespace
+
+int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+
+cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_count, cudaStream_t stream) {
+    F8Args a = args;
+    const int nt = f8_slab_rows(a.m);
+    a.m_tiles = (a.m + nt - 1) / nt;
+    // ranges of the contraction: up to 8, while the tiles leave SMs free
+    const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1);
+    const int total = a.shards * a.kblocks;
+    a.splits = 1;
+    while (a.splits < 8 && tiles * a.splits * 2 <= sm_count && total >= 4 * a.splits) a.splits *= 2;
+    if (gated) return launch_n<true, true>(a, nt, stream);
+    return bf16 ? launch_n<false, true>(a, nt, stream) : launch_n<false, false>(a, nt, stream);
+}
+
+// ---- the shards' activations one after another (AllGather of shards that lie apart)
+namespace {
+__global__ void __launch_bounds__(256) f8_stack_kernel(const __grid_constant__ F8StackArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int r = blockIdx.y;
+    const long long step = static_cast<long long>(gridDim.x) * blockDim.x, first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    uint4* dst = reinterpret_cast<uint4*>(a.x_dst) + r * a.vecs;
+    for (long long i = first; i < a.vecs; i += step) dst[i] = load_uint4(reinterpret_cast<const uint16_t*>(a.x[r]) + 8 * i);
+    for (long long i = first; i < a.scale_bytes; i += step) a.scale_dst[r * a.scale_bytes + i] = static_cast<uint8_t>(load_byte(a.scale[r] + i));
+}
+}  // namespace
+
+cudaError_t launch_f8_stack(const F8StackArgs& a, int sm_count, cudaStream_t stream) {
+    const long long work = std::max(a.vecs, a.scale_bytes);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((work + 255) / 256, 4LL * sm_count)), static_cast<unsigned>(a.R), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (pdl_launch()) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, f8_stack_kernel, a);
+}
+
+}  // namespace coc

@@ -246,6 +246,59 @@ struct W4Args {
 };
 cudaError_t launch_w4(const W4Args& a, bool bf16, int sm_count, cudaStream_t stream);
 
+// 8-bit floating point: e4m3 codes with a power-of-two scale (e8m0 byte) for
+// 128 columns of a row or 128 x 128 of a weight.  Rows to codes
+// (coc_f8_rows.cu): hidden a multiple of 16; the norm's at most
+// kF8MaxHidden.  residual[r] NULL: none, and sum[r] is not written.
+constexpr int kF8MaxHidden = 65536;
+struct F8RowsArgs {
+    const uint16_t* x[COC_MAX_RANKS];         // rows x hidden
+    const uint16_t* residual[COC_MAX_RANKS];
+    uint16_t* sum[COC_MAX_RANKS];
+    uint8_t* codes[COC_MAX_RANKS];            // rows x hidden
+    uint8_t* scale[COC_MAX_RANKS];            // rows x ceil(hidden / 128)
+    const uint16_t* weight;                   // hidden
+    float eps;
+    int R, rows, hidden;
+};
+cudaError_t launch_f8_quantize(const F8RowsArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStream_t stream);
+
+// Products of codes.  op: OP_AR, OP_RS (m rows, the shards summed) or OP_AG
+// (m gathered rows in x[0], every rank's n columns); gated: OP_AG with 2 n
+// weight rows a rank, gate first, whose result is codes and scales.  Maps:
+// 128 columns x 128 rows of a weight, 128 x f8_slab_rows(m) of x
+// (coc_f8_slab.cu), 128-byte swizzle, zero past the ends.
+struct F8Args {
+    CUtensorMap tm_x[COC_MAX_RANKS];
+    CUtensorMap tm_w[COC_MAX_RANKS];
+    const uint8_t* x_scale[COC_MAX_RANKS];    // m x kblocks
+    const uint8_t* w_scale[COC_MAX_RANKS];    // n_tiles (gated: 2 n_tiles) x kblocks
+    void* out[COC_MAX_RANKS];
+    uint8_t* out_scale[COC_MAX_RANKS];        // gated: m x n_tiles
+    unsigned* status;
+    int op, R, m, n;
+    int shards;                               // summed: R (OP_AG: 1)
+    int kblocks;                              // ceil(k / 128) of a shard
+    int n_tiles;                              // ceil(n / 128)
+    int rows_per_rank;                        // OP_RS: m / R
+    int inject_timeout;
+    int m_tiles, splits;                      // set by the launch
+};
+int f8_slab_rows(int64_t m);
+cudaError_t launch_f8_slab(const F8Args& a, bool gated, bool bf16, int sm_count, cudaStream_t stream);
+// R pieces of activations after one another: vecs 16-byte pieces of codes and
+// scale_bytes scales a rank.
+struct F8StackArgs {
+    const uint8_t* x[COC_MAX_RANKS];
+    const uint8_t* scale[COC_MAX_RANKS];
+    uint8_t* x_dst;
+    uint8_t* scale_dst;
+    long long vecs, scale_bytes;
+    int R;
+};
+cudaError_t launch_f8_stack(const F8StackArgs& a, int sm_count, cudaStream_t stream);
+
 // Host-side launch helpers implemented in coc_kernel.cu.  `pair` selects the
 // 2-SM variant (a cluster of two CTAs per 256-row tile; grid = 2 x pairs);
 // otherwise one CTA per 128-row tile.

@@ -1,0 +1,107 @@
+"""Plain 64-bit forms of the 8-bit operators, and the bounds of what a code may be off."""
+import torch
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+MIN_EXP = -100
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+def scale_exp(top):
+    """Exponent of the least power of two S with top <= 448 S, at least -100 (top: float64)."""
+    m, e = torch.frexp(top / 448.0)
+    e = torch.where(m > 0.5, e, e - 1)
+    return torch.where(top > 0, e, torch.full_like(e, MIN_EXP)).clamp(min=MIN_EXP)
+
+
+def pow2(e):
+    """2**e in float64, by its bits."""
+    return ((e.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
+def block_top(y):
+    """Largest finite magnitude of each row and 128 columns."""
+    rows, h = y.shape
+    mag = torch.where(y.isfinite(), y.abs(), torch.zeros_like(y))
+    return torch.nn.functional.pad(mag, (0, blocks(h) * 128 - h)).view(rows, blocks(h), 128).amax(2)
+
+
+def spread(s, h):
+    return s.repeat_interleave(128, 1)[:, :h]
+
+
+def round_e4m3(q):
+    """Nearest e4m3 value (ties to even), saturating, of float64 values."""
+    mag = q.abs().clamp(max=448.0)
+    _, e = torch.frexp(mag)
+    ulp = pow2((e - 1).clamp(min=-6) - 3)
+    return torch.sign(q) * torch.minimum(torch.round(mag / ulp) * ulp, torch.full_like(mag, 448.0))
+
+
+def value(scale):
+    """float64 values of scales (255: NaN)."""
+    b = scale.cpu().view(torch.uint8).to(torch.int64)
+    return torch.where(b == 255, torch.full((), float("nan"), dtype=torch.float64), pow2(b - 127))
+
+
+def real(codes, scale):
+    """float64 values of an activation."""
+    c = codes.cpu().view(torch.uint8).view(E4M3).double()
+    return c * spread(value(scale), codes.shape[1])
+
+
+def real_weight(codes, scale):
+    n, k = codes.shape
+    return codes.cpu().view(torch.uint8).view(E4M3).double() * spread(value(scale), k).repeat_interleave(128, 0)[:n]
+
+
+def check_codes(codes, scale, y, off, what=""):
+    """codes and scale against float64 values y that the kernel has to within `off` (a tensor like y): the scale is that of a
+    largest magnitude within off, and a code is off by half a step of e4m3 and off."""
+    h = y.shape[1]
+    finite = y.isfinite()
+    off = torch.where(finite, off, torch.zeros_like(off))
+    mag = torch.where(finite, y.abs(), torch.zeros_like(y))
+    lo, hi = scale_exp(block_top((mag - off).clamp(min=0))), scale_exp(block_top(mag + off))
+    e = scale.cpu().view(torch.uint8).to(torch.int32) - 127
+    assert e.shape == lo.shape, (what, e.shape, lo.shape)
+    assert ((lo <= e) & (e <= hi)).all(), f"{what}: a scale is another than {int((lo > e).sum() + (e > hi).sum())} blocks' values give"
+    s = spread(pow2(e), h)
+    got = codes.cpu().view(torch.uint8).view(E4M3).double() * s
+    assert torch.equal(got.isnan(), y.isnan()), f"{what}: NaN where there is none, or none where there is"
+    q = torch.where(finite, (mag + off) / s, torch.zeros_like(y))
+    _, x = torch.frexp(q)
+    half = pow2((x - 1).clamp(min=-6) - 4) * s
+    want = torch.where(y.isinf(), torch.sign(y) * 448.0 * s, y)
+    err = torch.where(y.isnan(), torch.zeros_like(y), (got - want).abs())
+    bad = err > half * finite + off
+    assert not bad.any(), f"{what}: {int(bad.sum())} codes out of bounds, worst {float((err / (half + off)).max()):.3f}"
+
+
+def activation(g, rows, k, spread_=0.5):
+    """Codes and scales of normal rows with a few strong columns."""
+    x = torch.randn(rows, k, generator=g, dtype=torch.float64) * torch.exp(spread_ * torch.randn(1, k, generator=g, dtype=torch.float64))
+    return quantize(x)
+
+
+def quantize(x):
+    e = scale_exp(block_top(x))
+    q = round_e4m3(x / spread(pow2(e), x.shape[1]))
+    return q.to(torch.float32).to(E4M3), (e + 127).to(torch.uint8).view(E8M0)
+
+
+def product(xs, x_scales, ws, w_scales):
+    """(sum of the ranks' products, sum of the magnitudes) in float64."""
+    y = size = 0.0
+    for x, xs_, w, ws_ in zip(xs, x_scales, ws, w_scales):
+        a, b = real(x, xs_), real_weight(w, ws_)
+        y = y + a @ b.t()
+        size = size + a.abs() @ b.abs().t()
+    return y, size
+
+
+def sum_error(size, K, splits=8):
+    """fp32 sums of exact products, 32 at a time and `splits` ranges joined: 2**-22 a step covers an addition that truncates."""
+    return (K / 32 + splits + 8) * 2.0 ** -22 * size + 2.0 ** -140

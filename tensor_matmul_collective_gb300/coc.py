@@ -156,7 +156,9 @@ def _marshal():
                           RuntimeWarning, stacklevel=3)
         _native = False if m is None else (
             m, *(ctypes.cast(f, ctypes.c_void_p).value for f in (L.coc_kv_cache_append, L.coc_kv_cache_attention,
-                                                                L.coc_matmul_all_reduce_w4a16)))
+                                                                L.coc_matmul_all_reduce_w4a16, L.coc_quantize_f8,
+                                                                L.coc_add_rms_norm_f8, L.coc_fused_matmul_f8,
+                                                                L.coc_all_gather_gated_matmul_f8)))
     return _native
 
 
@@ -848,6 +850,13 @@ def quantize_f8(xs, outs=None, scales=None, stream=None):
     hidden float8_e4m3fn, scales[r]: rows x ceil(hidden/128) float8_e8m0fnu,
     the least power of two that keeps 128 values within e4m3 (at least 2**-100).
     New ones are parts of one allocation each."""
+    native = _native or _marshal()
+    if native:
+        done = native[0].quantize_f8(native[4], xs, outs, scales, None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1:]
     R, rows, hidden, dt, dev = _f8_rows_shape(xs)
     outs, op = _head_outs(outs, "outs", R, (rows, hidden), torch.float8_e4m3fn, dev, stream)
     scales, sp = _head_outs(scales, "scales", R, (rows, _blocks(hidden)), torch.float8_e8m0fnu, dev, stream)
@@ -864,6 +873,13 @@ def add_rms_norm_f8(xs, weight, residuals=None, eps: float = 1e-6, outs=None, sc
     be given as sums[r]); codes[r], scales[r] = s / sqrt(mean(s**2) + eps) * weight
     as quantize_f8 gives them.  weight: hidden values in the type of xs, the
     same for every rank; hidden up to 65536."""
+    native = _native or _marshal()
+    if native:
+        done = native[0].norm_f8(native[5], xs, weight, residuals, eps, outs, scales, sums, None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1:]
     R, rows, hidden, dt, dev = _f8_rows_shape(xs)
     _check_list([weight], "weight", (hidden,), dt, dev)
     if residuals is None:
@@ -903,6 +919,14 @@ def _f8_prep(xs, x_scales, ws, w_scales, halves: int = 1):
 
 
 def _fused_f8(code, xs, x_scales, ws, w_scales, outs, dtype, stream):
+    native = _native or _marshal()
+    if native:
+        done = native[0].matmul_f8(native[6], code, xs, x_scales, ws, w_scales, outs, None if dtype is None else _dtype_code(dtype),
+                                   None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1]
     R, rows, k, n, dev = _f8_prep(xs, x_scales, ws, w_scales)
     if dtype is None:
         dtype = torch.bfloat16 if not outs or not isinstance(outs[0], torch.Tensor) else outs[0].dtype
@@ -948,6 +972,13 @@ def all_gather_gated_matmul_f8(xs, x_scales, ws, w_scales, outs=None, scales=Non
     codes, the gate's rows, then the up projection's, w_scales[r]
     (2 ceil(f_shard/128)) x ceil(k/128) (f8_pack with parts=2); f_shard a multiple of 16.
     codes[r]: (R m_shard) x f_shard, scales[r]: (R m_shard) x ceil(f_shard/128)."""
+    native = _native or _marshal()
+    if native:
+        done = native[0].gated_f8(native[7], xs, x_scales, ws, w_scales, outs, scales, None if stream is None else _stream(stream))
+        if done is not None:
+            if done[0] != OK:
+                _check(done[0])
+            return done[1:]
     R, rows, k, f, dev = _f8_prep(xs, x_scales, ws, w_scales, halves=2)
     outs, op = _head_outs(outs, "outs", R, (R * rows, f), torch.float8_e4m3fn, dev, stream)
     scales, sp = _head_outs(scales, "scales", R, (R * rows, _blocks(f)), torch.float8_e8m0fnu, dev, stream)

@@ -57,8 +57,8 @@ struct Ranks {
 
 const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// The first tensor of a list, on the current CUDA device, which is `index` where that is given, and of a 16-bit type.
-const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1) {
+// The first tensor of a list, on the current CUDA device, which is `index` where that is given, and of a 16-bit type (codes: e4m3).
+const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1, bool codes = false) {
     PyObject* x = nullptr;
     if (PyList_Check(o) && PyList_GET_SIZE(o) > 0) {
         *R = PyList_GET_SIZE(o);
@@ -70,6 +70,7 @@ const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1) {
     const at::Tensor* t = x != nullptr ? tensor_of(x) : nullptr;
     if (t == nullptr || *R > COC_MAX_RANKS || !t->is_cuda() || t->device().index() != c10::cuda::current_device()) return nullptr;
     if (index >= 0 && t->device().index() != index) return nullptr;
+    if (codes) return t->scalar_type() == at::kFloat8_e4m3fn ? t : nullptr;
     return t->scalar_type() == at::kHalf || t->scalar_type() == at::kBFloat16 ? t : nullptr;
 }
 
@@ -79,11 +80,11 @@ coc_dtype_t code_of(const at::Tensor& t) { return t.scalar_type() == at::kBFloat
 // New ones of a call on another than the current stream are that stream's
 // memory (what the current stream has freed may still be in use there), and the
 // current stream, on which the caller goes on with them, is noted as a user.
-bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor& like, coc_stream_t stream, PyObject** list,
-             void* (&p)[COC_MAX_RANKS]) {
+bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, at::ScalarType dt, const at::Device& dev, coc_stream_t stream,
+             PyObject** list, void* (&p)[COC_MAX_RANKS]) {
     if (given != Py_None) {
         Ranks o;
-        if (!o.take(given, R, like.scalar_type(), like.device()) || !o.packed(R, shape)) return false;
+        if (!o.take(given, R, dt, dev) || !o.packed(R, shape)) return false;
         *list = PySequence_List(given);
         for (int64_t r = 0; r < R; ++r) p[r] = const_cast<void*>(o.p[r]);
         return *list != nullptr;
@@ -92,8 +93,8 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, const at::Tensor
     const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream();
     const bool other = reinterpret_cast<cudaStream_t>(stream) != now.stream();
     c10::cuda::OptionalCUDAStreamGuard on;
-    if (other) on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), like.device().index()));
-    const at::TensorOptions opt = at::TensorOptions().dtype(like.scalar_type()).device(like.device());
+    if (other) on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), dev.index()));
+    const at::TensorOptions opt = at::TensorOptions().dtype(dt).device(dev);
     if (R == 1) {
         at::Tensor t = at::empty(shape, opt);
         if (other) t.record_stream(now);
@@ -197,7 +198,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* qo[COC_MAX_RANKS] = {};
     if (a[9] != Py_None) {
         if (!q.take(a[9], R, dt, dev) || !q.heads(R, T, d, &hq, qs)) return none();
-        if (!outputs(a[10], R, {T, hq, d}, *k0, stream, &list, qo)) return PyErr_Occurred() ? nullptr : none();
+        if (!outputs(a[10], R, {T, hq, d}, dt, dev, stream, &list, qo)) return PyErr_Occurred() ? nullptr : none();
     } else {
         if (a[10] != Py_None) return none();
         list = none();
@@ -236,7 +237,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[11], &stream)) return nullptr;
     PyObject* list = nullptr;
     void* out[COC_MAX_RANKS];
-    if (!outputs(a[10], R, {T, hq, d}, *q0, stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
+    if (!outputs(a[10], R, {T, hq, d}, q0->scalar_type(), q0->device(), stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(cache, T, ix.seqs, static_cast<int>(hq), q.p, qs, out, ix.table, ix.width, ix.lens, ix.cu, static_cast<float>(scale), window,
@@ -271,7 +272,7 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[7], &stream)) return nullptr;
     PyObject* list = nullptr;
     void* out[COC_MAX_RANKS];
-    if (!outputs(a[6], R, {m, cols}, *x0, stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
+    if (!outputs(a[6], R, {m, cols}, dt, dev, stream, &list, out)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(R), m, cols, k, x.p, w.p, s.p, zero ? z.p : nullptr, group, out, code_of(*x0), stream);
@@ -280,7 +281,169 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Up to three lists of outputs; those not handed on are dropped.
+struct Lists {
+    PyObject* l[3] = {nullptr, nullptr, nullptr};
+    void* p[3][COC_MAX_RANKS] = {};
+    ~Lists() {
+        for (PyObject* o : l) Py_XDECREF(o);
+    }
+    PyObject* done(coc_status_t st, int n) {
+        PyObject* r = PyTuple_New(n + 1);
+        if (r == nullptr) return nullptr;
+        PyTuple_SET_ITEM(r, 0, PyLong_FromLong(static_cast<long>(st)));
+        for (int i = 0; i < n; ++i) {
+            PyTuple_SET_ITEM(r, i + 1, l[i] != nullptr ? l[i] : none());
+            l[i] = nullptr;
+        }
+        return r;
+    }
+};
+
+int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
+
+// (entry point, xs, outs, scales, stream) -> (status, codes, scales)
+PyObject* quantize_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 5) return none();
+    const auto fn = reinterpret_cast<decltype(&coc_quantize_f8)>(PyLong_AsVoidPtr(a[0]));
+    if (fn == nullptr) return none();
+    int64_t R = 0;
+    const at::Tensor* x0 = first_of(a[1], &R);
+    if (x0 == nullptr || x0->dim() != 2) return none();
+    const int64_t rows = x0->size(0), h = x0->size(1);
+    const at::Device dev = x0->device();
+    Ranks x;
+    if (!x.take(a[1], R, x0->scalar_type(), dev) || !x.packed(R, {rows, h})) return none();
+    coc_stream_t stream;
+    if (!stream_of(a[4], &stream)) return nullptr;
+    Lists o;
+    if (!outputs(a[2], R, {rows, h}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) ||
+        !outputs(a[3], R, {rows, f8_blocks(h)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]))
+        return PyErr_Occurred() ? nullptr : none();
+    coc_status_t st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn(static_cast<int>(R), rows, h, x.p, o.p[0], o.p[1], code_of(*x0), stream);
+    Py_END_ALLOW_THREADS
+    return o.done(st, 2);
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry point, xs, weight, residuals, eps, outs, scales, sums, stream) -> (status, codes, scales, sums)
+PyObject* norm_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 9) return none();
+    const auto fn = reinterpret_cast<decltype(&coc_add_rms_norm_f8)>(PyLong_AsVoidPtr(a[0]));
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (PyErr_Occurred()) return nullptr;
+    if (fn == nullptr) return none();
+    int64_t R = 0;
+    const at::Tensor* x0 = first_of(a[1], &R);
+    const at::Tensor* w = tensor_of(a[2]);
+    if (x0 == nullptr || x0->dim() != 2 || w == nullptr) return none();
+    const int64_t rows = x0->size(0), h = x0->size(1);
+    const at::ScalarType dt = x0->scalar_type();
+    const at::Device dev = x0->device();
+    Ranks x, res;
+    if (!x.take(a[1], R, dt, dev) || !x.packed(R, {rows, h})) return none();
+    if (w->scalar_type() != dt || w->device() != dev || w->dim() != 1 || w->size(0) != h || !w->is_contiguous()) return none();
+    const bool add = a[3] != Py_None;
+    if (add ? !res.take(a[3], R, dt, dev) || !res.packed(R, {rows, h}) : a[7] != Py_None) return none();
+    coc_stream_t stream;
+    if (!stream_of(a[8], &stream)) return nullptr;
+    Lists o;
+    if (!outputs(a[5], R, {rows, h}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) ||
+        !outputs(a[6], R, {rows, f8_blocks(h)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]) ||
+        (add && !outputs(a[7], R, {rows, h}, dt, dev, stream, &o.l[2], o.p[2])))
+        return PyErr_Occurred() ? nullptr : none();
+    coc_status_t st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn(static_cast<int>(R), rows, h, x.p, add ? res.p : nullptr, w->data_ptr(), static_cast<float>(eps), add ? o.p[2] : nullptr, o.p[0],
+            o.p[1], code_of(*x0), stream);
+    Py_END_ALLOW_THREADS
+    return o.done(st, 3);
+    END_HANDLE_TH_ERRORS
+}
+
+// Operands of an 8-bit product: codes and scales of R ranks.
+struct F8Operands {
+    Ranks x, xs, w, ws;
+    int64_t R = 0, rows = 0, k = 0, n = 0;          // n: columns (gated: of a half)
+    c10::optional<at::Device> dev;
+    bool take(PyObject* const* a, int64_t halves) {
+        const at::Tensor* x0 = first_of(a[0], &R, -1, true);
+        if (x0 == nullptr || x0->dim() != 2) return false;
+        rows = x0->size(0);
+        k = x0->size(1);
+        dev = x0->device();
+        if (!x.take(a[0], R, at::kFloat8_e4m3fn, *dev) || !x.packed(R, {rows, k}) || !xs.take(a[1], R, at::kFloat8_e8m0fnu, *dev) ||
+            !xs.packed(R, {rows, f8_blocks(k)}) || !w.take(a[2], R, at::kFloat8_e4m3fn, *dev) || w.t[0]->dim() != 2 ||
+            w.t[0]->size(0) % halves != 0)
+            return false;
+        n = w.t[0]->size(0) / halves;
+        return w.packed(R, {halves * n, k}) && ws.take(a[3], R, at::kFloat8_e8m0fnu, *dev) &&
+               ws.packed(R, {halves * f8_blocks(n), f8_blocks(k)});
+    }
+};
+
+// (entry point, op, xs, x_scales, ws, w_scales, outs, dtype code or None, stream) -> (status, outs)
+PyObject* matmul_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 9) return none();
+    const auto fn = reinterpret_cast<decltype(&coc_fused_matmul_f8)>(PyLong_AsVoidPtr(a[0]));
+    const long op = PyLong_AsLong(a[1]), code = a[7] == Py_None ? -1 : PyLong_AsLong(a[7]);
+    if (PyErr_Occurred()) return nullptr;
+    F8Operands in;
+    if (fn == nullptr || !in.take(a + 2, 1)) return none();
+    if (op == COC_OP_REDUCE_SCATTER && in.rows % in.R != 0) return none();
+    coc_dtype_t dt = code == COC_FP16 ? COC_FP16 : COC_BF16;
+    if (code < 0 && a[6] != Py_None) {
+        int64_t given = 0;
+        const at::Tensor* o0 = first_of(a[6], &given);
+        if (o0 == nullptr) return none();
+        dt = code_of(*o0);
+    }
+    const int64_t m = op == COC_OP_REDUCE_SCATTER ? in.rows / in.R : op == COC_OP_ALL_GATHER ? in.R * in.rows : in.rows;
+    coc_stream_t stream;
+    if (!stream_of(a[8], &stream)) return nullptr;
+    Lists o;
+    if (!outputs(a[6], in.R, {m, in.n}, dt == COC_BF16 ? at::kBFloat16 : at::kHalf, *in.dev, stream, &o.l[0], o.p[0]))
+        return PyErr_Occurred() ? nullptr : none();
+    coc_status_t st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn(static_cast<coc_op_t>(op), static_cast<int>(in.R), in.rows, in.n, in.k, in.x.p, in.xs.p, in.w.p, in.ws.p, o.p[0], dt, stream);
+    Py_END_ALLOW_THREADS
+    return o.done(st, 1);
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry point, xs, x_scales, ws, w_scales, outs, scales, stream) -> (status, codes, scales)
+PyObject* gated_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 8) return none();
+    const auto fn = reinterpret_cast<decltype(&coc_all_gather_gated_matmul_f8)>(PyLong_AsVoidPtr(a[0]));
+    F8Operands in;
+    if (fn == nullptr || !in.take(a + 1, 2)) return none();
+    coc_stream_t stream;
+    if (!stream_of(a[7], &stream)) return nullptr;
+    Lists o;
+    const int64_t m = in.R * in.rows;
+    if (!outputs(a[5], in.R, {m, in.n}, at::kFloat8_e4m3fn, *in.dev, stream, &o.l[0], o.p[0]) ||
+        !outputs(a[6], in.R, {m, f8_blocks(in.n)}, at::kFloat8_e8m0fnu, *in.dev, stream, &o.l[1], o.p[1]))
+        return PyErr_Occurred() ? nullptr : none();
+    coc_status_t st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn(static_cast<int>(in.R), in.rows, in.n, in.k, in.x.p, in.xs.p, in.w.p, in.ws.p, o.p[0], o.p[1], stream);
+    Py_END_ALLOW_THREADS
+    return o.done(st, 2);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
+    {"quantize_f8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantize_f8)), METH_FASTCALL, nullptr},
+    {"norm_f8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_f8)), METH_FASTCALL, nullptr},
+    {"matmul_f8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(matmul_f8)), METH_FASTCALL, nullptr},
+    {"gated_f8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(gated_f8)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attend)), METH_FASTCALL, nullptr},
     {"w4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(w4)), METH_FASTCALL, nullptr},

@@ -130,7 +130,8 @@
  *     (w8A16 also 4),
  *     COC_SLAB_SPLIT=1|2|4 and COC_SLAB_KPS=1|2|4 (its slab width in
  *     64-column groups, CTAs per slab, k-blocks per stage; 256-column slabs
- *     take one k-block per stage), COC_PDL=0 (the kernels launched in
+ *     take one k-block per stage), COC_F8_TILE=0|1 (8-bit products by slabs
+ *     of weight rows or by tiles of CTA pairs), COC_PDL=0 (the kernels launched in
  *     plain stream order instead of as programmatic dependent launches,
  *     which run their set-up while the previous kernel in the stream
  *     finishes).  Forcing one can change the last bit of

@@ -1881,13 +1881,14 @@ static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n
             s0 = g.scale_dst;
         }
     }
+    const bool tiles = f8_use_tiles(op, gated, R, m, n, k, ds->sm_count);
     for (int r = 0; r < R && needed && st == COC_OK; ++r) {
         const uint64_t w_rows = static_cast<uint64_t>(gated ? 2 * n : n);
         st = encode(&a.tm_w[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, w[r], k, w_rows, k, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
         a.w_scale[r] = static_cast<const uint8_t*>(w_scale[r]);
         if (st == COC_OK && (!ag || r == 0)) {
-            st = encode(&a.tm_x[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, ag ? x0 : x[r], k, m, k, 128, static_cast<uint32_t>(f8_slab_rows(m)),
-                        CU_TENSOR_MAP_SWIZZLE_128B);
+            st = encode(&a.tm_x[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, ag ? x0 : x[r], k, m, k, 128,
+                        static_cast<uint32_t>(tiles ? 128 : f8_slab_rows(m)), CU_TENSOR_MAP_SWIZZLE_128B);
             a.x_scale[r] = ag ? s0 : static_cast<const uint8_t*>(x_scale[r]);
         }
     }
@@ -1906,7 +1907,7 @@ static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n
     a.kblocks = static_cast<int>(kblocks);
     a.n_tiles = static_cast<int>(n_tiles);
     a.rows_per_rank = op == OP_RS ? static_cast<int>(m / R) : static_cast<int>(m);
-    const cudaError_t e = launch_f8_slab(a, gated, dt == COC_BF16, ds->sm_count, str);
+    const cudaError_t e = tiles ? launch_f8_tile(a, gated, dt == COC_BF16, str) : launch_f8_slab(a, gated, dt == COC_BF16, ds->sm_count, str);
     if (e != cudaSuccess) st = cuda_fail(e, "8-bit product launch");
     return scratch_release(str, sc, st);
 }

@@ -19,6 +19,7 @@
 // read the accumulators.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 
 #include "coc_f8.cuh"
 
@@ -350,6 +351,11 @@ cudaError_t launch_n(const F8Args& a, int nt, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
+    if (const char* e = std::getenv("COC_F8_TILE")) return std::atoi(e) != 0;
+    return m > 512;
+}
 
 int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 

@@ -268,7 +268,7 @@ cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStr
 // (m gathered rows in x[0], every rank's n columns); gated: OP_AG with 2 n
 // weight rows a rank, gate first, whose result is codes and scales.  Maps:
 // 128 columns x 128 rows of a weight, 128 x f8_slab_rows(m) of x
-// (coc_f8_slab.cu), 128-byte swizzle, zero past the ends.
+// (coc_f8_slab.cu) or 128 x 128 (coc_f8_tile.cu), 128-byte swizzle, zero past the ends.
 struct F8Args {
     CUtensorMap tm_x[COC_MAX_RANKS];
     CUtensorMap tm_w[COC_MAX_RANKS];
@@ -283,9 +283,13 @@ struct F8Args {
     int n_tiles;                              // ceil(n / 128)
     int rows_per_rank;                        // OP_RS: m / R
     int inject_timeout;
-    int m_tiles, splits;                      // set by the launch
+    int m_tiles, splits, group_mt;            // set by the launch
 };
+// Which kernel takes m rows (sizes as in F8Args): tiles of CTA pairs, or slabs
+// of weight rows; and the rows of their X maps' boxes (tiles: 128).
+bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count);
 int f8_slab_rows(int64_t m);
+cudaError_t launch_f8_tile(const F8Args& a, bool gated, bool bf16, cudaStream_t stream);
 cudaError_t launch_f8_slab(const F8Args& a, bool gated, bool bf16, int sm_count, cudaStream_t stream);
 // R pieces of activations after one another: vecs 16-byte pieces of codes and
 // scale_bytes scales a rank.

@@ -37,6 +37,13 @@ def check(out, ref, size, K, dt):
     assert (err <= bound).all(), f"worst {float((err / bound).max()):.3f} of the bound"
 
 
+@pytest.fixture(params=["", "0", "1"], ids=["rule", "slab", "tile"])
+def kernel(request, monkeypatch):
+    """The kernel by its rule, or either one at every size."""
+    if request.param:
+        monkeypatch.setenv("COC_F8_TILE", request.param)
+
+
 CASES = [
     # R, m, n, k, dtype: one tile and less, ragged everywhere, many tiles, every number of rows a tile takes
     (1, 1, 8, 16, BF), (1, 1, 128, 128, HF), (1, 3, 136, 144, BF), (2, 2, 264, 512, HF), (1, 16, 1000, 640, BF), (4, 4, 72, 1040, BF),
@@ -47,7 +54,7 @@ CASES = [
 
 
 @pytest.mark.parametrize("R,m,n,k,dt", CASES)
-def test_all_reduce(R, m, n, k, dt):
+def test_all_reduce(R, m, n, k, dt, kernel):
     x, xs, w, ws = make(R, m, n, k, m + n + k)
     outs = coc.matmul_all_reduce_f8(*dev(x, xs, w, ws), dtype=dt)
     coc.sync_status()
@@ -57,7 +64,7 @@ def test_all_reduce(R, m, n, k, dt):
 
 
 @pytest.mark.parametrize("R,m,n,k,dt", [c for c in CASES if c[1] % c[0] == 0])
-def test_reduce_scatter_is_all_reduce_in_rows(R, m, n, k, dt):
+def test_reduce_scatter_is_all_reduce_in_rows(R, m, n, k, dt, kernel):
     x, xs, w, ws = make(R, m, n, k, m + n + k)
     d = dev(x, xs, w, ws)
     outs = coc.matmul_reduce_scatter_f8(*d, dtype=dt)
@@ -69,7 +76,7 @@ def test_reduce_scatter_is_all_reduce_in_rows(R, m, n, k, dt):
 
 @pytest.mark.parametrize("apart", [False, True])
 @pytest.mark.parametrize("R,m,n,k,dt", CASES)
-def test_all_gather(R, m, n, k, dt, apart):
+def test_all_gather(R, m, n, k, dt, apart, kernel):
     m = -(-m // R)
     x, xs, w, ws = make(R, m, n, k, m + n + k)
     d = dev(x, xs, w, ws)
@@ -89,7 +96,7 @@ GATED = [(1, 1, 16, 16), (1, 1, 1376, 256), (1, 2, 128, 640), (2, 3, 144, 144), 
 
 
 @pytest.mark.parametrize("R,m,f,k", GATED)
-def test_gated(R, m, f, k):
+def test_gated(R, m, f, k, kernel):
     x, xs, w, ws = make(R, m, 2 * f, k, m + f + k, parts=2)
     codes, scales = coc.all_gather_gated_matmul_f8(*dev(x, xs, w, ws))
     coc.sync_status()
@@ -105,7 +112,7 @@ def test_gated(R, m, f, k):
         f8.check_codes(codes[r], scales[r], silu * u, off, f"rank {r}")
 
 
-def test_scales_of_every_kind_reach_their_values():
+def test_scales_of_every_kind_reach_their_values(kernel):
     """Codes of one value, scales that differ by row, block and position in the word: exact sums of powers of two."""
     m, n, k = 40, 256, 128 * 11
     g = torch.Generator().manual_seed(5)
@@ -119,7 +126,7 @@ def test_scales_of_every_kind_reach_their_values():
 
 
 @pytest.mark.parametrize("a,b", [(0, 0), (27, 27), (1, 254), (254, 1), (100, 200), (247, 27)])
-def test_extreme_scales(a, b):
+def test_extreme_scales(a, b, kernel):
     """The product of the scales is taken in the range of fp32: it overflows or goes to nothing only where the result does."""
     m, n, k = 3, 16, 256
     g = torch.Generator().manual_seed(a + b)
@@ -131,7 +138,7 @@ def test_extreme_scales(a, b):
     check(out, ref, size, k, BF)
 
 
-def test_nan_and_bad_scales_stay_in_their_rows():
+def test_nan_and_bad_scales_stay_in_their_rows(kernel):
     m, n, k = 20, 264, 384
     x, xs, w, ws = make(1, m, n, k, 9)
     clean = coc.matmul_all_reduce_f8(*dev(x, xs, w, ws))[0].cpu()
@@ -146,7 +153,7 @@ def test_nan_and_bad_scales_stay_in_their_rows():
     assert torch.equal(out[~bad], clean[~bad])
 
 
-def test_inner_zero_writes_zeros():
+def test_inner_zero_writes_zeros(kernel):
     x, w = torch.empty(5, 0, dtype=f8.E4M3, device=DEV), torch.empty(24, 0, dtype=f8.E4M3, device=DEV)
     xs, ws = torch.empty(5, 0, dtype=f8.E8M0, device=DEV), torch.empty(1, 0, dtype=f8.E8M0, device=DEV)
     out = [torch.full((5, 24), 7.0, dtype=BF, device=DEV)]
@@ -154,7 +161,7 @@ def test_inner_zero_writes_zeros():
     assert (out[0] == 0).all()
 
 
-def test_runs_give_the_same_bits():
+def test_runs_give_the_same_bits(kernel):
     x, xs, w, ws = make(2, 40, 520, 4112, 3)
     d = dev(x, xs, w, ws)
     first = coc.matmul_all_reduce_f8(*d)[0].clone()

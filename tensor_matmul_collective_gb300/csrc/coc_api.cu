@@ -1898,6 +1898,10 @@ static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n
         a.out_scale[r] = gated ? static_cast<uint8_t*>(out_scale[r]) : nullptr;
     }
     a.status = ds->status;
+    uintptr_t scale_bits = static_cast<uintptr_t>(kblocks);
+    for (int r = 0; r < R && needed; ++r)
+        scale_bits |= reinterpret_cast<uintptr_t>(a.w_scale[r]) | reinterpret_cast<uintptr_t>(a.x_scale[r]);
+    a.scale_words = (scale_bits & 3u) == 0;
     a.inject_timeout = g_inject.load();
     a.op = op;
     a.R = R;

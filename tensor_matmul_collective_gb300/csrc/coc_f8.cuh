@@ -49,23 +49,49 @@ __host__ __device__ constexpr uint32_t f8_idesc(int M, int N) {
 }
 __device__ __forceinline__ uint32_t f8_idesc_byte(uint32_t idesc, uint32_t byte) { return idesc | (byte << 4) | (byte << 29); }
 
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale,
-                                          uint32_t b_scale, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
-        : "memory");
+// Issued by a whole warp in step, of which one elected thread (the same one every
+// time) carries them out.  With a branch around them instead the descriptors
+// would be moved to uniform registers before every product: a k-block then took
+// 870 cycles, 344 of them to issue four products and their commit, where the
+// tensor cores need 512 (4096 x 4864 x 32768: 470 us; issued so: 374).
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
+                                          uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
 }
-__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale,
-                                               uint32_t b_scale, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
-        : "memory");
+// The barrier (PAIR: at this offset in both CTAs) arrives once the products issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_f8(uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+            : "memory");
+}
+// warp_wait that costs a test and a vote where the phase is over already.
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, const Ctl& c, unsigned where) {
+    if (__all_sync(0xffffffffu, try_wait_scoped<CLUSTER>(bar, parity))) return true;
+    return warp_wait<CLUSTER>(bar, parity, c, where);
 }
 
 // Scale words of 128 rows, shared memory -> 4 columns of tensor memory (in all
@@ -77,11 +103,16 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
     // no swizzle; eight-row groups of 16 bytes follow each other at 128 bytes
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
 }
-__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint32_t saddr) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(saddr)) : "memory");
-}
-__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint32_t saddr) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(scale_desc(saddr)) : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                     "l"(desc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                     "l"(desc)
+                     : "memory");
 }
 
 // One byte that an earlier kernel on the stream may have written.
@@ -90,13 +121,29 @@ __device__ __forceinline__ uint32_t load_byte(const uint8_t* p) {
     asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
-// The scale word of a row: bytes [kb, kb + 4) of its `blocks` scale bytes, zero past them.
-__device__ __forceinline__ uint32_t load_scale_word(const uint8_t* row, int kb, int blocks) {
-    uint32_t v = 0;
+// Scale words of N rows at once: word i holds bytes [kb, kb + 4) of the
+// `blocks` scale bytes at p[i], zero past them and where on[i] is false (p[i] is
+// then not read).  kb is a multiple of 4 below `blocks`.  All loads are in
+// flight together; whole words where rows of scales are words.
+template <int N>
+__device__ __forceinline__ void load_scale_words(const uint8_t* const (&p)[N], const bool (&on)[N], int kb, int blocks, bool words,
+                                                 uint32_t (&v)[N]) {
+    if (words) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-        if (kb + b < blocks) v |= load_byte(row + kb + b) << (8 * b);
-    return v;
+        for (int i = 0; i < N; ++i)
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.u32 %0, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
+                         : "=r"(v[i]) : "l"(p[i] + kb), "r"(static_cast<int>(on[i])));
+        return;
+    }
+    uint32_t byte[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.u32 %0, 0;\n\t@q ld.global.u8 %0, [%1];\n\t}"
+                         : "=r"(byte[i][b]) : "l"(p[i] + kb + b), "r"(static_cast<int>(on[i] && kb + b < blocks)));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = byte[i][0] | byte[i][1] << 8 | byte[i][2] << 16 | byte[i][3] << 24;
 }
 
 // The k-blocks of all shards one after another, taken from `begin` in runs that

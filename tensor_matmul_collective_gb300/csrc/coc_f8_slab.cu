@@ -148,56 +148,49 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
                 if (filled & (1u << s)) drain_wait(smem_u32(&full[s]), (parity >> s) & 1u, kDrainNs);
         __syncwarp();
     } else if (warp == 1) {
-        constexpr uint32_t idesc = f8_idesc(128, NT);
-        uint32_t stage = 0, phase = 0;
+        const uint64_t tiles = make_sdesc(smem_u32(smem), 16, 1024);
+        uint32_t stage = 0, phase = 0, onto = 0;
         int run_i = 0;
         for (int at = b0; ok && at < b1; ++run_i) {
             const F8Run run = f8_run(at, b1, p.kblocks);
+            at += run.count;
             const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
-            ok = warp_wait(smem_u32(&sf_full[ss]), sph, ctl, 0x720u + ss);
+            ok = warp_wait_soon<false>(smem_u32(&sf_full[ss]), sph, ctl, 0x720u + ss);
             // the words two runs ago, in the same columns, have been used
             if (ok && run_i >= 2) {
                 const int was = run_i - 2;
-                ok = warp_wait(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x730u);
+                ok = warp_wait_soon<false>(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x730u);
             }
             if (!ok) break;
             tc_fence_after();
             const uint32_t sc = tmem + WT * NT + (run_i & 1) * kSfCols;
-            if (lane == 0) {
-                const uint32_t src = smem_u32(sf) + ss * (WT + 1) * kScaleBlock;
+            const uint64_t src = scale_desc(smem_u32(sf)) + ss * ((WT + 1) * kScaleBlock / 16);
 #pragma unroll
-                for (int w = 0; w < WT + 1; ++w) tc_copy_scales(sc + 4 * w, src + w * kScaleBlock);
-            }
-            __syncwarp();
-            for (int j = 0; j < run.count; ++j, ++at) {
-                ok = warp_wait(smem_u32(&full[stage]), phase, ctl, 0x740u + stage);
+            for (int w = 0; w < WT + 1; ++w) tc_copy_scales<false>(sc + 4 * w, src + w * (kScaleBlock / 16));
+            for (int j = 0; j < run.count; ++j) {
+                ok = warp_wait_soon<false>(smem_u32(&full[stage]), phase, ctl, 0x740u + stage);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t base = smem_u32(smem) + stage * C::STAGE;
-                    const uint64_t xd = make_sdesc(base + WT * kWTile, 16, 1024);
-                    const uint32_t id = f8_idesc_byte(idesc, (run.kb + j) & 3);
+                const uint64_t wd = tiles + stage * (C::STAGE / 16), xd = wd + WT * (kWTile / 16);
+                const uint32_t id = f8_idesc_byte(f8_idesc(128, NT), (run.kb + j) & 3);
 #pragma unroll
-                    for (int w = 0; w < WT; ++w) {
-                        const uint64_t wd = make_sdesc(base + w * kWTile, 16, 1024);
+                for (int w = 0; w < WT; ++w)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)      // 32 of k: 32 bytes of the swizzled row
-                            tc_mma_f8(tmem + w * NT, wd + 2 * kk, xd + 2 * kk, id, sc + 4 * w, sc + 4 * WT, (at > b0 || kk > 0) ? 1u : 0u);
-                    }
-                    tc_commit(smem_u32(&empty[stage]));
-                    if (j == run.count - 1) tc_commit(smem_u32(&sf_empty[ss]));
-                }
-                __syncwarp();
+                    for (int kk = 0; kk < 4; ++kk)      // 32 of k: 32 bytes of the swizzled row
+                        tc_mma_f8<false>(tmem + w * NT, wd + w * (kWTile / 16) + 2 * kk, xd + 2 * kk, id, sc + 4 * w, sc + 4 * WT,
+                                         kk > 0 ? 1u : onto);
+                onto = 1;
+                tc_commit_f8<false>(smem_u32(&empty[stage]));
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
+            if (ok) tc_commit_f8<false>(smem_u32(&sf_empty[ss]));
         }
-        if (lane == 0) {
-            tc_commit(smem_u32(done));
-            if (!ok) drain_wait(smem_u32(done), 0, kDrainNs);
-        }
+        tc_commit_f8<false>(smem_u32(done));
+        if (!ok) drain_wait(smem_u32(done), 0, kDrainNs);
         __syncwarp();
     } else {
         // scale words: the weights' are one for all of a tile's rows, the activations' one a row
+        constexpr int XW = NT > 32 ? NT / 32 : 1;
         int run_i = 0;
         for (int at = b0; ok && at < b1; ++run_i) {
             const F8Run run = f8_run(at, b1, p.kblocks);
@@ -205,24 +198,31 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
             if ((run_i & 1) != warp - 2) continue;
             const int kb = run.kb & ~3;
             const uint8_t* ws = p.w_scale[ag ? r : run.shard];
-            uint32_t wv[WT], xv[NT > 32 ? NT / 32 : 1];
+            const uint8_t* xs = p.x_scale[ag ? 0 : run.shard];
+            const uint8_t* at_row[WT + XW];
+            bool on[WT + XW];
+            uint32_t v[WT + XW];
 #pragma unroll
-            for (int w = 0; w < WT; ++w) wv[w] = load_scale_word(ws + static_cast<long long>(nt + w * p.n_tiles) * p.kblocks, kb, p.kblocks);
-#pragma unroll
-            for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) {
-                const int row = row0 + lane + 32 * i;
-                xv[i] = row < p.m && lane + 32 * i < NT
-                            ? load_scale_word(p.x_scale[ag ? 0 : run.shard] + static_cast<long long>(row) * p.kblocks, kb, p.kblocks) : 0u;
+            for (int w = 0; w < WT; ++w) {
+                at_row[w] = ws + static_cast<long long>(nt + w * p.n_tiles) * p.kblocks;
+                on[w] = true;
             }
+#pragma unroll
+            for (int i = 0; i < XW; ++i) {
+                const int row = row0 + lane + 32 * i;
+                on[WT + i] = row < p.m && lane + 32 * i < NT;
+                at_row[WT + i] = xs + static_cast<long long>(row) * p.kblocks;
+            }
+            load_scale_words(at_row, on, kb, p.kblocks, p.scale_words != 0, v);
             const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
             ok = warp_wait(smem_u32(&sf_empty[ss]), sph ^ 1u, ctl, 0x750u + ss);
             if (!ok) break;
             uint8_t* dst = sf + ss * (WT + 1) * kScaleBlock;
 #pragma unroll
             for (int w = 0; w < WT; ++w)
-                *reinterpret_cast<uint4*>(dst + w * kScaleBlock + lane * 16) = make_uint4(wv[w], wv[w], wv[w], wv[w]);
+                *reinterpret_cast<uint4*>(dst + w * kScaleBlock + lane * 16) = make_uint4(v[w], v[w], v[w], v[w]);
 #pragma unroll
-            for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) *reinterpret_cast<uint32_t*>(dst + WT * kScaleBlock + scale_word_at(lane + 32 * i)) = xv[i];
+            for (int i = 0; i < XW; ++i) *reinterpret_cast<uint32_t*>(dst + WT * kScaleBlock + scale_word_at(lane + 32 * i)) = v[WT + i];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sf_full[ss]));

@@ -145,58 +145,54 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            constexpr uint32_t idesc = f8_idesc(256, 256);
+            const uint64_t tiles = make_sdesc(smem_u32(smem), 16, 1024);
             uint32_t stage = 0, phase = 0;
             int run_i = 0, tile_i = 0;
             for (int u = first; ok && u < units; u += step, ++tile_i) {
-                if (tile_i > 0) ok = warp_wait<true>(smem_u32(acc_early), (tile_i - 1) & 1, ctl, 0x820u);
+                if (tile_i > 0) ok = warp_wait_soon<true>(smem_u32(acc_early), (tile_i - 1) & 1, ctl, 0x820u);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (tile_i & 1) * kAcc1;
-                for (int at = 0; ok && at < total; ++run_i) {
-                    const F8Run run = f8_run(at, total, p.kblocks);
-                    const uint32_t ss = run_i % kSfStages;
-                    ok = warp_wait<true>(smem_u32(&sf_full[ss]), (run_i / kSfStages) & 1u, ctl, 0x830u + ss);
-                    // the words two runs ago, in the same columns, have been used
-                    if (ok && run_i >= 2) {
-                        const int was = run_i - 2;
-                        ok = warp_wait<true>(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x840u);
-                    }
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sc = tmem + kSfCol + (run_i & 1) * 16;
-                    if (lane == 0) {
-                        const uint32_t src = smem_u32(sf) + ss * kSfBytes;
-#pragma unroll
-                        for (int w = 0; w < 3; ++w) tc_copy_scales_pair(sc + 4 * w, src + w * kScaleBlock);
-                    }
-                    __syncwarp();
-                    for (int j = 0; j < run.count; ++j, ++at) {
-                        ok = warp_wait<true>(smem_u32(&full[stage]), phase, ctl, 0x850u + stage);
+                uint32_t onto = 0;
+                for (int shard = 0; ok && shard < p.shards; ++shard)
+                    for (int kb = 0; kb < p.kblocks; kb += 4, ++run_i) {
+                        const uint32_t ss = run_i % kSfStages;
+                        ok = warp_wait_soon<true>(smem_u32(&sf_full[ss]), (run_i / kSfStages) & 1u, ctl, 0x830u + ss);
+                        // the words two runs ago, in the same columns, have been used
+                        if (ok && run_i >= 2) {
+                            const int was = run_i - 2;
+                            ok = warp_wait_soon<true>(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x840u);
+                        }
                         if (!ok) break;
                         tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t base = smem_u32(smem) + stage * 2 * kTileBytes;
-                            const uint64_t xd = make_sdesc(base, 16, 1024), wd = make_sdesc(base + kTileBytes, 16, 1024);
-                            const uint32_t id = f8_idesc_byte(idesc, (run.kb + j) & 3);
+                        const uint32_t sc = tmem + kSfCol + (run_i & 1) * 16;
+                        const uint64_t src = scale_desc(smem_u32(sf)) + ss * (kSfBytes / 16);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_f8_pair(d, xd + 2 * kk, wd + 2 * kk, id, sc, sc + 4, (at > 0 || kk > 0) ? 1u : 0u);
-                            tc_commit_pair_both(smem_u32(&empty[stage]));
-                            if (j == run.count - 1) tc_commit_pair_both(smem_u32(&sf_empty[ss]));
+                        for (int w = 0; w < 3; ++w) tc_copy_scales<true>(sc + 4 * w, src + w * (kScaleBlock / 16));
+                        const int count = min(4, p.kblocks - kb);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j == count) break;
+                            ok = warp_wait_soon<true>(smem_u32(&full[stage]), phase, ctl, 0x850u + stage);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t xd = tiles + stage * (2 * kTileBytes / 16), wd = xd + kTileBytes / 16;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                tc_mma_f8<true>(d, xd + 2 * kk, wd + 2 * kk, f8_idesc_byte(f8_idesc(256, 256), j), sc, sc + 4, onto);
+                                onto = 1;
+                            }
+                            tc_commit_f8<true>(smem_u32(&empty[stage]));
+                            if (++stage == kStages) { stage = 0; phase ^= 1u; }
                         }
-                        __syncwarp();
-                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                        if (!ok) break;
+                        tc_commit_f8<true>(smem_u32(&sf_empty[ss]));
                     }
-                }
                 if (!ok) break;
-                if (lane == 0) tc_commit_pair_both(smem_u32(acc_full));
-                __syncwarp();
+                tc_commit_f8<true>(smem_u32(acc_full));
             }
-            if (lane == 0) {        // every product is done before tensor memory is given back
-                tc_commit_pair_local(smem_u32(drain));
-                drain_wait(smem_u32(drain), 0, kDrainNs);
-            }
+            tc_commit_f8<true>(smem_u32(drain));    // every product is done before tensor memory is given back
+            drain_wait(smem_u32(drain), 0, kDrainNs);
             __syncwarp();
         }
     } else if (warp < 6) {
@@ -336,23 +332,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                 at += run.count;
                 if ((run_i & 1) != warp - 6) continue;
                 const uint8_t *xs = p.x_scale[run.shard], *ws = p.w_scale[ag ? r : run.shard];
-                uint32_t xv[4], wv[2];
+                const uint8_t* at_row[6];
+                bool on[6];
+                uint32_t v[6];      // four activation rows', two weight tiles'
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = row0 + lane + 32 * i;
-                    xv[i] = row < p.m ? load_scale_word(xs + static_cast<long long>(row) * p.kblocks, run.kb, p.kblocks) : 0u;
+                    on[i] = row < p.m;
+                    at_row[i] = xs + static_cast<long long>(row) * p.kblocks;
                 }
-                wv[0] = load_scale_word(ws + static_cast<long long>(w0) * p.kblocks, run.kb, p.kblocks);
-                wv[1] = GATED || w1 < p.n_tiles ? load_scale_word(ws + static_cast<long long>(w1) * p.kblocks, run.kb, p.kblocks) : 0u;
+                at_row[4] = ws + static_cast<long long>(w0) * p.kblocks;
+                at_row[5] = ws + static_cast<long long>(w1) * p.kblocks;
+                on[4] = true;
+                on[5] = GATED || w1 < p.n_tiles;
+                load_scale_words(at_row, on, run.kb, p.kblocks, p.scale_words != 0, v);
                 const uint32_t ss = run_i % kSfStages;
                 ok = warp_wait<true>(smem_u32(&sf_empty[ss]), ((run_i / kSfStages) & 1u) ^ 1u, ctl, 0x870u + ss);
                 if (!ok) break;
                 uint8_t* dst = sf + ss * kSfBytes;
                 // rows lane, lane + 32, lane + 64, lane + 96 are 16 bytes
-                *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(xv[0], xv[1], xv[2], xv[3]);
+                *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(v[0], v[1], v[2], v[3]);
 #pragma unroll
                 for (int w = 0; w < 2; ++w)
-                    *reinterpret_cast<uint4*>(dst + (w + 1) * kScaleBlock + lane * 16) = make_uint4(wv[w], wv[w], wv[w], wv[w]);
+                    *reinterpret_cast<uint4*>(dst + (w + 1) * kScaleBlock + lane * 16) = make_uint4(v[4 + w], v[4 + w], v[4 + w], v[4 + w]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&sf_full[ss]), 0));

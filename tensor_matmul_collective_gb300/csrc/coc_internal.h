@@ -282,6 +282,7 @@ struct F8Args {
     int kblocks;                              // ceil(k / 128) of a shard
     int n_tiles;                              // ceil(n / 128)
     int rows_per_rank;                        // OP_RS: m / R
+    int scale_words;                          // kblocks % 4 == 0 and all scales 4-byte aligned: read as words
     int inject_timeout;
     int m_tiles, splits, group_mt;            // set by the launch
 };

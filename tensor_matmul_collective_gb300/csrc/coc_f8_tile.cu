@@ -149,9 +149,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
             uint32_t stage = 0, phase = 0;
             int run_i = 0, tile_i = 0;
             for (int u = first; ok && u < units; u += step, ++tile_i) {
-                if (tile_i > 0) ok = warp_wait_soon<true>(smem_u32(acc_early), (tile_i - 1) & 1, ctl, 0x820u);
-                if (!ok) break;
-                tc_fence_after();
+                bool shared_free = tile_i == 0;     // the columns this accumulator shares with the one before
                 const uint32_t d = tmem + (tile_i & 1) * kAcc1;
                 uint32_t onto = 0;
                 for (int shard = 0; ok && shard < p.shards; ++shard)
@@ -174,6 +172,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                         for (int j = 0; j < 4; ++j) {
                             if (j == count) break;
                             ok = warp_wait_soon<true>(smem_u32(&full[stage]), phase, ctl, 0x850u + stage);
+                            if (!shared_free && ok) {
+                                ok = warp_wait_soon<true>(smem_u32(acc_early), (tile_i - 1) & 1, ctl, 0x820u);
+                                shared_free = true;
+                            }
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t xd = tiles + stage * (2 * kTileBytes / 16), wd = xd + kTileBytes / 16;
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                         if (!ok) break;
                         tc_commit_f8<true>(smem_u32(&sf_empty[ss]));
                     }
+                if (ok && !shared_free) ok = warp_wait_soon<true>(smem_u32(acc_early), (tile_i - 1) & 1, ctl, 0x820u);   // (no k at all)
                 if (!ok) break;
                 tc_commit_f8<true>(smem_u32(acc_full));
             }

@@ -159,6 +159,14 @@ def test_inner_zero_writes_zeros(kernel):
     out = [torch.full((5, 24), 7.0, dtype=BF, device=DEV)]
     coc.matmul_all_reduce_f8([x], [xs], [w], [ws], outs=out)
     assert (out[0] == 0).all()
+    # more tiles than the GPU takes at once
+    x, w = torch.empty(2300, 0, dtype=f8.E4M3, device=DEV), torch.empty(16384, 0, dtype=f8.E4M3, device=DEV)
+    xs, ws = torch.empty(2300, 0, dtype=f8.E8M0, device=DEV), torch.empty(128, 0, dtype=f8.E8M0, device=DEV)
+    out = [torch.full((2300, 16384), 7.0, dtype=BF, device=DEV)]
+    coc.matmul_all_reduce_f8([x], [xs], [w], [ws], outs=out)
+    codes, scales = coc.all_gather_gated_matmul_f8([x], [xs], [w], [ws.view(torch.uint8).new_empty(128, 0).view(f8.E8M0)])
+    coc.sync_status()
+    assert (out[0] == 0).all() and (codes[0].view(torch.uint8) == 0).all() and (scales[0].view(torch.uint8) == 27).all()
 
 
 def test_runs_give_the_same_bits(kernel):

@@ -147,9 +147,10 @@ coc_status_t encode(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
 // dimension, rows, blocks), strides (pitch, d0 * elem).  Returns the driver's
 // result without reporting (the caller falls back to 2-D boxes).
 CUresult encode_blocked(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t d0, uint64_t rows,
-                        uint64_t blocks, uint64_t pitch_bytes, uint32_t box0, uint32_t box_rows, uint32_t box_blocks) {
+                        uint64_t blocks, uint64_t pitch_bytes, uint32_t box0, uint32_t box_rows, uint32_t box_blocks,
+                        uint32_t elem = 2) {
     const cuuint64_t dims[3] = {d0, rows, blocks};
-    const cuuint64_t strides[2] = {pitch_bytes, d0 * 2};
+    const cuuint64_t strides[2] = {pitch_bytes, d0 * elem};
     const cuuint32_t box[3] = {box0, box_rows, box_blocks};
     const cuuint32_t estr[3] = {1, 1, 1};
     return g_encode(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1882,13 +1883,18 @@ static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n
         }
     }
     const bool tiles = f8_use_tiles(op, gated, R, m, n, k, ds->sm_count);
+    const uint32_t stage_blocks = tiles ? 1 : static_cast<uint32_t>(f8_slab_kblocks(m, gated));
+    a.maps_3d = stage_blocks > 1 && k % 128 == 0;
+    auto map = [&](CUtensorMap* t, const void* base, int64_t rows_of, uint32_t box_rows) -> coc_status_t {
+        if (!a.maps_3d) return encode(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, k, rows_of, k, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (encode_blocked(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 128, rows_of, kblocks, k, 128, box_rows, stage_blocks, 1) == CUDA_SUCCESS) return COC_OK;
+        return fail(COC_ERR_CUDA, "cuTensorMapEncodeTiled failed for %lld x %lld codes", (long long)rows_of, (long long)k);
+    };
     for (int r = 0; r < R && needed && st == COC_OK; ++r) {
-        const uint64_t w_rows = static_cast<uint64_t>(gated ? 2 * n : n);
-        st = encode(&a.tm_w[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, w[r], k, w_rows, k, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        st = map(&a.tm_w[r], w[r], gated ? 2 * n : n, 128);
         a.w_scale[r] = static_cast<const uint8_t*>(w_scale[r]);
         if (st == COC_OK && (!ag || r == 0)) {
-            st = encode(&a.tm_x[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, ag ? x0 : x[r], k, m, k, 128,
-                        static_cast<uint32_t>(tiles ? 128 : f8_slab_rows(m)), CU_TENSOR_MAP_SWIZZLE_128B);
+            st = map(&a.tm_x[r], ag ? x0 : x[r], m, static_cast<uint32_t>(tiles ? 128 : f8_slab_rows(m)));
             a.x_scale[r] = ag ? s0 : static_cast<const uint8_t*>(x_scale[r]);
         }
     }

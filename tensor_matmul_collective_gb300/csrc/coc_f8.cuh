@@ -87,6 +87,27 @@ __device__ __forceinline__ void tc_commit_f8(uint32_t bar) {
             "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
             : "memory");
 }
+// Copies of a whole warp in step likewise: `bytes` announced on `bar`, boxes of
+// 2-D and 3-D maps (coordinates innermost first).
+__device__ __forceinline__ void expect_tx_f8(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_f8(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_f8(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+        : "memory");
+}
 // warp_wait that costs a test and a vote where the phase is over already.
 template <bool CLUSTER>
 __device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, const Ctl& c, unsigned where) {
@@ -146,16 +167,16 @@ __device__ __forceinline__ void load_scale_words(const uint8_t* const (&p)[N], c
     for (int i = 0; i < N; ++i) v[i] = byte[i][0] | byte[i][1] << 8 | byte[i][2] << 16 | byte[i][3] << 24;
 }
 
-// The k-blocks of all shards one after another, taken from `begin` in runs that
-// share a scale word: up to 4 blocks of one shard, from a multiple of 4 of it.
+// The k-blocks of all shards one after another, in runs that share a scale
+// word: up to 4 blocks of one shard.
 struct F8Run {
-    int shard, kb, count;      // blocks kb .. kb + count - 1 of the shard; kb & ~3 is the word's first
+    int shard, kb, count;      // blocks kb .. kb + count - 1 of the shard
 };
-__device__ __forceinline__ F8Run f8_run(int at, int end, int kblocks) {
+__device__ __forceinline__ F8Run f8_run(int i, int per_shard, int kblocks) {
     F8Run r;
-    r.shard = at / kblocks;
-    r.kb = at - r.shard * kblocks;
-    r.count = min(min(4 - (r.kb & 3), kblocks - r.kb), end - at);
+    r.shard = i / per_shard;
+    r.kb = 4 * (i - r.shard * per_shard);
+    r.count = min(4, kblocks - r.kb);
     return r;
 }
 

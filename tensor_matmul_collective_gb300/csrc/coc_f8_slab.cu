@@ -33,14 +33,16 @@ constexpr int kSfCols = 16;             // columns of a set of scale words in te
 template <int NT, bool GATED>
 struct SlabCfg {
     static constexpr int WT = GATED ? 2 : 1;
-    static constexpr int STAGE = WT * kWTile + NT * 128;
-    // two blocks on an SM where a ring of at least 3 stages fits in half its shared memory
+    static constexpr int BLOCK = WT * kWTile + NT * 128;        // a k-block's tiles
     static constexpr int SF_BYTES = kSfStages * (WT + 1) * kScaleBlock;
-    static constexpr int HALF = 112 * 1024 - 2048 - SF_BYTES, FULL = 224 * 1024 - 2048 - SF_BYTES;
-    static constexpr bool TWO = HALF / STAGE >= 3;
+    static constexpr int HALF = 112 * 1024 - 1024 - SF_BYTES, FULL = 224 * 1024 - 1024 - SF_BYTES;
+    // two blocks on an SM where a ring of at least 4 k-blocks fits in half its shared memory
+    static constexpr bool TWO = HALF / BLOCK >= 4;
+    static constexpr int KPS = FULL / (2 * BLOCK) >= 3 ? 2 : 1;     // k-blocks of a stage
+    static constexpr int STAGE = KPS * BLOCK;
     static constexpr int S = (TWO ? HALF : FULL) / STAGE;
     static constexpr int SUMS = WT * NT * 128 * 4;
-    static constexpr int SMEM = 1024 + S * STAGE + SF_BYTES + 256;
+    static constexpr int SMEM = 1024 + S * STAGE + SF_BYTES + 512;
     static constexpr int COLS = WT * NT + 2 * kSfCols;
     static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(S >= 2 && S <= 16 && SUMS <= S * STAGE && SMEM <= kSlabSmemCap, "shared memory");
@@ -69,7 +71,8 @@ __device__ __forceinline__ float4 load_part(uint32_t addr, bool cluster) {
 template <int NT, bool GATED, bool BF16>
 __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8Args p) {
     using C = SlabCfg<NT, GATED>;
-    constexpr int WT = C::WT, S = C::S;
+    constexpr int WT = C::WT, S = C::S, KPS = C::KPS;
+    constexpr int kXAt = KPS * WT * kWTile;     // a stage: W tiles of its k-blocks, second W tiles (gated), X tiles
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sf = smem + S * C::STAGE;
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
     const int mt = tile % p.m_tiles, col_tile = tile / p.m_tiles;
     const int nt = col_tile % p.n_tiles, r = col_tile / p.n_tiles;      // r: the AllGather's rank
     const int row0 = mt * NT;
-    const int total = p.shards * p.kblocks;
+    const int per_shard = (p.kblocks + 3) / 4, total = p.shards * per_shard;     // runs of k-blocks
     const int b0 = static_cast<int>(static_cast<long long>(total) * split / splits);
     const int b1 = static_cast<int>(static_cast<long long>(total) * (split + 1) / splits);
     const bool ag = p.op == OP_AG;
@@ -126,22 +129,36 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
     if (warp == 0) {
         uint32_t stage = 0, phase = 0, filled = 0, parity = 0;
         const uint64_t pol_w = make_l2_policy(p.m_tiles > 1 ? 0 : 1), pol_x = make_l2_policy(2);
+        const uint32_t ring = smem_u32(smem);
         for (int i = b0; ok && i < b1; ++i) {
-            ok = warp_wait(smem_u32(&empty[stage]), phase ^ 1u, ctl, 0x710u + stage);
-            if (!ok) break;
-            if (lane == 0) {
-                const int shard = i / p.kblocks, kc = (i - shard * p.kblocks) * 128;
-                const CUtensorMap* wm = &p.tm_w[ag ? r : shard];
-                const uint32_t fb = smem_u32(&full[stage]), dst = smem_u32(smem) + stage * C::STAGE;
-                mbar_expect_tx(fb, C::STAGE);
-                tma_load_2d_hint(dst, wm, kc, nt * 128, fb, pol_w);
-                if constexpr (GATED) tma_load_2d_hint(dst + kWTile, wm, kc, p.n + nt * 128, fb, pol_w);
-                tma_load_2d_hint(dst + WT * kWTile, &p.tm_x[ag ? 0 : shard], kc, row0, fb, pol_x);
+            const F8Run run = f8_run(i, per_shard, p.kblocks);
+            const CUtensorMap *wm = &p.tm_w[ag ? r : run.shard], *xm = &p.tm_x[ag ? 0 : run.shard];
+            for (int j = 0; j < run.count; j += KPS) {
+                ok = warp_wait_soon<false>(smem_u32(&empty[stage]), phase ^ 1u, ctl, 0x710u + stage);
+                if (!ok) break;
+                const uint32_t fb = smem_u32(&full[stage]), dst = ring + stage * C::STAGE;
+                const int kb = run.kb + j;
+                if (KPS == 2 && p.maps_3d) {
+                    // both k-blocks in one box (a last odd one: zeros behind it)
+                    expect_tx_f8(fb, C::STAGE);
+                    tma_load_3d_f8(dst, wm, 0, nt * 128, kb, fb, pol_w);
+                    if constexpr (GATED) tma_load_3d_f8(dst + KPS * kWTile, wm, 0, p.n + nt * 128, kb, fb, pol_w);
+                    tma_load_3d_f8(dst + kXAt, xm, 0, row0, kb, fb, pol_x);
+                } else {
+                    const int count = min(KPS, run.count - j);
+                    expect_tx_f8(fb, count * C::BLOCK);
+#pragma unroll
+                    for (int q = 0; q < KPS; ++q) {
+                        if (q == count) break;
+                        tma_load_2d_f8(dst + q * kWTile, wm, (kb + q) * 128, nt * 128, fb, pol_w);
+                        if constexpr (GATED) tma_load_2d_f8(dst + (KPS + q) * kWTile, wm, (kb + q) * 128, p.n + nt * 128, fb, pol_w);
+                        tma_load_2d_f8(dst + kXAt + q * NT * 128, xm, (kb + q) * 128, row0, fb, pol_x);
+                    }
+                }
                 filled |= 1u << stage;
                 parity = (parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == S) { stage = 0; phase ^= 1u; }
             }
-            __syncwarp();
-            if (++stage == S) { stage = 0; phase ^= 1u; }
         }
         if (!ok && lane == 0)       // no copy stays in flight into shared memory
             for (int s = 0; s < S; ++s)
@@ -151,9 +168,8 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
         const uint64_t tiles = make_sdesc(smem_u32(smem), 16, 1024);
         uint32_t stage = 0, phase = 0, onto = 0;
         int run_i = 0;
-        for (int at = b0; ok && at < b1; ++run_i) {
-            const F8Run run = f8_run(at, b1, p.kblocks);
-            at += run.count;
+        for (int i = b0; ok && i < b1; ++i, ++run_i) {
+            const F8Run run = f8_run(i, per_shard, p.kblocks);
             const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
             ok = warp_wait_soon<false>(smem_u32(&sf_full[ss]), sph, ctl, 0x720u + ss);
             // the words two runs ago, in the same columns, have been used
@@ -167,21 +183,27 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
             const uint64_t src = scale_desc(smem_u32(sf)) + ss * ((WT + 1) * kScaleBlock / 16);
 #pragma unroll
             for (int w = 0; w < WT + 1; ++w) tc_copy_scales<false>(sc + 4 * w, src + w * (kScaleBlock / 16));
-            for (int j = 0; j < run.count; ++j) {
-                ok = warp_wait_soon<false>(smem_u32(&full[stage]), phase, ctl, 0x740u + stage);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t wd = tiles + stage * (C::STAGE / 16), xd = wd + WT * (kWTile / 16);
-                const uint32_t id = f8_idesc_byte(f8_idesc(128, NT), (run.kb + j) & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= run.count) break;
+                if (j % KPS == 0) {
+                    ok = warp_wait_soon<false>(smem_u32(&full[stage]), phase, ctl, 0x740u + stage);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const uint64_t wd = tiles + stage * (C::STAGE / 16) + (j % KPS) * (kWTile / 16);
+                const uint64_t xd = tiles + stage * (C::STAGE / 16) + (kXAt + (j % KPS) * NT * 128) / 16;
 #pragma unroll
                 for (int w = 0; w < WT; ++w)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)      // 32 of k: 32 bytes of the swizzled row
-                        tc_mma_f8<false>(tmem + w * NT, wd + w * (kWTile / 16) + 2 * kk, xd + 2 * kk, id, sc + 4 * w, sc + 4 * WT,
-                                         kk > 0 ? 1u : onto);
+                        tc_mma_f8<false>(tmem + w * NT, wd + w * KPS * (kWTile / 16) + 2 * kk, xd + 2 * kk, f8_idesc_byte(f8_idesc(128, NT), j),
+                                         sc + 4 * w, sc + 4 * WT, kk > 0 ? 1u : onto);
                 onto = 1;
-                tc_commit_f8<false>(smem_u32(&empty[stage]));
-                if (++stage == S) { stage = 0; phase ^= 1u; }
+                if (j % KPS == KPS - 1 || j == run.count - 1) {
+                    tc_commit_f8<false>(smem_u32(&empty[stage]));
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
             }
             if (ok) tc_commit_f8<false>(smem_u32(&sf_empty[ss]));
         }
@@ -192,11 +214,9 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
         // scale words: the weights' are one for all of a tile's rows, the activations' one a row
         constexpr int XW = NT > 32 ? NT / 32 : 1;
         int run_i = 0;
-        for (int at = b0; ok && at < b1; ++run_i) {
-            const F8Run run = f8_run(at, b1, p.kblocks);
-            at += run.count;
+        for (int i = b0; ok && i < b1; ++i, ++run_i) {
             if ((run_i & 1) != warp - 2) continue;
-            const int kb = run.kb & ~3;
+            const F8Run run = f8_run(i, per_shard, p.kblocks);
             const uint8_t* ws = p.w_scale[ag ? r : run.shard];
             const uint8_t* xs = p.x_scale[ag ? 0 : run.shard];
             const uint8_t* at_row[WT + XW];
@@ -213,7 +233,7 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
                 on[WT + i] = row < p.m && lane + 32 * i < NT;
                 at_row[WT + i] = xs + static_cast<long long>(row) * p.kblocks;
             }
-            load_scale_words(at_row, on, kb, p.kblocks, p.scale_words != 0, v);
+            load_scale_words(at_row, on, run.kb, p.kblocks, p.scale_words != 0, v);
             const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
             ok = warp_wait(smem_u32(&sf_empty[ss]), sph ^ 1u, ctl, 0x750u + ss);
             if (!ok) break;
@@ -357,6 +377,17 @@ bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, in
     return m > 512;
 }
 
+template <int NT>
+static int kps_of(bool gated) { return gated ? SlabCfg<NT, true>::KPS : SlabCfg<NT, false>::KPS; }
+int f8_slab_kblocks(int64_t m, bool gated) {
+    switch (f8_slab_rows(m)) {
+        case 16: return kps_of<16>(gated);
+        case 32: return kps_of<32>(gated);
+        case 64: return kps_of<64>(gated);
+        default: return kps_of<128>(gated);
+    }
+}
+
 int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 
 cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_count, cudaStream_t stream) {
@@ -365,9 +396,9 @@ cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_cou
     a.m_tiles = (a.m + nt - 1) / nt;
     // ranges of the contraction: up to 8, while the tiles leave SMs free
     const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1);
-    const int total = a.shards * a.kblocks;
+    const int total = a.shards * ((a.kblocks + 3) / 4);
     a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits * 2 <= sm_count && total >= 4 * a.splits) a.splits *= 2;
+    while (a.splits < 8 && tiles * a.splits * 2 <= sm_count && total >= 2 * a.splits) a.splits *= 2;
     if (gated) return launch_n<true, true>(a, nt, stream);
     return bf16 ? launch_n<false, true>(a, nt, stream) : launch_n<false, false>(a, nt, stream);
 }

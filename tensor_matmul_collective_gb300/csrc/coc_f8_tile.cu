@@ -324,16 +324,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
         }
     } else {
         // scale words: this CTA's 128 activation rows, and all 256 weight rows (two words)
+        const int per_shard = (p.kblocks + 3) / 4;
         int run_i = 0;
         for (int u = first; ok && u < units; u += step) {
             int r, mt, nt;
             decode(u, r, mt, nt);
             const int row0 = mt * 256 + static_cast<int>(rank) * 128;
             const int w0 = GATED ? nt : 2 * nt, w1 = GATED ? p.n_tiles + nt : 2 * nt + 1;
-            for (int at = 0; at < total; ++run_i) {
-                const F8Run run = f8_run(at, total, p.kblocks);
-                at += run.count;
+            for (int i = 0; i < p.shards * per_shard; ++i, ++run_i) {
                 if ((run_i & 1) != warp - 6) continue;
+                const F8Run run = f8_run(i, per_shard, p.kblocks);
                 const uint8_t *xs = p.x_scale[run.shard], *ws = p.w_scale[ag ? r : run.shard];
                 const uint8_t* at_row[6];
                 bool on[6];

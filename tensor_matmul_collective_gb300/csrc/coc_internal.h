@@ -268,7 +268,8 @@ cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStr
 // (m gathered rows in x[0], every rank's n columns); gated: OP_AG with 2 n
 // weight rows a rank, gate first, whose result is codes and scales.  Maps:
 // 128 columns x 128 rows of a weight, 128 x f8_slab_rows(m) of x
-// (coc_f8_slab.cu) or 128 x 128 (coc_f8_tile.cu), 128-byte swizzle, zero past the ends.
+// (coc_f8_slab.cu) or 128 x 128 (coc_f8_tile.cu), 128-byte swizzle, zero past the ends;
+// maps_3d: (128, rows, k-blocks), boxes of f8_slab_kblocks(m) k-blocks.
 struct F8Args {
     CUtensorMap tm_x[COC_MAX_RANKS];
     CUtensorMap tm_w[COC_MAX_RANKS];
@@ -282,6 +283,7 @@ struct F8Args {
     int kblocks;                              // ceil(k / 128) of a shard
     int n_tiles;                              // ceil(n / 128)
     int rows_per_rank;                        // OP_RS: m / R
+    int maps_3d;                              // slabs of a k that is whole blocks
     int scale_words;                          // kblocks % 4 == 0 and all scales 4-byte aligned: read as words
     int inject_timeout;
     int m_tiles, splits, group_mt;            // set by the launch
@@ -290,6 +292,7 @@ struct F8Args {
 // of weight rows; and the rows of their X maps' boxes (tiles: 128).
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count);
 int f8_slab_rows(int64_t m);
+int f8_slab_kblocks(int64_t m, bool gated);     // k-blocks of a stage: 1 or 2
 cudaError_t launch_f8_tile(const F8Args& a, bool gated, bool bf16, cudaStream_t stream);
 cudaError_t launch_f8_slab(const F8Args& a, bool gated, bool bf16, int sm_count, cudaStream_t stream);
 // R pieces of activations after one another: vecs 16-byte pieces of codes and

@@ -27,26 +27,26 @@ namespace coc {
 namespace {
 
 constexpr int kWTile = 128 * 128;       // bytes of 128 weight rows' k-block
-constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight
-constexpr int kSfCols = 16;             // columns of a set of scale words in tensor memory
+constexpr int kMaxStages = 8;
+constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight, in shared and in tensor memory
+constexpr int kSfCols = 16;             // columns of a run's scale words in tensor memory
 
 template <int NT, bool GATED>
 struct SlabCfg {
     static constexpr int WT = GATED ? 2 : 1;
     static constexpr int BLOCK = WT * kWTile + NT * 128;        // a k-block's tiles
-    static constexpr int SF_BYTES = kSfStages * (WT + 1) * kScaleBlock;
-    static constexpr int HALF = 112 * 1024 - 1024 - SF_BYTES, FULL = 224 * 1024 - 1024 - SF_BYTES;
-    // two blocks on an SM where a ring of at least 4 k-blocks fits in half its shared memory
-    static constexpr bool TWO = HALF / BLOCK >= 4;
-    static constexpr int KPS = FULL / (2 * BLOCK) >= 3 ? 2 : 1;     // k-blocks of a stage
+    static constexpr int KPS = !GATED && NT <= 64 ? 2 : 1;      // k-blocks of a stage
     static constexpr int STAGE = KPS * BLOCK;
-    static constexpr int S = (TWO ? HALF : FULL) / STAGE;
+    static constexpr int SF_BYTES = kSfStages * (WT + 1) * kScaleBlock;
+    static constexpr int REST = 1024 + SF_BYTES + 512;          // alignment, scale words, barriers
     static constexpr int SUMS = WT * NT * 128 * 4;
-    static constexpr int SMEM = 1024 + S * STAGE + SF_BYTES + 512;
-    static constexpr int COLS = WT * NT + 2 * kSfCols;
-    static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static_assert(S >= 2 && S <= 16 && SUMS <= S * STAGE && SMEM <= kSlabSmemCap, "shared memory");
-    static_assert(!TWO || TMEM <= 256, "tensor memory of two blocks");
+    static constexpr int COLS = WT * NT + kSfStages * kSfCols;
+    static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    // stages of a ring that has an SM to itself, and of one that shares it with another block's (0: cannot)
+    static constexpr int ALONE = (224 * 1024 - REST) / STAGE;
+    static constexpr int HALF = (112 * 1024 - REST) / STAGE;
+    static constexpr int SHARED = HALF >= 2 && TMEM <= 256 && SUMS <= HALF * STAGE ? HALF : 0;
+    static_assert(ALONE >= 2 && ALONE <= kMaxStages && SUMS <= ALONE * STAGE && ALONE * STAGE + REST <= kSlabSmemCap, "shared memory");
 };
 
 // 32 lanes x 16 consecutive columns: thread t receives lane (base + t).
@@ -71,15 +71,16 @@ __device__ __forceinline__ float4 load_part(uint32_t addr, bool cluster) {
 template <int NT, bool GATED, bool BF16>
 __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8Args p) {
     using C = SlabCfg<NT, GATED>;
-    constexpr int WT = C::WT, S = C::S, KPS = C::KPS;
+    constexpr int WT = C::WT, KPS = C::KPS;
+    const uint32_t S = p.stages;
     constexpr int kXAt = KPS * WT * kWTile;     // a stage: W tiles of its k-blocks, second W tiles (gated), X tiles
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sf = smem + S * C::STAGE;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sf + C::SF_BYTES);
     uint64_t* full = bars;                  // [S] tiles landed
-    uint64_t* empty = full + S;             // [S] tiles read by the products
-    uint64_t* sf_full = empty + S;          // [kSfStages] a run's scale words written
+    uint64_t* empty = full + kMaxStages;    // [S] tiles read by the products
+    uint64_t* sf_full = empty + kMaxStages; // [kSfStages] a run's scale words written
     uint64_t* sf_empty = sf_full + kSfStages;   // [kSfStages] the run's products are done
     uint64_t* done = sf_empty + kSfStages;  // all products are done
     uint64_t* never = done + 1;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
     const bool ag = p.op == OP_AG;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (uint32_t s = 0; s < S; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
             }
         }
         if (!ok && lane == 0)       // no copy stays in flight into shared memory
-            for (int s = 0; s < S; ++s)
+            for (uint32_t s = 0; s < S; ++s)
                 if (filled & (1u << s)) drain_wait(smem_u32(&full[s]), (parity >> s) & 1u, kDrainNs);
         __syncwarp();
     } else if (warp == 1) {
@@ -172,14 +173,10 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
             const F8Run run = f8_run(i, per_shard, p.kblocks);
             const uint32_t ss = run_i % kSfStages, sph = (run_i / kSfStages) & 1u;
             ok = warp_wait_soon<false>(smem_u32(&sf_full[ss]), sph, ctl, 0x720u + ss);
-            // the words two runs ago, in the same columns, have been used
-            if (ok && run_i >= 2) {
-                const int was = run_i - 2;
-                ok = warp_wait_soon<false>(smem_u32(&sf_empty[was % kSfStages]), (was / kSfStages) & 1u, ctl, 0x730u);
-            }
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sc = tmem + WT * NT + (run_i & 1) * kSfCols;
+            // (the columns' words of four runs ago have been used: their bytes in shared memory would not have been replaced else)
+            const uint32_t sc = tmem + WT * NT + ss * kSfCols;
             const uint64_t src = scale_desc(smem_u32(sf)) + ss * ((WT + 1) * kScaleBlock / 16);
 #pragma unroll
             for (int w = 0; w < WT + 1; ++w) tc_copy_scales<false>(sc + 4 * w, src + w * (kScaleBlock / 16));
@@ -329,29 +326,51 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
 }
 
 template <int NT, bool GATED, bool BF16>
-cudaError_t launch_t(const F8Args& a, cudaStream_t stream) {
+cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     using C = SlabCfg<NT, GATED>;
     auto kern = f8_slab_kernel<NT, GATED, BF16>;
-    static std::atomic<unsigned char> smem_set[64];
+    static std::atomic<int> known[64][9];   // clusters of k that run at once, a block on an SM each; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !smem_set[dev].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) smem_set[dev].store(1, std::memory_order_release);
-    }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1) * a.splits), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
+    // k == 1 raises the kernel's shared memory limit, once a device
+    auto clusters = [&](int k, int* n) -> cudaError_t {
+        if (dev >= 0 && dev < 64 && (*n = known[dev][k].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+        cfg.dynamicSmemBytes = C::REST + C::ALONE * C::STAGE;
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
+        if (err != cudaSuccess) return err;
+        *n = sm_count;
+        if (k > 1) {
+            cfg.gridDim = dim3(static_cast<unsigned>(k), 1, 1);
+            attr[0].val.clusterDim.x = static_cast<unsigned>(k);
+            if ((err = cudaOccupancyMaxActiveClusters(n, kern, &cfg)) != cudaSuccess) return err;
+        }
+        if (dev >= 0 && dev < 64) known[dev][k].store(std::max(*n, 1), std::memory_order_release);
+        return cudaSuccess;
+    };
+    const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1);
+    const int total = a.shards * ((a.kblocks + 3) / 4);
+    int room = 0;
+    if ((e = clusters(1, &room)) != cudaSuccess) return e;
+    const bool alone = C::SHARED == 0 || tiles <= room;
+    a.splits = 1;
+    for (int k = 2; k <= 8 && k <= total && tiles * k <= sm_count; ++k) {
+        if ((e = clusters(k, &room)) != cudaSuccess) return e;
+        if (tiles <= room) a.splits = k;
+    }
+    a.stages = alone ? C::ALONE : C::SHARED;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
+    cfg.dynamicSmemBytes = C::REST + a.stages * C::STAGE;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
     if (pdl_launch()) {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -361,20 +380,36 @@ cudaError_t launch_t(const F8Args& a, cudaStream_t stream) {
 }
 
 template <bool GATED, bool BF16>
-cudaError_t launch_n(const F8Args& a, int nt, cudaStream_t stream) {
+cudaError_t launch_n(const F8Args& a, int nt, int sm_count, cudaStream_t stream) {
     switch (nt) {
-        case 16: return launch_t<16, GATED, BF16>(a, stream);
-        case 32: return launch_t<32, GATED, BF16>(a, stream);
-        case 64: return launch_t<64, GATED, BF16>(a, stream);
-        default: return launch_t<128, GATED, BF16>(a, stream);
+        case 16: return launch_t<16, GATED, BF16>(a, sm_count, stream);
+        case 32: return launch_t<32, GATED, BF16>(a, sm_count, stream);
+        case 64: return launch_t<64, GATED, BF16>(a, sm_count, stream);
+        default: return launch_t<128, GATED, BF16>(a, sm_count, stream);
     }
 }
 
 }  // namespace
 
+// Tiles of CTA pairs or slabs of weight rows, by the time either takes for its
+// rounds of k-blocks: a tile's k-block takes 0.335 us, a slab's of 128 rows 0.3
+// where it has an SM to itself and 0.52 where two share one; joining ranges
+// costs 3.  Up to 128 rows (gated: 64) the weights' bytes decide, and slabs
+// stream them better.  Measured, slab / tile: n 8192, k 8 x 3584, m 128 45 / 78 us,
+// 256 65 / 80, 384 106 / 85, 4096 816 / 574; n 1024, k 4096, m 512 11.7 / 15.2, 2048
+// 15.0 / 15.7, 4096 22.7 / 17.3; n 2048, k 1024, m 512 10.3 / 9.0; gated, 8 x 3584, k
+// 8192, m 64 84 / 87, 128 105 / 88, 4096 1807 / 1049; 11008, k 4096, m 64 28 / 39, 128 32 / 33.
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
     if (const char* e = std::getenv("COC_F8_TILE")) return std::atoi(e) != 0;
-    return m > 512;
+    if (m <= (gated ? 64 : 128)) return false;
+    if (gated) return true;
+    const int64_t cols = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R);
+    const int64_t units = (m + 255) / 256 * ((n + 255) / 256) * cols, slabs = (m + 127) / 128 * ((n + 127) / 128) * cols;
+    const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>(8, sm_count / slabs));
+    const double tile = 5.0 + 0.335 * static_cast<double>((units + pairs - 1) / pairs * blocks);
+    const double slab = 5.5 + (slabs <= sm_count ? 0.3 * static_cast<double>(blocks) / static_cast<double>(split) + (split > 1 ? 3.0 : 0.0)
+                                                 : 0.52 * static_cast<double>((slabs + 2 * sm_count - 1) / (2 * sm_count) * blocks));
+    return tile < slab;
 }
 
 template <int NT>
@@ -390,17 +425,21 @@ int f8_slab_kblocks(int64_t m, bool gated) {
 
 int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 
+// Blocks.  Where the tiles leave SMs free, a tile's contraction is cut into as
+// many ranges (2 to 8) as clusters of that size find an SM for every block: a
+// block alone on an SM has all its shared memory for the ring.  More tiles
+// than SMs go unsplit, two blocks on an SM, which overlaps one's beginning and end
+// with the other's middle.  Measured, ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1
+// 9.6 / 7.6 / 7.0 / 17.5 us; n 8192, k 8 x 3584, m 64 49 / 41 / 49 / 76 (shared 70 /
+// 47 / 44 / 55); n 14336, k 8 x 7168, m 16 120 / 128 / 144 / 162 (shared 148 / 127 /
+// 132 / 151); n 1024, k 2 x 8192, m 16 27 / 17 / 12 / 9.0.  Gated, 8 x 3584, k 8192, m
+// 64: shared 84 unsplit, 92 in two, alone 88.
 cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_count, cudaStream_t stream) {
     F8Args a = args;
     const int nt = f8_slab_rows(a.m);
     a.m_tiles = (a.m + nt - 1) / nt;
-    // ranges of the contraction: up to 8, while the tiles leave SMs free
-    const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1);
-    const int total = a.shards * ((a.kblocks + 3) / 4);
-    a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits * 2 <= sm_count && total >= 2 * a.splits) a.splits *= 2;
-    if (gated) return launch_n<true, true>(a, nt, stream);
-    return bf16 ? launch_n<false, true>(a, nt, stream) : launch_n<false, false>(a, nt, stream);
+    if (gated) return launch_n<true, true>(a, nt, sm_count, stream);
+    return bf16 ? launch_n<false, true>(a, nt, sm_count, stream) : launch_n<false, false>(a, nt, sm_count, stream);
 }
 
 // ---- the shards' activations one after another (AllGather of shards that lie apart)

@@ -108,6 +108,12 @@ __device__ __forceinline__ void tma_load_3d_f8(uint32_t dst, const CUtensorMap* 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
         : "memory");
 }
+// Arrival at a barrier of the cluster that hands nothing over in memory: a
+// release at the cluster's scope waits for all that the thread has stored (1600
+// cycles of an epilogue).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // warp_wait that costs a test and a vote where the phase is over already.
 template <bool CLUSTER>
 __device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, const Ctl& c, unsigned where) {

@@ -213,11 +213,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
             const int buf = tile_i & 1;
             const int row0 = mt * 256 + static_cast<int>(rank) * 128 + 32 * q;
             const uint32_t acc = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * kAcc1;
-            // the shared columns are in registers: the next tile may begin
+            // the shared columns are in registers (their loads are complete): the next tile may begin
             auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(early);
+                if (lane == 0) mbar_arrive_cluster_relaxed(early);
             };
             auto load = [&](uint32_t at, uint32_t (&v)[32]) {
                 if (total > 0) {

@@ -849,7 +849,7 @@ def quantize_f8(xs, outs=None, scales=None, stream=None):
     xs[r]: rows x hidden (fp16/bf16), hidden a multiple of 16; codes[r]: rows x
     hidden float8_e4m3fn, scales[r]: rows x ceil(hidden/128) float8_e8m0fnu,
     the least power of two that keeps 128 values within e4m3 (at least 2**-100).
-    New ones are parts of one allocation each."""
+    New ones are parts of one allocation."""
     native = _native or _marshal()
     if native:
         done = native[0].quantize_f8(native[4], xs, outs, scales, None if stream is None else _stream(stream))

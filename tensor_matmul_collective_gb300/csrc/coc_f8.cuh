@@ -22,10 +22,12 @@ namespace {
 __device__ __forceinline__ uint32_t f8_scale_byte(float amax) { return __float_as_uint(scale_for(amax)) >> 23; }
 __device__ __forceinline__ float f8_inverse(uint32_t scale_byte) { return __uint_as_float((254u - scale_byte) << 23); }
 
+constexpr float kF8Largest = 3.4028234663852886e38f;     // fp32's
+
 // |v| where it is finite, else 0: what counts in a block's largest magnitude.
 __device__ __forceinline__ float f8_magnitude(float v) {
     const float a = fabsf(v);
-    return a <= 3.4028234663852886e38f ? a : 0.f;
+    return a <= kF8Largest ? a : 0.f;
 }
 
 // Four codes, e4m3(v * f), round-to-nearest-even; beyond 448 (infinities) +-448, NaN stays NaN.

@@ -29,11 +29,17 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     }
 }
 
-// The 16 lanes' block: its scale byte, and this lane's 8 codes.
+// The 16 lanes' block: its scale byte, and this lane's 8 codes.  Infinities do
+// not count, but are seldom there to be taken out.
 __device__ __forceinline__ uint32_t block_codes(const float (&y)[8], uint2& codes) {
     float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, f8_magnitude(y[j]));
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+    if (__any_sync(0xffffffffu, top > kF8Largest)) {
+        top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, f8_magnitude(y[j]));
+    }
 #pragma unroll
     for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     const uint32_t byte = f8_scale_byte(top);
@@ -44,27 +50,26 @@ __device__ __forceinline__ uint32_t block_codes(const float (&y)[8], uint2& code
 
 // Half a warp a block of 128, kBlocksEach blocks of it in flight.
 constexpr int kQuantThreads = 256;
-constexpr int kBlocksEach = 4;
+constexpr int kBlocksEach = 2;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kQuantThreads) f8_quantize_kernel(const __grid_constant__ F8RowsArgs a) {
     grid_dependency_wait();
     grid_dependents_launch();
     const int r = blockIdx.y;
-    const int blocks = (a.hidden + 127) / 128, lane16 = threadIdx.x & 15;
-    const long long all = static_cast<long long>(a.rows) * blocks;
-    const long long first = static_cast<long long>(blockIdx.x) * (kQuantThreads / 16 * kBlocksEach) + (threadIdx.x >> 4);
+    const uint32_t blocks = (a.hidden + 127) / 128, all = a.rows * blocks;      // at most 2^31
+    const int lane16 = threadIdx.x & 15;
+    const uint32_t first = blockIdx.x * (kQuantThreads / 16 * kBlocksEach) + (threadIdx.x >> 4);
     uint4 v[kBlocksEach];
-    long long row[kBlocksEach];
-    int block[kBlocksEach];
+    long long at[kBlocksEach];      // the lane's values in the matrix; -1: none
 #pragma unroll
     for (int i = 0; i < kBlocksEach; ++i) {
-        const long long at = first + i * (kQuantThreads / 16);
-        row[i] = at / blocks;
-        block[i] = static_cast<int>(at - row[i] * blocks);
-        const int col = block[i] * 128 + lane16 * 8;
+        const uint32_t b = first + i * (kQuantThreads / 16);
+        const uint32_t row = b / blocks;
+        const int col = static_cast<int>(b - row * blocks) * 128 + lane16 * 8;
+        at[i] = b < all && col < a.hidden ? static_cast<long long>(row) * a.hidden + col : -1;
         v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at < all && col < a.hidden) v[i] = load_uint4(a.x[r] + row[i] * a.hidden + col);
+        if (at[i] >= 0) v[i] = load_uint4(a.x[r] + at[i]);
     }
 #pragma unroll
     for (int i = 0; i < kBlocksEach; ++i) {
@@ -72,18 +77,20 @@ __global__ void __launch_bounds__(kQuantThreads) f8_quantize_kernel(const __grid
         unpack8<BF16>(v[i], y);
         uint2 codes;
         const uint32_t byte = block_codes(y, codes);
-        const int col = block[i] * 128 + lane16 * 8;
-        if (row[i] < a.rows && col < a.hidden) {
-            *reinterpret_cast<uint2*>(a.codes[r] + row[i] * a.hidden + col) = codes;
-            if (lane16 == 0) a.scale[r][row[i] * blocks + block[i]] = static_cast<uint8_t>(byte);
+        if (at[i] >= 0) {
+            *reinterpret_cast<uint2*>(a.codes[r] + at[i]) = codes;
+            if (lane16 == 0) a.scale[r][first + i * (kQuantThreads / 16)] = static_cast<uint8_t>(byte);
         }
     }
 }
 
 // blockDim.x threads a row (a multiple of 32), blockDim.y rows a block; VPT
 // pieces of 8 values a thread.
+constexpr int norm_threads(int vpt) { return vpt <= 2 ? 1024 : 512; }
+
+// (VPT 4, two blocks of 512 on an SM: 8 x 1024 rows of 8192 75.7 to 70.2 us, 4096 of 16384 103 to 73.8)
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F8RowsArgs a) {
+__global__ void __launch_bounds__(norm_threads(VPT), VPT == 4 ? 2 : 1) f8_norm_kernel(const __grid_constant__ F8RowsArgs a) {
     __shared__ float sums[32];
     grid_dependency_wait();
     grid_dependents_launch();
@@ -93,7 +100,10 @@ __global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F
     const int pieces = a.hidden / 8;
     const long long base = row * a.hidden;
 
+    // all loads first; the weights' wait in registers where these are not many
+    constexpr bool kAhead = VPT <= 4;
     float s[VPT][8];
+    uint4 wv[kAhead ? VPT : 1];
     {
         uint4 xv[VPT], rv[VPT];
 #pragma unroll
@@ -103,6 +113,13 @@ __global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F
             if (live && p < pieces) {
                 xv[i] = load_uint4(a.x[r] + base + 8 * p);
                 if (a.residual[r] != nullptr) rv[i] = load_uint4(a.residual[r] + base + 8 * p);
+            }
+        }
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int p = t + i * T;
+                wv[i] = p < pieces ? load_uint4(a.weight + 8 * p) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
 #pragma unroll
@@ -140,7 +157,6 @@ __global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) q += __shfl_xor_sync(0xffffffffu, q, d);
         if (warps > 1) {
-            __syncthreads();
             if ((t & 31) == 0) sums[warp] = q;
             __syncthreads();
             q = 0.f;
@@ -150,11 +166,15 @@ __global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F
     };
     float f = 1.f, q = total(1.f);
     // Squares of values from 2^64 on overflow; the row is then taken 2^-80 times
-    // (what underflows is nothing beside them).  Every thread of a block goes in
-    // or none: the barriers inside are the block's.
-    if (__syncthreads_or(!(q <= 3.4028234663852886e38f))) {
+    // (what underflows is nothing beside them).  All threads of a block go in or none
+    // (a block of one row agrees by itself): the barriers are the block's.
+    bool over = !(q <= kF8Largest);
+    const bool mine = over;
+    if (blockDim.y > 1 && warps > 1) over = __syncthreads_or(over);
+    if (over) {
+        if (warps > 1) __syncthreads();     // the sums have been read
         const float scaled = total(kDown);
-        if (!(q <= 3.4028234663852886e38f)) {
+        if (mine) {
             f = kDown;
             q = scaled;
         }
@@ -167,7 +187,8 @@ __global__ void __launch_bounds__(1024) f8_norm_kernel(const __grid_constant__ F
         const int p = t + i * T;
         float w[8], y[8];
         const bool in = live && p < pieces;
-        unpack8<BF16>(in ? load_uint4(a.weight + 8 * p) : make_uint4(0u, 0u, 0u, 0u), w);
+        if constexpr (kAhead) unpack8<BF16>(wv[i], w);
+        else unpack8<BF16>(in ? load_uint4(a.weight + 8 * p) : make_uint4(0u, 0u, 0u, 0u), w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = in ? s[i][j] * f * inv * w[j] : 0.f;
         uint2 codes;
@@ -201,7 +222,8 @@ const void* norm_kernel(int vpt) {
         case 1: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 1>);
         case 2: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 2>);
         case 4: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 4>);
-        default: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 8>);
+        case 8: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 8>);
+        default: return reinterpret_cast<const void*>(f8_norm_kernel<BF16, 16>);
     }
 }
 
@@ -217,9 +239,12 @@ cudaError_t launch_f8_quantize(const F8RowsArgs& a, bool bf16, cudaStream_t stre
 
 cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStream_t stream) {
     const int pieces = a.hidden / 8;
+    // 4 pieces a thread, more only for long rows; fewer where rows are short, and
+    // where there are fewer rows than SMs (one row of 4096: 2.8 us with 1, 4.1 with 4)
+    const auto fits = [&](int v) { return (pieces + v - 1) / v <= norm_threads(v); };
     int vpt = 4;
-    while (vpt < 8 && (pieces + vpt - 1) / vpt > 1024) vpt *= 2;
-    while (vpt > 1 && static_cast<long long>(a.rows) * a.R <= sm_count && (pieces + vpt / 2 - 1) / (vpt / 2) <= 1024) vpt /= 2;
+    while (vpt < 16 && !fits(vpt)) vpt *= 2;
+    while (vpt > 1 && fits(vpt / 2) && (static_cast<long long>(a.rows) * a.R <= sm_count || pieces <= 32 * (vpt / 2))) vpt /= 2;
     const int T = ((pieces + vpt - 1) / vpt + 31) / 32 * 32;
     const int rows = T >= 128 ? 1 : 128 / T;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.rows) + rows - 1) / rows), static_cast<unsigned>(a.R));

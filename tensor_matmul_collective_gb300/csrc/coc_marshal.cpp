@@ -76,6 +76,23 @@ const at::Tensor* first_of(PyObject* o, int64_t* R, int64_t index = -1, bool cod
 
 coc_dtype_t code_of(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 ? COC_BF16 : COC_FP16; }
 
+// A list of R tensors of the given shape that follow each other in `all`'s memory from an offset in bytes.
+bool parts(const at::Tensor& all, int64_t R, at::IntArrayRef shape, caffe2::TypeMeta type, int64_t offset, PyObject** list,
+           void* (&p)[COC_MAX_RANKS]) {
+    int64_t n = 1;
+    for (const int64_t x : shape) n *= x;
+    const int64_t first = offset / static_cast<int64_t>(type.itemsize());
+    if ((*list = PyList_New(R)) == nullptr) return false;
+    for (int64_t r = 0; r < R; ++r) {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+        t.unsafeGetTensorImpl()->set_storage_offset(first + r * n);
+        p[r] = t.data_ptr();
+        PyList_SET_ITEM(*list, r, THPVariable_Wrap(std::move(t)));
+    }
+    return true;
+}
+
 // Outputs: the given list's tensors, or R new ones; `list` is a new reference.
 // New ones of a call on another than the current stream are that stream's
 // memory (what the current stream has freed may still be in use there), and the
@@ -109,15 +126,7 @@ bool outputs(PyObject* given, int64_t R, at::IntArrayRef shape, at::ScalarType d
     for (const int64_t x : shape) n *= x;
     const at::Tensor all = at::empty({R * n}, opt);
     if (other) all.record_stream(now);
-    if ((*list = PyList_New(R)) == nullptr) return false;
-    for (int64_t r = 0; r < R; ++r) {
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), all.dtype());
-        t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-        t.unsafeGetTensorImpl()->set_storage_offset(r * n);
-        p[r] = t.data_ptr();
-        PyList_SET_ITEM(*list, r, THPVariable_Wrap(std::move(t)));
-    }
-    return true;
+    return parts(all, R, shape, all.dtype(), 0, list, p);
 }
 
 // int32 arrays that index the cache.
@@ -302,6 +311,23 @@ struct Lists {
 
 int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
 
+// Codes (rows x cols) and scales of R ranks, given or new; both new ones are
+// one allocation, all ranks' codes and then all ranks' scales.
+bool code_outputs(PyObject* codes, PyObject* scales, int64_t R, int64_t rows, int64_t cols, const at::Device& dev, coc_stream_t stream, Lists& o) {
+    if (codes != Py_None || scales != Py_None)
+        return outputs(codes, R, {rows, cols}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) &&
+               outputs(scales, R, {rows, f8_blocks(cols)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]);
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream();
+    const bool other = reinterpret_cast<cudaStream_t>(stream) != now.stream();
+    c10::cuda::OptionalCUDAStreamGuard on;
+    if (other) on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), dev.index()));
+    const int64_t code_bytes = R * rows * cols;
+    const at::Tensor all = at::empty({code_bytes + R * rows * f8_blocks(cols)}, at::TensorOptions().dtype(at::kByte).device(dev));
+    if (other) all.record_stream(now);
+    return parts(all, R, {rows, cols}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e4m3fn), 0, &o.l[0], o.p[0]) &&
+           parts(all, R, {rows, f8_blocks(cols)}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e8m0fnu), code_bytes, &o.l[1], o.p[1]);
+}
+
 // (entry point, xs, outs, scales, stream) -> (status, codes, scales)
 PyObject* quantize_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -318,9 +344,7 @@ PyObject* quantize_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     coc_stream_t stream;
     if (!stream_of(a[4], &stream)) return nullptr;
     Lists o;
-    if (!outputs(a[2], R, {rows, h}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) ||
-        !outputs(a[3], R, {rows, f8_blocks(h)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]))
-        return PyErr_Occurred() ? nullptr : none();
+    if (!code_outputs(a[2], a[3], R, rows, h, dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(R), rows, h, x.p, o.p[0], o.p[1], code_of(*x0), stream);
@@ -352,9 +376,7 @@ PyObject* norm_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     coc_stream_t stream;
     if (!stream_of(a[8], &stream)) return nullptr;
     Lists o;
-    if (!outputs(a[5], R, {rows, h}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) ||
-        !outputs(a[6], R, {rows, f8_blocks(h)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]) ||
-        (add && !outputs(a[7], R, {rows, h}, dt, dev, stream, &o.l[2], o.p[2])))
+    if (!code_outputs(a[5], a[6], R, rows, h, dev, stream, o) || (add && !outputs(a[7], R, {rows, h}, dt, dev, stream, &o.l[2], o.p[2])))
         return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
@@ -428,9 +450,7 @@ PyObject* gated_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[7], &stream)) return nullptr;
     Lists o;
     const int64_t m = in.R * in.rows;
-    if (!outputs(a[5], in.R, {m, in.n}, at::kFloat8_e4m3fn, *in.dev, stream, &o.l[0], o.p[0]) ||
-        !outputs(a[6], in.R, {m, f8_blocks(in.n)}, at::kFloat8_e8m0fnu, *in.dev, stream, &o.l[1], o.p[1]))
-        return PyErr_Occurred() ? nullptr : none();
+    if (!code_outputs(a[5], a[6], in.R, m, in.n, *in.dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(in.R), in.rows, in.n, in.k, in.x.p, in.xs.p, in.w.p, in.ws.p, o.p[0], o.p[1], stream);

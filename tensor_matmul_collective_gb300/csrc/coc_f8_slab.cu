@@ -276,12 +276,23 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
 #pragma unroll
         for (int w = 0; w < WT; ++w) {
             const uint32_t at = sums_at + ((w * NT + i) * 128 + c8) * 4;
-            for (int b = 0; b < splits; ++b) {
-                const uint32_t src = splits > 1 ? map_to_rank(at, b) : at;
-                const float4 lo = load_part(src, splits > 1), hi = load_part(src + 16, splits > 1);
-                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            // all parts' loads first, four at a time, then their sum in order
+            for (int b0 = 0; b0 < splits; b0 += 4) {
+                float4 lo[4], hi[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[w][j] = b == 0 ? v[j] : y[w][j] + v[j];
+                for (int b = 0; b < 4; ++b) {
+                    if (b0 + b >= splits) break;
+                    const uint32_t src = splits > 1 ? map_to_rank(at, b0 + b) : at;
+                    lo[b] = load_part(src, splits > 1);
+                    hi[b] = load_part(src + 16, splits > 1);
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (b0 + b >= splits) break;
+                    const float v[8] = {lo[b].x, lo[b].y, lo[b].z, lo[b].w, hi[b].x, hi[b].y, hi[b].z, hi[b].w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[w][j] = b0 + b == 0 ? v[j] : y[w][j] + v[j];
+                }
             }
         }
         const bool in = row < p.m && col < p.n;

@@ -408,7 +408,8 @@ cudaError_t launch_n(const F8Args& a, int nt, int sm_count, cudaStream_t stream)
 // costs 3.  Up to 128 rows (gated: 64) the weights' bytes decide, and slabs
 // stream them better.  Measured, slab / tile: n 8192, k 8 x 3584, m 128 45 / 78 us,
 // 256 65 / 80, 384 106 / 85, 4096 816 / 574; n 1024, k 4096, m 512 11.7 / 15.2, 2048
-// 15.0 / 15.7, 4096 22.7 / 17.3; n 2048, k 1024, m 512 10.3 / 9.0; gated, 8 x 3584, k
+// 15.0 / 15.7, 4096 22.7 / 17.3; n 2048, k 1024, m 512 10.3 / 9.0; n 2 x 1384, m 666, k 4096
+// 15.3 / 15.8, 4112 21.7 / 18.5, 4128 17.0 / 16.4; gated, 8 x 3584, k
 // 8192, m 64 84 / 87, 128 105 / 88, 4096 1807 / 1049; 11008, k 4096, m 64 28 / 39, 128 32 / 33.
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
     if (const char* e = std::getenv("COC_F8_TILE")) return std::atoi(e) != 0;
@@ -417,9 +418,11 @@ bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, in
     const int64_t cols = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R);
     const int64_t units = (m + 255) / 256 * ((n + 255) / 256) * cols, slabs = (m + 127) / 128 * ((n + 127) / 128) * cols;
     const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>(8, sm_count / slabs));
-    const double tile = 5.0 + 0.335 * static_cast<double>((units + pairs - 1) / pairs * blocks);
-    const double slab = 5.5 + (slabs <= sm_count ? 0.3 * static_cast<double>(blocks) / static_cast<double>(split) + (split > 1 ? 3.0 : 0.0)
-                                                 : 0.52 * static_cast<double>((slabs + 2 * sm_count - 1) / (2 * sm_count) * blocks));
+    // rows that start between L2's sectors (16 bytes) or lines are fetched in more of them
+    const double tile_rows = k % 32 ? 1.25 : k % 128 ? 1.03 : 1.0, slab_rows = k % 32 ? 1.6 : k % 128 ? 1.1 : 1.0;
+    const double tile = 5.0 + 0.335 * tile_rows * static_cast<double>((units + pairs - 1) / pairs * blocks);
+    const double slab = 5.5 + (slabs <= sm_count ? 0.3 * slab_rows * static_cast<double>(blocks) / static_cast<double>(split) + (split > 1 ? 3.0 : 0.0)
+                                                 : 0.52 * slab_rows * static_cast<double>((slabs + 2 * sm_count - 1) / (2 * sm_count) * blocks));
     return tile < slab;
 }
 

@@ -1,14 +1,17 @@
-"""The attention block of a decode step over R tensor-parallel ranks, from the
-operators of ``coc``: the fused QKV projection (ALL_GATHER_MATMUL of the
-sequence-parallel input), append to the 8-bit key/value cache with the position
-rotation, attention over the cache, and the output projection with 4-bit
-weights (w4A16 MATMUL_ALL_REDUCE).
+"""The blocks of a decode step over R tensor-parallel ranks, from the
+operators of ``coc``.  Attention: the fused QKV projection (ALL_GATHER_MATMUL of
+the sequence-parallel input), append to the 8-bit key/value cache with the
+position rotation, attention over the cache, and the output projection with
+4-bit weights (w4A16 MATMUL_ALL_REDUCE).  Feed-forward, in 8-bit floating point:
+residual addition and RMS norm, gate and up projection with the activation
+(ALL_GATHER), down projection (MATMUL_REDUCE_SCATTER).
 
 ``python -m tensor_matmul_collective_gb300.decode_step`` appends the keys and
 values of prompts to the cache (their own attention is not part of it) and then
 runs a number of single-token steps of one layer with random weights and prints
 the time of a step (``--ranks 8 --hidden 8192 --heads 64 --kv-heads 8 --batch 64``
-by default; the step is captured into a CUDA graph).
+by default; the step is captured into a CUDA graph).  With ``--ffn 28672`` the
+feed-forward block of that size follows the attention block in every step.
 """
 from __future__ import annotations
 
@@ -58,6 +61,51 @@ class AttentionBlock:
                                            zeros=self.zeros, outs=outs)
 
 
+class MlpBlock:
+    """One layer's gated feed-forward block on R ranks with 8-bit weights: rank r
+    holds ffn/R columns of the gate and the up projection and as many rows of
+    the down projection.
+
+    norm: hidden values in the activations' type.  w_up[r], up_scales[r]: the
+    rank's gate rows, then its up rows (coc.f8_pack with parts=2 of (2 ffn/R) x
+    hidden); w_down[r], down_scales[r]: hidden x ffn/R (coc.f8_pack)."""
+
+    def __init__(self, norm, w_up, up_scales, w_down, down_scales, eps: float = 1e-6):
+        self.norm, self.eps = norm, eps
+        self.w_up, self.up_scales, self.w_down, self.down_scales = w_up, up_scales, w_down, down_scales
+
+    def __call__(self, xs, residuals=None, outs=None, sums=None, stream=None):
+        """xs[r], residuals[r]: rank r's rows (any number, the same on every
+        rank) x hidden.  Returns (outs, sums): the block's output of the rank's rows,
+        and xs + residuals (the residual that goes with it; None without
+        residuals).  With a stream everything that is allocated on the way is that stream's."""
+        if stream is not None and coc._stream(stream) != torch.cuda.current_stream().cuda_stream:
+            now = torch.cuda.current_stream()
+            with torch.cuda.stream(coc._as_stream(stream)):
+                new = self(xs, residuals, outs=outs, sums=sums)
+            for given, ts in ((outs, new[0]), (sums, new[1])):
+                if given is None and ts is not None:
+                    ts[0].record_stream(now)        # all ranks' are one allocation
+            return new
+        x, x_scales, sums = coc.add_rms_norm_f8(xs, self.norm, residuals=residuals, eps=self.eps, sums=sums)
+        h, h_scales = coc.all_gather_gated_matmul_f8(x, x_scales, self.w_up, self.up_scales)
+        return coc.matmul_reduce_scatter_f8(h, h_scales, self.w_down, self.down_scales, outs=outs, dtype=xs[0].dtype), sums
+
+
+def random_mlp(R: int, hidden: int, ffn: int, dtype=torch.bfloat16, seed: int = 0, device="cuda"):
+    """An MlpBlock with random weights."""
+    g = torch.Generator(device=device)
+    g.manual_seed(seed)
+    f = ffn // R
+
+    def normal(n, k, std):
+        return torch.randn(n, k, generator=g, device=device) * std
+    up = [coc.f8_pack(normal(2 * f, hidden, hidden ** -0.5), parts=2) for _ in range(R)]
+    down = [coc.f8_pack(normal(hidden, f, ffn ** -0.5)) for _ in range(R)]
+    norm = (1.0 + 0.1 * torch.randn(hidden, generator=g, device=device)).to(dtype)
+    return MlpBlock(norm, *(list(t) for t in zip(*up)), *(list(t) for t in zip(*down)))
+
+
 def rotation_tables(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     """(cos, sin), float32 positions x rot_dim/2, of the angles p * base**(-2j/rot_dim)."""
     freq = base ** (-torch.arange(rot_dim // 2, dtype=torch.float64, device=device) * 2 / rot_dim)
@@ -94,6 +142,7 @@ def main() -> None:
     ap.add_argument("--prompt", type=int, default=1024, help="tokens every sequence starts with")
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--page", type=int, default=64)
+    ap.add_argument("--ffn", type=int, default=0, help="feed-forward size (a multiple of 16 x ranks); 0: no feed-forward block")
     a = ap.parse_args()
     R, B, dev = a.ranks, a.batch, torch.device("cuda")
     per_seq = -(-(a.prompt + a.steps + 1) // a.page)
@@ -113,10 +162,18 @@ def main() -> None:
     x = [torch.randn(B // R, a.hidden, device=dev).to(torch.bfloat16) for _ in range(R)]
     outs = [torch.empty(B, a.hidden, dtype=torch.bfloat16, device=dev) for _ in range(R)]
     lens += 1
-    block(x, table, lens, outs=outs)
+    mlp = random_mlp(R, a.hidden, a.ffn) if a.ffn else None
+    rows = B // R
+
+    def step():
+        y = block(x, table, lens, outs=outs)
+        if mlp is not None:
+            mlp([t[r * rows:(r + 1) * rows] for r, t in enumerate(y)], residuals=x)
+
+    step()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        block(x, table, lens, outs=outs)
+        step()
     torch.cuda.synchronize()
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     begin.record()

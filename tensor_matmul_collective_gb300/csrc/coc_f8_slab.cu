@@ -15,7 +15,7 @@
 // added in their order.
 //
 // Roles: warp 0 copies tiles (TMA), warp 1 issues products and owns tensor
-// memory, warps 2 and 3 gather scale words, alternating; then all four warps
+// memory, warps 2 and 3 gather scale words, alternating; then all eight warps
 // read the accumulators.
 #include <algorithm>
 #include <atomic>
@@ -27,6 +27,7 @@ namespace coc {
 namespace {
 
 constexpr int kWTile = 128 * 128;       // bytes of 128 weight rows' k-block
+constexpr int kSlabThreads = 256;
 constexpr int kMaxStages = 8;
 constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight, in shared and in tensor memory
 constexpr int kSfCols = 16;             // columns of a run's scale words in tensor memory
@@ -69,7 +70,7 @@ __device__ __forceinline__ float4 load_part(uint32_t addr, bool cluster) {
 }
 
 template <int NT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8Args p) {
+__global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_constant__ F8Args p) {
     using C = SlabCfg<NT, GATED>;
     constexpr int WT = C::WT, KPS = C::KPS;
     const uint32_t S = p.stages;
@@ -99,31 +100,34 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
     const int b1 = static_cast<int>(static_cast<long long>(total) * (split + 1) / splits);
     const bool ag = p.op == OP_AG;
 
-    if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+    // The producer needs the barriers alone, and nobody but warp 1 tensor memory
+    // before the end: loads are on their way while the rest is set up.
+    if (warp == 0) {
+        if (lane == 0) {
+            for (uint32_t s = 0; s < S; ++s) {
+                mbar_init(smem_u32(&full[s]), 1);
+                mbar_init(smem_u32(&empty[s]), 1);
+            }
+            for (int s = 0; s < kSfStages; ++s) {
+                mbar_init(smem_u32(&sf_full[s]), 1);
+                mbar_init(smem_u32(&sf_empty[s]), 1);
+            }
+            mbar_init(smem_u32(done), 1);
+            mbar_init(smem_u32(never), 1);
+            *abort_word = 0u;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            fence_proxy_async_smem();
+        } else if (total > 0 && lane <= p.shards) {
+            prefetch_tmap(&p.tm_w[ag ? r : lane - 1]);
+            prefetch_tmap(&p.tm_x[ag ? 0 : lane - 1]);
         }
-        for (int s = 0; s < kSfStages; ++s) {
-            mbar_init(smem_u32(&sf_full[s]), 1);
-            mbar_init(smem_u32(&sf_empty[s]), 1);
-        }
-        mbar_init(smem_u32(done), 1);
-        mbar_init(smem_u32(never), 1);
-        *abort_word = 0u;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async_smem();
+        __syncwarp();
+        named_arrive(1, kSlabThreads);
+    } else {
+        named_sync(1, kSlabThreads);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     grid_dependency_wait();
     grid_dependents_launch();
-    const uint32_t tmem = *tmem_slot;
     bool ok = true;
     if (p.inject_timeout) ok = warp_wait(smem_u32(never), 0, ctl, 0x700u);
 
@@ -166,6 +170,12 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
                 if (filled & (1u << s)) drain_wait(smem_u32(&full[s]), (parity >> s) & 1u, kDrainNs);
         __syncwarp();
     } else if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+        tmem_relinquish();
+        tc_fence_before();
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
         const uint64_t tiles = make_sdesc(smem_u32(smem), 16, 1024);
         uint32_t stage = 0, phase = 0, onto = 0;
         int run_i = 0;
@@ -205,9 +215,10 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
             if (ok) tc_commit_f8<false>(smem_u32(&sf_empty[ss]));
         }
         tc_commit_f8<false>(smem_u32(done));
-        if (!ok) drain_wait(smem_u32(done), 0, kDrainNs);
+        if (!ok || !warp_wait(smem_u32(done), 0, ctl, 0x760u)) drain_wait(smem_u32(done), 0, kDrainNs);
+        tc_fence_before();
         __syncwarp();
-    } else {
+    } else if (warp < 4) {
         // scale words: the weights' are one for all of a tile's rows, the activations' one a row
         constexpr int XW = NT > 32 ? NT / 32 : 1;
         int run_i = 0;
@@ -246,31 +257,33 @@ __global__ void __launch_bounds__(128) f8_slab_kernel(const __grid_constant__ F8
         }
     }
 
-    // ---- accumulators to shared memory: sums[weight tile][activation row][weight row]
-    if (ok) ok = warp_wait(smem_u32(done), 0, ctl, 0x760u);
-    tc_fence_after();
-    // every warp is through with the ring (an abort's products too: warp 1 waited for them)
+    // ---- accumulators to shared memory: sums[weight tile][activation row][weight row].  All products are done and the
+    // ring is idle (after an abort too: warp 1 waited for them, warp 0 for its copies).
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int rows = min(NT, p.m - row0);
     float* sums = reinterpret_cast<float*>(smem);
-    for (int c = 0; c < WT * NT; c += 16) {
+    for (int c = 16 * (warp >> 2); c < WT * NT; c += 32) {
+        if (c % NT >= rows) continue;
         uint32_t v[16];
         if (b1 > b0) {
-            tmem_ld_16cols(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, v);
+            tmem_ld_16cols(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
             tmem_wait_ld();
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 0u;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + 32 * warp + lane] = __uint_as_float(v[i]);
+        for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
     }
     tc_fence_before();
     if (splits > 1) cluster_sync();
     else __syncthreads();
 
-    // ---- 16 threads an activation row, 8 columns each; the cluster's blocks share the rows
+    // ---- 16 threads an activation row, 8 columns each; the cluster's warps share the rows
     const uint32_t sums_at = smem_u32(sums);
-    for (int x = threadIdx.x + split * 128; x < NT * 16; x += 128 * splits) {
+    for (int x = (warp * splits + split) * 32 + lane; x < ((rows * 16 + 31) & ~31); x += kSlabThreads * splits) {
         const int i = x >> 4, row = row0 + i, c8 = (x & 15) * 8, col = nt * 128 + c8;
         float y[WT][8];
 #pragma unroll
@@ -346,7 +359,7 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.blockDim = dim3(kSlabThreads, 1, 1);
     cfg.stream = stream;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -372,12 +385,13 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     const int total = a.shards * ((a.kblocks + 3) / 4);
     int room = 0;
     if ((e = clusters(1, &room)) != cudaSuccess) return e;
-    const bool alone = C::SHARED == 0 || tiles <= room;
+    const bool fit = C::SHARED == 0 || tiles <= room;
     a.splits = 1;
     for (int k = 2; k <= 8 && k <= total && tiles * k <= sm_count; ++k) {
         if ((e = clusters(k, &room)) != cudaSuccess) return e;
         if (tiles <= room) a.splits = k;
     }
+    const bool alone = fit && (C::SHARED == 0 || C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
     a.stages = alone ? C::ALONE : C::SHARED;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
     cfg.dynamicSmemBytes = C::REST + a.stages * C::STAGE;
@@ -443,7 +457,8 @@ int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 
 // many ranges (2 to 8) as clusters of that size find an SM for every block: a
 // block alone on an SM has all its shared memory for the ring.  More tiles
 // than SMs go unsplit, two blocks on an SM, which overlaps one's beginning and end
-// with the other's middle.  Measured, ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1
+// with the other's middle.  So do blocks of up to 8 k-blocks: the next launch's
+// set themselves up beside them (n 4096, k 4096, m 1 6.8 to 6.2 us).  Measured, ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1
 // 9.6 / 7.6 / 7.0 / 17.5 us; n 8192, k 8 x 3584, m 64 49 / 41 / 49 / 76 (shared 70 /
 // 47 / 44 / 55); n 14336, k 8 x 7168, m 16 120 / 128 / 144 / 162 (shared 148 / 127 /
 // 132 / 151); n 1024, k 2 x 8192, m 16 27 / 17 / 12 / 9.0.  Gated, 8 x 3584, k 8192, m

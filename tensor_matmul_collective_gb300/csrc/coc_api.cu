@@ -1894,7 +1894,7 @@ static coc_status_t f8_matmul(int op, bool gated, int R, int64_t rows, int64_t n
         st = map(&a.tm_w[r], w[r], gated ? 2 * n : n, 128);
         a.w_scale[r] = static_cast<const uint8_t*>(w_scale[r]);
         if (st == COC_OK && (!ag || r == 0)) {
-            st = map(&a.tm_x[r], ag ? x0 : x[r], m, static_cast<uint32_t>(tiles ? 128 : f8_slab_rows(m)));
+            st = map(&a.tm_x[r], ag ? x0 : x[r], m, static_cast<uint32_t>(tiles ? 128 : f8_slab_rows(m, gated)));
             a.x_scale[r] = ag ? s0 : static_cast<const uint8_t*>(x_scale[r]);
         }
     }

@@ -47,7 +47,9 @@ struct SlabCfg {
     static constexpr int ALONE = (224 * 1024 - REST) / STAGE;
     static constexpr int HALF = (112 * 1024 - REST) / STAGE;
     static constexpr int SHARED = HALF >= 2 && TMEM <= 256 && SUMS <= HALF * STAGE ? HALF : 0;
-    static_assert(ALONE >= 2 && ALONE <= kMaxStages && SUMS <= ALONE * STAGE && ALONE * STAGE + REST <= kSlabSmemCap, "shared memory");
+    static constexpr int PARTS = WT * (NT + 7) * 512;           // the cluster's sums of a block's rows, rounded up for each block
+    static_assert(ALONE >= 2 && ALONE <= kMaxStages && SUMS + PARTS <= ALONE * STAGE && ALONE * STAGE + REST <= kSlabSmemCap, "shared memory");
+    static_assert(SHARED == 0 || KPS == 1 || SUMS + PARTS <= SHARED * STAGE, "shared memory (split blocks that share an SM)");
 };
 
 // 32 lanes x 16 consecutive columns: thread t receives lane (base + t).
@@ -60,14 +62,13 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&v)[16]
         : "memory");
 }
 
-__device__ __forceinline__ float4 load_part(uint32_t addr, bool cluster) {
+__device__ __forceinline__ float4 load_part(uint32_t addr) {
     float4 v;
-    if (cluster)
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
+
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 
 template <int NT, bool GATED, bool BF16>
 __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_constant__ F8Args p) {
@@ -84,7 +85,9 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     uint64_t* sf_full = empty + kMaxStages; // [kSfStages] a run's scale words written
     uint64_t* sf_empty = sf_full + kSfStages;   // [kSfStages] the run's products are done
     uint64_t* done = sf_empty + kSfStages;  // all products are done
-    uint64_t* never = done + 1;
+    uint64_t* idle = done + 1;              // the products of all the cluster's blocks are done: their rings are free
+    uint64_t* parts = idle + 1;             // the other blocks' sums of this block's rows are here
+    uint64_t* never = parts + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never + 1);
     uint32_t* abort_word = tmem_slot + 1;
 
@@ -99,6 +102,9 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     const int b0 = static_cast<int>(static_cast<long long>(total) * split / splits);
     const int b1 = static_cast<int>(static_cast<long long>(total) * (split + 1) / splits);
     const bool ag = p.op == OP_AG;
+    // the cluster's blocks finish own_rows of the tile's rows each
+    const int rows = min(NT, p.m - row0), own_rows = (rows + splits - 1) / splits;
+    const int own = max(0, min(own_rows, rows - split * own_rows));
 
     // The producer needs the barriers alone, and nobody but warp 1 tensor memory
     // before the end: loads are on their way while the rest is set up.
@@ -113,10 +119,13 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
                 mbar_init(smem_u32(&sf_empty[s]), 1);
             }
             mbar_init(smem_u32(done), 1);
+            mbar_init(smem_u32(idle), splits);
+            mbar_init(smem_u32(parts), 1);
             mbar_init(smem_u32(never), 1);
             *abort_word = 0u;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             fence_proxy_async_smem();
+            if (splits > 1) mbar_expect_tx(smem_u32(parts), (splits - 1) * WT * own * 512);
         } else if (total > 0 && lane <= p.shards) {
             prefetch_tmap(&p.tm_w[ag ? r : lane - 1]);
             prefetch_tmap(&p.tm_x[ag ? 0 : lane - 1]);
@@ -126,6 +135,7 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     } else {
         named_sync(1, kSlabThreads);
     }
+    if (splits > 1) cluster_arrive_relaxed();       // the cluster's barriers are there (waited for before they are used)
     grid_dependency_wait();
     grid_dependents_launch();
     bool ok = true;
@@ -261,9 +271,13 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     // ring is idle (after an abort too: warp 1 waited for them, warp 0 for its copies).
     __syncthreads();
     tc_fence_after();
+    if (splits > 1) {
+        cluster_wait();
+        if (warp == 0 && lane < splits) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(idle), lane));
+    }
     const uint32_t tmem = *tmem_slot;
-    const int rows = min(NT, p.m - row0);
     float* sums = reinterpret_cast<float*>(smem);
+    const uint32_t sums_at = smem_u32(sums), parts_at = sums_at + C::SUMS;
     for (int c = 16 * (warp >> 2); c < WT * NT; c += 32) {
         if (c % NT >= rows) continue;
         uint32_t v[16];
@@ -278,37 +292,44 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
     }
     tc_fence_before();
-    if (splits > 1) cluster_sync();
-    else __syncthreads();
+    if (splits > 1) fence_proxy_async_smem();
+    __syncthreads();
+    if (splits > 1) {
+        // every block's rows of this block's sums go to it in one piece a weight tile, behind its own sums in its idle ring:
+        // parts[block][weight tile][own row][weight row].  (Read row by row from the others' shared memory between two
+        // cluster barriers they took longer: n 4096, k 4096, m 64 8.9 us, with nothing exchanged 5.5.)
+        if (warp == 0) {
+            const bool go = warp_wait<true>(smem_u32(idle), 0, ctl, 0x770u);
+            const int theirs = min(own_rows, rows - lane * own_rows);
+            if (go && lane < splits && lane != split && theirs > 0) {
+                const uint32_t bar = map_to_rank(smem_u32(parts), lane);
+#pragma unroll
+                for (int w = 0; w < WT; ++w)
+                    bulk_copy_s2s_signal(map_to_rank(parts_at + (split * WT + w) * own_rows * 512, lane), sums_at + (w * NT + lane * own_rows) * 512,
+                                         theirs * 512, bar);
+            }
+            __syncwarp();
+        }
+        if (own > 0) warp_wait<true>(smem_u32(parts), 0, ctl, 0x780u);
+        __syncwarp();
+        cluster_arrive_relaxed();       // this block's part is over; waited for before it leaves
+    }
 
-    // ---- 16 threads an activation row, 8 columns each; the cluster's warps share the rows
-    const uint32_t sums_at = smem_u32(sums);
-    for (int x = (warp * splits + split) * 32 + lane; x < ((rows * 16 + 31) & ~31); x += kSlabThreads * splits) {
-        const int i = x >> 4, row = row0 + i, c8 = (x & 15) * 8, col = nt * 128 + c8;
+    // ---- 16 threads an activation row, 8 columns each
+    for (int x = threadIdx.x; x < ((own * 16 + 31) & ~31); x += kSlabThreads) {
+        const int o = x >> 4, i = split * own_rows + o, row = row0 + i, c8 = (x & 15) * 8, col = nt * 128 + c8;
         float y[WT][8];
 #pragma unroll
         for (int w = 0; w < WT; ++w) {
-            const uint32_t at = sums_at + ((w * NT + i) * 128 + c8) * 4;
-            // all parts' loads first, four at a time, then their sum in order
-            for (int b0 = 0; b0 < splits; b0 += 4) {
-                float4 lo[4], hi[4];
+            for (int b = 0; b < splits; ++b) {      // in the ranges' order
+                const uint32_t at = b == split ? sums_at + ((w * NT + i) * 128 + c8) * 4 : parts_at + (((b * WT + w) * own_rows + o) * 128 + c8) * 4;
+                const float4 lo = load_part(at), hi = load_part(at + 16);
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b0 + b >= splits) break;
-                    const uint32_t src = splits > 1 ? map_to_rank(at, b0 + b) : at;
-                    lo[b] = load_part(src, splits > 1);
-                    hi[b] = load_part(src + 16, splits > 1);
-                }
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b0 + b >= splits) break;
-                    const float v[8] = {lo[b].x, lo[b].y, lo[b].z, lo[b].w, hi[b].x, hi[b].y, hi[b].z, hi[b].w};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[w][j] = b0 + b == 0 ? v[j] : y[w][j] + v[j];
-                }
+                for (int j = 0; j < 8; ++j) y[w][j] = b == 0 ? v[j] : y[w][j] + v[j];
             }
         }
-        const bool in = row < p.m && col < p.n;
+        const bool in = o < own && col < p.n;
         if constexpr (GATED) {
             float top = 0.f;
 #pragma unroll
@@ -341,8 +362,14 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
             }
         }
     }
-    if (splits > 1) cluster_sync();     // no block leaves while its sums are read
-    else __syncthreads();
+    if (splits > 1) {
+        if (*reinterpret_cast<volatile uint32_t*>(abort_word) != 0u) {      // copies that nobody waited for
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 200000ull) {
+            }
+        }
+        cluster_wait();     // every block has its parts: none leaves while its sums are copied
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM);
@@ -410,7 +437,9 @@ cudaError_t launch_n(const F8Args& a, int nt, int sm_count, cudaStream_t stream)
         case 16: return launch_t<16, GATED, BF16>(a, sm_count, stream);
         case 32: return launch_t<32, GATED, BF16>(a, sm_count, stream);
         case 64: return launch_t<64, GATED, BF16>(a, sm_count, stream);
-        default: return launch_t<128, GATED, BF16>(a, sm_count, stream);
+        default:
+            if constexpr (!GATED) return launch_t<128, GATED, BF16>(a, sm_count, stream);
+            else return cudaErrorInvalidValue;
     }
 }
 
@@ -440,18 +469,19 @@ bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, in
     return tile < slab;
 }
 
+// (gated: more rows go to the tiles)
+int f8_slab_rows(int64_t m, bool gated) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || gated ? 64 : 128; }
+
 template <int NT>
 static int kps_of(bool gated) { return gated ? SlabCfg<NT, true>::KPS : SlabCfg<NT, false>::KPS; }
 int f8_slab_kblocks(int64_t m, bool gated) {
-    switch (f8_slab_rows(m)) {
+    switch (f8_slab_rows(m, gated)) {
         case 16: return kps_of<16>(gated);
         case 32: return kps_of<32>(gated);
         case 64: return kps_of<64>(gated);
-        default: return kps_of<128>(gated);
+        default: return SlabCfg<128, false>::KPS;
     }
 }
-
-int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 
 // Blocks.  Where the tiles leave SMs free, a tile's contraction is cut into as
 // many ranges (2 to 8) as clusters of that size find an SM for every block: a
@@ -465,7 +495,7 @@ int f8_slab_rows(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 
 // 64: shared 84 unsplit, 92 in two, alone 88.
 cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_count, cudaStream_t stream) {
     F8Args a = args;
-    const int nt = f8_slab_rows(a.m);
+    const int nt = f8_slab_rows(a.m, gated);
     a.m_tiles = (a.m + nt - 1) / nt;
     if (gated) return launch_n<true, true>(a, nt, sm_count, stream);
     return bf16 ? launch_n<false, true>(a, nt, sm_count, stream) : launch_n<false, false>(a, nt, sm_count, stream);

@@ -267,7 +267,7 @@ cudaError_t launch_f8_norm(const F8RowsArgs& a, bool bf16, int sm_count, cudaStr
 // Products of codes.  op: OP_AR, OP_RS (m rows, the shards summed) or OP_AG
 // (m gathered rows in x[0], every rank's n columns); gated: OP_AG with 2 n
 // weight rows a rank, gate first, whose result is codes and scales.  Maps:
-// 128 columns x 128 rows of a weight, 128 x f8_slab_rows(m) of x
+// 128 columns x 128 rows of a weight, 128 x f8_slab_rows(m, gated) of x
 // (coc_f8_slab.cu) or 128 x 128 (coc_f8_tile.cu), 128-byte swizzle, zero past the ends;
 // maps_3d: (128, rows, k-blocks), boxes of f8_slab_kblocks(m) k-blocks.
 struct F8Args {
@@ -291,7 +291,7 @@ struct F8Args {
 // Which kernel takes m rows (sizes as in F8Args): tiles of CTA pairs, or slabs
 // of weight rows; and the rows of their X maps' boxes (tiles: 128).
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count);
-int f8_slab_rows(int64_t m);
+int f8_slab_rows(int64_t m, bool gated);
 int f8_slab_kblocks(int64_t m, bool gated);     // k-blocks of a stage: 1 or 2
 cudaError_t launch_f8_tile(const F8Args& a, bool gated, bool bf16, cudaStream_t stream);
 cudaError_t launch_f8_slab(const F8Args& a, bool gated, bool bf16, int sm_count, cudaStream_t stream);

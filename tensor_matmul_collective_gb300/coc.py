@@ -152,7 +152,7 @@ def _marshal():
             from . import _coc_marshal as m
         except ImportError as e:
             m = None
-            warnings.warn(f"_coc_marshal does not load ({e}): the decode-step calls take the slower checks in Python; build() makes it",
+            warnings.warn(f"_coc_marshal does not load ({e}): the decode-step and 8-bit calls take the slower checks in Python; build() makes it",
                           RuntimeWarning, stacklevel=3)
         _native = False if m is None else (
             m, *(ctypes.cast(f, ctypes.c_void_p).value for f in (L.coc_kv_cache_append, L.coc_kv_cache_attention,

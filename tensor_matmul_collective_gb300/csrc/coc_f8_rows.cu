@@ -8,7 +8,10 @@
 //
 // What bounds it.  Every value is read and written once: 7 bytes a value with
 // residual and sum, 3 without.  A row stays in registers between the sum of
-// squares and the scaling.
+// squares and the scaling, so HBM is the bound: 8 x 1024 rows of 8192 with
+// residual take 70 us, 6.7 TB/s (a copy: 6.8); quantised alone, 2 x 4095 rows of
+// 3584 16.4 us, 5.4 TB/s (instructions: 100 for 24 bytes a lane); one row 2.8 us,
+// the launch and one chain of load, sum and store.
 //
 // Layout.  16 lanes hold a block of 128 (8 values, 16 bytes each), so its
 // largest magnitude is four shuffles away and codes go out 8 bytes a lane.

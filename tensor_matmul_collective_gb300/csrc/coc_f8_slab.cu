@@ -7,12 +7,21 @@
 // the same activations, h = silu(g) u, and quantises h per row and 128 columns,
 // which is one tile.
 //
-// What bounds it.  n k bytes of weights, read once.  A tile is 128 weight rows
-// by NT activation rows, so few rows cost the tensor cores little.
+// What bounds it.  n k bytes of weights, read once: n 8192, k 8 x 3584, 64 rows
+// on 8 ranks take 39 to 41 us, 6.0 to 6.3 TB/s with the outputs; gated 8 x 3584, k
+// 8192, 64 rows 76 to 80 us, 6.1 TB/s; gated 11008, k 4096, one row 18.5 us, 4.9
+// TB/s; n 4096, k 4096, one row 5.5 to 5.9 us, of which the weights' bytes are 2.5.  A
+// tile is 128 weight rows by NT activation rows, so few rows cost the tensor cores
+// little (a product of 32 of k takes 40 cycles with 16 rows, 65 with 128).
+//
+// Stages.  A k-block is 128 of k, one 128-byte swizzled row; two of them come
+// in one box where the ring has room (a block's SM took 600 cycles a k-block
+// before, 470 then), and the loads start before the rest is set up.
 //
 // Split.  Where the tiles do not fill the GPU, the blocks of a cluster take
-// contiguous ranges of the k-blocks; the parts meet in shared memory and are
-// added in their order.
+// contiguous ranges of the k-blocks.  Each finishes a part of the rows: the
+// others' sums of them come as bulk copies between shared memories and are added
+// in the ranges' order.
 //
 // Roles: warp 0 copies tiles (TMA), warp 1 issues products and owns tensor
 // memory, warps 2 and 3 gather scale words, alternating; then all eight warps
@@ -420,6 +429,7 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     }
     const bool alone = fit && (C::SHARED == 0 || C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
     a.stages = alone ? C::ALONE : C::SHARED;
+    if (a.splits > 1 && a.stages * C::STAGE < C::SUMS + C::PARTS) return cudaErrorInvalidConfiguration;    // (never: see SlabCfg)
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
     cfg.dynamicSmemBytes = C::REST + a.stages * C::STAGE;
     attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);
@@ -446,30 +456,33 @@ cudaError_t launch_n(const F8Args& a, int nt, int sm_count, cudaStream_t stream)
 }  // namespace
 
 // Tiles of CTA pairs or slabs of weight rows, by the time either takes for its
-// rounds of k-blocks: a tile's k-block takes 0.335 us, a slab's of 128 rows 0.3
-// where it has an SM to itself and 0.52 where two share one; joining ranges
-// costs 3.  Up to 128 rows (gated: 64) the weights' bytes decide, and slabs
-// stream them better.  Measured, slab / tile: n 8192, k 8 x 3584, m 128 45 / 78 us,
-// 256 65 / 80, 384 106 / 85, 4096 816 / 574; n 1024, k 4096, m 512 11.7 / 15.2, 2048
-// 15.0 / 15.7, 4096 22.7 / 17.3; n 2048, k 1024, m 512 10.3 / 9.0; n 2 x 1384, m 666, k 4096
-// 15.3 / 15.8, 4112 21.7 / 18.5, 4128 17.0 / 16.4; gated, 8 x 3584, k
-// 8192, m 64 84 / 87, 128 105 / 88, 4096 1807 / 1049; 11008, k 4096, m 64 28 / 39, 128 32 / 33.
+// rounds of k-blocks (us, measured): a tile 6 and 0.31 a k-block (gated 8 and
+// 0.31), a slab of 128 rows (gated: of 64) 5 and 0.28 (0.39) where it has an SM to
+// itself, 0.5 (0.83) where two share one, and 2.5 to join ranges.  Up to 128 rows
+// (gated: 64) the weights' bytes decide, and slabs stream them better.  Measured,
+// slab / tile: n 8192, k 8 x 3584, m 128 43 / 78 us, 256 68 / 80, 384 109 / 93, 4096
+// 816 / 574; n 1024, k 4096, m 512 9.6 / 15.1, 2048 13.8 / 15.2, 4096 22.6 / 17.1; n
+// 4096, k 1024, m 512 8.2 / 9.0, 1024 10.5 / 9.6; n 2 x 1384, m 666, k 4096 15.3 / 15.8,
+// 4112 21.7 / 18.5, 4128 17.0 / 16.4; gated, 8 x 3584, k 8192, m 64 81 / 88, 96 110 /
+// 90, 4096 1807 / 1049; 1376, k 4096, m 128 10.4 / 16.5, 512 17.8 / 17.2; 3584, k 8192,
+// m 128 19.3 / 27.4, 256 28.1 / 27.5.
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
     if (const char* e = std::getenv("COC_F8_TILE")) return std::atoi(e) != 0;
-    if (m <= (gated ? 64 : 128)) return false;
-    if (gated) return true;
-    const int64_t cols = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R);
-    const int64_t units = (m + 255) / 256 * ((n + 255) / 256) * cols, slabs = (m + 127) / 128 * ((n + 127) / 128) * cols;
+    const int64_t slab_m = gated ? 64 : 128;
+    if (m <= slab_m) return false;
+    const int64_t ranks = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R), n_tiles = (n + 127) / 128;
+    const int64_t units = (m + 255) / 256 * (gated ? n_tiles : (n_tiles + 1) / 2) * ranks, slabs = (m + slab_m - 1) / slab_m * n_tiles * ranks;
     const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>(8, sm_count / slabs));
+    const int64_t rounds = slabs <= sm_count ? 1 : (slabs + 2 * sm_count - 1) / (2 * sm_count);
     // rows that start between L2's sectors (16 bytes) or lines are fetched in more of them
     const double tile_rows = k % 32 ? 1.25 : k % 128 ? 1.03 : 1.0, slab_rows = k % 32 ? 1.6 : k % 128 ? 1.1 : 1.0;
-    const double tile = 5.0 + 0.335 * tile_rows * static_cast<double>((units + pairs - 1) / pairs * blocks);
-    const double slab = 5.5 + (slabs <= sm_count ? 0.3 * slab_rows * static_cast<double>(blocks) / static_cast<double>(split) + (split > 1 ? 3.0 : 0.0)
-                                                 : 0.52 * slab_rows * static_cast<double>((slabs + 2 * sm_count - 1) / (2 * sm_count) * blocks));
+    const double each = slabs <= sm_count ? (gated ? 0.39 : 0.28) : (gated ? 0.83 : 0.5);
+    const double tile = (gated ? 8.0 : 6.0) + 0.31 * tile_rows * static_cast<double>((units + pairs - 1) / pairs * blocks);
+    const double slab = 5.0 + each * slab_rows * static_cast<double>(rounds * blocks) / static_cast<double>(split) + (split > 1 ? 2.5 : 0.0);
     return tile < slab;
 }
 
-// (gated: more rows go to the tiles)
+// (gated slabs have two weight tiles: 128 rows of both would leave no ring)
 int f8_slab_rows(int64_t m, bool gated) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 || gated ? 64 : 128; }
 
 template <int NT>

@@ -4,13 +4,23 @@
 //
 // Mathematics as in coc_f8_slab.cu.
 //
-// What bounds it.  The tensor cores: a stage (128 of k) is 32 KiB a CTA and four
-// products.
+// What bounds it.  The tensor cores: a k-block of a pair is four products of
+// 256 x 256 x 32, 512 cycles, and 32 KiB of copies a CTA, 64 bytes a cycle.  Gated, 8
+// x 3584, k 8192, 4096 rows: 1049 us for a short while (3.67 PFLOP/s; tensor
+// pipes 83% active under the profiler at 1.68 GHz, 13.9 TB/s out of L2), 1220 to
+// 1250 in a long loop, where the GPU's power holds the clock at 1.4 GHz; n 8192, k 8
+// x 3584, 4096 rows scattered: 537 and 640 us.  With a quarter of the copies
+// left out (wrong results) the loops take 1179 and 563 us: what moves between L2
+// and the SMs costs both time and power.
 //
 // Tensor memory.  Two accumulators of 256 columns would fill it, and the scale
 // words need 24 columns: the accumulators lie at columns 0 and 224 and share
 // 32.  A tile's epilogue reads those first; then the next tile's products may
-// start, and the rest is read beside them.
+// start, and the rest is read beside them.  Between a tile's last product and the
+// next tile's first some 1500 cycles remain.
+//
+// Order.  Row tiles in groups whose activations stay in L2, the row tiles of a
+// column tile adjacent, so that pairs that run together share both operands.
 //
 // Roles: warp 0 copies tiles (TMA), warp 1 issues the pair's products (leader),
 // warps 2-5 are the epilogue, warps 6 and 7 gather scale words, alternating.

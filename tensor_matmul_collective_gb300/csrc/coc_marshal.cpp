@@ -1,4 +1,4 @@
-// Argument marshalling of the decode-step calls for Python, over the C ABI.
+// Argument marshalling of the decode-step and 8-bit calls for Python, over the C ABI.
 //
 // Those calls' kernels take a few microseconds, less than it takes an
 // interpreter to look at 8 ranks' tensors one attribute at a time (51 us for

@@ -85,7 +85,7 @@
  *     parts of a rank-split AllReduce / ReduceScatter, the MoE routing
  *     tables, the w8A16 pre-pass's dequantised weight, the stacked X of an
  *     AllGather that keeps no gathered copy, the parts of cached attention's
- *     split items) take it from a
+ *     split items, the stacked 8-bit shards of an AllGather) take it from a
  *     workspace the library keeps per stream: allocated by the first such
  *     call on the stream and grown only when a later call needs more (the
  *     growing call waits for the earlier users of the old buffer first), so
@@ -100,7 +100,8 @@
  *     stream has one workspace, which goes from thread to thread in stream
  *     order.  A stream with the handle of a destroyed one takes over its
  *     workspace in stream order; where the destroyed stream's last call was
- *     cached attention, the new one's first call waits for the device.
+ *     cached attention or an 8-bit AllGather that stacked its shards, the new
+ *     one's first call waits for the device.
  *     coc_matmul_all_reduce_noalloc takes none of this memory.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  Outputs must not alias inputs or each other.

@@ -146,7 +146,17 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     }
     if (splits > 1) cluster_arrive_relaxed();       // the cluster's barriers are there (waited for before they are used)
     grid_dependency_wait();
-    grid_dependents_launch();
+    // Tensor memory is asked for behind the wait, so that no kernel before this
+    // one finds it taken by a block that waits for that kernel; and later kernels
+    // may come only when this block has its own.
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+        tmem_relinquish();
+        tc_fence_before();
+        __syncwarp();
+        tc_fence_after();
+        grid_dependents_launch();
+    }
     bool ok = true;
     if (p.inject_timeout) ok = warp_wait(smem_u32(never), 0, ctl, 0x700u);
 
@@ -189,11 +199,6 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
                 if (filled & (1u << s)) drain_wait(smem_u32(&full[s]), (parity >> s) & 1u, kDrainNs);
         __syncwarp();
     } else if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
-        tmem_relinquish();
-        tc_fence_before();
-        __syncwarp();
-        tc_fence_after();
         const uint32_t tmem = *tmem_slot;
         const uint64_t tiles = make_sdesc(smem_u32(smem), 16, 1024);
         uint32_t stage = 0, phase = 0, onto = 0;
@@ -372,12 +377,12 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         }
     }
     if (splits > 1) {
-        if (*reinterpret_cast<volatile uint32_t*>(abort_word) != 0u) {      // copies that nobody waited for
+        cluster_wait();     // every block has its parts: none leaves while its sums are copied
+        if (*reinterpret_cast<volatile uint32_t*>(abort_word) != 0u) {      // copies to this block that it did not wait for
             const uint64_t t0 = globaltimer();
             while (globaltimer() - t0 < 200000ull) {
             }
         }
-        cluster_wait();     // every block has its parts: none leaves while its sums are copied
     }
     if (warp == 1) {
         tc_fence_after();
@@ -501,8 +506,8 @@ int f8_slab_kblocks(int64_t m, bool gated) {
 // block alone on an SM has all its shared memory for the ring.  More tiles
 // than SMs go unsplit, two blocks on an SM, which overlaps one's beginning and end
 // with the other's middle.  So do blocks of up to 8 k-blocks: the next launch's
-// set themselves up beside them (n 4096, k 4096, m 1 6.8 to 6.2 us).  Measured, ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1
-// 9.6 / 7.6 / 7.0 / 17.5 us; n 8192, k 8 x 3584, m 64 49 / 41 / 49 / 76 (shared 70 /
+// set themselves up beside them (n 4096, k 4096, m 1 6.8 to 6.2 us).  Measured,
+// ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1 9.6 / 7.6 / 7.0 / 17.5 us; n 8192, k 8 x 3584, m 64 49 / 41 / 49 / 76 (shared 70 /
 // 47 / 44 / 55); n 14336, k 8 x 7168, m 16 120 / 128 / 144 / 162 (shared 148 / 127 /
 // 132 / 151); n 1024, k 2 x 8192, m 16 27 / 17 / 12 / 9.0.  Gated, 8 x 3584, k 8192, m
 // 64: shared 84 unsplit, 92 in two, alone 88.

@@ -271,6 +271,34 @@ def test_a_chain_of_layers_without_waits():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_products_of_every_kind_in_a_row():
+    """16-bit, w8A16-like and 8-bit products one after another without waits: kernels that come early share SMs and
+    tensor memory with the ones before them."""
+    R, hidden = 2, 512
+    g = torch.Generator().manual_seed(6)
+    w16 = [(torch.randn(hidden, hidden, generator=g) * hidden ** -0.5).to(BF).to(DEV) for _ in range(R)]
+    mlps = [ds.random_mlp(R, hidden, f, seed=f) for f in (256, 1024)]
+    start = {n: rows(R, n, hidden, BF, n) for n in (8, 40, 264)}
+
+    def chain(x, wait):
+        for i in range(12):
+            x = coc.matmul_all_reduce(x, w16)
+            x = [t.clone() for t in x] if wait else x
+            n = x[0].shape[0]
+            for mlp in mlps:
+                x, _ = mlp([t[:n] for t in x])
+            x = coc.all_gather_matmul([t[:n // 8 * 8] for t in x], w16)
+            x = [t[:n].contiguous() for t in x]
+            if wait:
+                torch.cuda.synchronize()
+        return x
+    for n, x in start.items():
+        want = [t.clone() for t in chain(x, True)]
+        for _ in range(4):
+            assert all(torch.equal(a, b) for a, b in zip(chain(x, False), want))
+    coc.sync_status()
+
+
 @pytest.mark.parametrize("tile", ["0", "1"])
 def test_nothing_is_written_around_the_outputs(monkeypatch, tile):
     """Outputs in the middle of buffers whose other bytes stay as they were: ragged rows, columns and last blocks."""
@@ -297,10 +325,12 @@ def test_nothing_is_written_around_the_outputs(monkeypatch, tile):
     assert all(torch.equal(v, views[2][0]) for v in views[2])
 
 
-def test_bounded_wait_reports(monkeypatch):
-    """A wait that nothing ends runs out, the call's status says so, and the next call is right again (the test hook, no fault)."""
-    mlp = ds.random_mlp(1, 256, 256)
-    c, s = coc.quantize_f8(rows(1, 40, 256, BF, 1))
+@pytest.mark.parametrize("inner", [256, 4096])
+def test_bounded_wait_reports(monkeypatch, inner):
+    """A wait that nothing ends runs out, the call's status says so, and the next call is right again (the test hook, no
+    fault); the longer contraction is cut into ranges of a cluster."""
+    mlp = ds.random_mlp(1, 256, inner)
+    c, s = coc.quantize_f8(rows(1, 40, inner, BF, 1))
     want = coc.matmul_all_reduce_f8(c, s, mlp.w_down, mlp.down_scales)[0].clone()
     for tile in "01":
         monkeypatch.setenv("COC_F8_TILE", tile)

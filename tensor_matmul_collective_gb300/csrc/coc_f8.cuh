@@ -37,9 +37,14 @@ __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d
     return lo | (hi << 16);
 }
 
-// silu(g) u = g u / (1 + e^-g).  For g -> -inf the quotient goes to -0 as
-// e^-g overflows to infinity; NaN comes through.
-__device__ __forceinline__ float f8_gated(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+// silu(g) u = g u / (1 + e^-g), e^-g = 2^(-g log2 e).  Where 2^x overflows
+// (g < -88) the quotient is -0; NaN comes through.
+__device__ __forceinline__ float f8_gated(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r * u;
+}
 
 // ---- block-scaled products ----
 

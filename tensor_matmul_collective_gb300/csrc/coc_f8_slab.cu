@@ -118,26 +118,18 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     // The producer needs the barriers alone, and nobody but warp 1 tensor memory
     // before the end: loads are on their way while the rest is set up.
     if (warp == 0) {
-        if (lane == 0) {
-            for (uint32_t s = 0; s < S; ++s) {
-                mbar_init(smem_u32(&full[s]), 1);
-                mbar_init(smem_u32(&empty[s]), 1);
-            }
-            for (int s = 0; s < kSfStages; ++s) {
-                mbar_init(smem_u32(&sf_full[s]), 1);
-                mbar_init(smem_u32(&sf_empty[s]), 1);
-            }
-            mbar_init(smem_u32(done), 1);
-            mbar_init(smem_u32(idle), splits);
-            mbar_init(smem_u32(parts), 1);
-            mbar_init(smem_u32(never), 1);
-            *abort_word = 0u;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            fence_proxy_async_smem();
-            if (splits > 1) mbar_expect_tx(smem_u32(parts), (splits - 1) * WT * own * 512);
-        } else if (total > 0 && lane <= p.shards) {
-            prefetch_tmap(&p.tm_w[ag ? r : lane - 1]);
-            prefetch_tmap(&p.tm_x[ag ? 0 : lane - 1]);
+        // a lane a barrier (one lane for all took 700 cycles): they lie one after another
+        constexpr int kBars = 2 * kMaxStages + 2 * kSfStages + 4;
+        static_assert(kBars <= 32, "a lane a barrier");
+        if (lane < kBars) mbar_init(smem_u32(&bars[lane]), &bars[lane] == idle ? splits : 1);
+        if (lane == 0) *abort_word = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (splits > 1 && lane == 0) mbar_expect_tx(smem_u32(parts), (splits - 1) * WT * own * 512);
+        if (total > 0 && lane < p.shards) {
+            prefetch_tmap(&p.tm_w[ag ? r : lane]);
+            prefetch_tmap(&p.tm_x[ag ? 0 : lane]);
         }
         __syncwarp();
         named_arrive(1, kSlabThreads);
@@ -345,10 +337,13 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         }
         const bool in = o < own && col < p.n;
         if constexpr (GATED) {
+            // (all eight at once, whatever comes of them: with the test in front they took turns, 110 cycles each)
             float top = 0.f;
 #pragma unroll
+            for (int j = 0; j < 8; ++j) y[0][j] = f8_gated(y[0][j], y[1][j]);
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
-                y[0][j] = in ? f8_gated(y[0][j], y[1][j]) : 0.f;
+                y[0][j] = in ? y[0][j] : 0.f;
                 top = fmaxf(top, f8_magnitude(y[0][j]));
             }
 #pragma unroll

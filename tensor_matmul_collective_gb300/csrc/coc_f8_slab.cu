@@ -284,18 +284,26 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     float* sums = reinterpret_cast<float*>(smem);
     const uint32_t sums_at = smem_u32(sums), parts_at = sums_at + C::SUMS;
-    for (int c = 16 * (warp >> 2); c < WT * NT; c += 32) {
-        if (c % NT >= rows) continue;
-        uint32_t v[16];
-        if (b1 > b0) {
-            tmem_ld_16cols(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
-            tmem_wait_ld();
-        } else {
+    // two warps a quadrant of lanes, pieces of 16 columns in turns, two on their way at a time
+    for (int c = 16 * (warp >> 2); c < WT * NT; c += 64) {
+        uint32_t v[2][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0u;
+        for (int h = 0; h < 2; ++h) {
+            if (c + 32 * h >= WT * NT || (c + 32 * h) % NT >= rows) continue;
+            if (b1 > b0) {
+                tmem_ld_16cols(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c + 32 * h, v[h]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[h][i] = 0u;
+            }
         }
+        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+        for (int h = 0; h < 2; ++h) {
+            if (c + 32 * h >= WT * NT || (c + 32 * h) % NT >= rows) continue;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sums[(c + 32 * h + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[h][i]);
+        }
     }
     tc_fence_before();
     if (splits > 1) fence_proxy_async_smem();
@@ -304,14 +312,15 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         // every block's rows of this block's sums go to it in one piece a weight tile, behind its own sums in its idle ring:
         // parts[block][weight tile][own row][weight row].  (Read row by row from the others' shared memory between two
         // cluster barriers they took longer: n 4096, k 4096, m 64 8.9 us, with nothing exchanged 5.5.)
-        if (warp == 0) {
+        // (a warp a block: one warp's lanes took 100 cycles a copy)
+        if (warp < splits && warp != split) {
             const bool go = warp_wait<true>(smem_u32(idle), 0, ctl, 0x770u);
-            const int theirs = min(own_rows, rows - lane * own_rows);
-            if (go && lane < splits && lane != split && theirs > 0) {
-                const uint32_t bar = map_to_rank(smem_u32(parts), lane);
+            const int theirs = min(own_rows, rows - warp * own_rows);
+            if (go && lane == 0 && theirs > 0) {
+                const uint32_t bar = map_to_rank(smem_u32(parts), warp);
 #pragma unroll
                 for (int w = 0; w < WT; ++w)
-                    bulk_copy_s2s_signal(map_to_rank(parts_at + (split * WT + w) * own_rows * 512, lane), sums_at + (w * NT + lane * own_rows) * 512,
+                    bulk_copy_s2s_signal(map_to_rank(parts_at + (split * WT + w) * own_rows * 512, warp), sums_at + (w * NT + warp * own_rows) * 512,
                                          theirs * 512, bar);
             }
             __syncwarp();

@@ -196,6 +196,26 @@ def test_shards_apart_on_two_streams_and_in_threads():
     assert not bad
 
 
+def test_no_allocation_after_the_first_calls():
+    """The library's own memory: stacked shards take the stream's workspace, everything else none."""
+    R, n, hidden = 4, 10, 512
+    mlp = ds.random_mlp(R, hidden, 1024)
+    w, ws = zip(*[coc.f8_pack(torch.randn(264, hidden, device=DEV)) for _ in range(R)])
+    xs = rows(R, n, hidden, BF, 1)
+
+    def calls():
+        mlp(xs, xs)
+        c, s = coc.quantize_f8(xs)
+        coc.all_gather_matmul_f8([t.clone() for t in c], [t.clone() for t in s], list(w), list(ws))
+    calls()
+    torch.cuda.synchronize()
+    before = coc.alloc_count()
+    for _ in range(5):
+        calls()
+    coc.sync_status()
+    assert coc.alloc_count() == before
+
+
 def test_block_on_a_given_stream():
     mlp = ds.random_mlp(2, 512, 1024)
     xs, rs = rows(2, 9, 512, BF, 1), rows(2, 9, 512, BF, 2)

@@ -10,7 +10,7 @@
 // residual and sum, 3 without.  A row stays in registers between the sum of
 // squares and the scaling, so HBM is the bound: 8 x 1024 rows of 8192 with
 // residual take 70 us, 6.7 TB/s (a copy: 6.8); quantised alone, 2 x 4095 rows of
-// 3584 16.4 us, 5.4 TB/s (instructions: 100 for 24 bytes a lane); one row 2.8 us,
+// 3584 15.1 us, 5.8 TB/s (instructions: 100 for 24 bytes a lane); one row 2.8 us,
 // the launch and one chain of load, sum and store.
 //
 // Layout.  16 lanes hold a block of 128 (8 values, 16 bytes each), so its
@@ -32,23 +32,37 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     }
 }
 
-// The 16 lanes' block: its scale byte, and this lane's 8 codes.  Infinities do
-// not count, but are seldom there to be taken out.
-__device__ __forceinline__ uint32_t block_codes(const float (&y)[8], uint2& codes) {
-    float top = 0.f;
+// N blocks of the 16 lanes: their scale bytes, and this lane's 8 codes of each.
+// Infinities do not count, but are seldom there to be taken out: one test for
+// all blocks, so that their shuffles go side by side.
+template <int N>
+__device__ __forceinline__ void block_codes(const float (&y)[N][8], uint32_t (&byte)[N], uint2 (&codes)[N]) {
+    float top[N], most = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
-    if (__any_sync(0xffffffffu, top > kF8Largest)) {
-        top = 0.f;
+    for (int i = 0; i < N; ++i) {
+        top[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, f8_magnitude(y[j]));
+        for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], fabsf(y[i][j]));
+        most = fmaxf(most, top[i]);
+    }
+    if (__any_sync(0xffffffffu, most > kF8Largest)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            top[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], f8_magnitude(y[i][j]));
+        }
     }
 #pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const uint32_t byte = f8_scale_byte(top);
-    const float f = f8_inverse(byte);
-    codes = make_uint2(f8_codes4(y[0], y[1], y[2], y[3], f), f8_codes4(y[4], y[5], y[6], y[7], f));
-    return byte;
+    for (int d = 8; d >= 1; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        byte[i] = f8_scale_byte(top[i]);
+        const float f = f8_inverse(byte[i]);
+        codes[i] = make_uint2(f8_codes4(y[i][0], y[i][1], y[i][2], y[i][3], f), f8_codes4(y[i][4], y[i][5], y[i][6], y[i][7], f));
+    }
 }
 
 // Half a warp a block of 128, kBlocksEach blocks of it in flight.
@@ -74,17 +88,18 @@ __global__ void __launch_bounds__(kQuantThreads) f8_quantize_kernel(const __grid
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (at[i] >= 0) v[i] = load_uint4(a.x[r] + at[i]);
     }
+    float y[kBlocksEach][8];
+    uint32_t byte[kBlocksEach];
+    uint2 codes[kBlocksEach];
 #pragma unroll
-    for (int i = 0; i < kBlocksEach; ++i) {
-        float y[8];
-        unpack8<BF16>(v[i], y);
-        uint2 codes;
-        const uint32_t byte = block_codes(y, codes);
+    for (int i = 0; i < kBlocksEach; ++i) unpack8<BF16>(v[i], y[i]);
+    block_codes(y, byte, codes);
+#pragma unroll
+    for (int i = 0; i < kBlocksEach; ++i)
         if (at[i] >= 0) {
-            *reinterpret_cast<uint2*>(a.codes[r] + at[i]) = codes;
-            if (lane16 == 0) a.scale[r][first + i * (kQuantThreads / 16)] = static_cast<uint8_t>(byte);
+            *reinterpret_cast<uint2*>(a.codes[r] + at[i]) = codes[i];
+            if (lane16 == 0) a.scale[r][first + i * (kQuantThreads / 16)] = static_cast<uint8_t>(byte[i]);
         }
-    }
 }
 
 // blockDim.x threads a row (a multiple of 32), blockDim.y rows a block; VPT
@@ -185,20 +200,22 @@ __global__ void __launch_bounds__(norm_threads(VPT), VPT == 4 ? 2 : 1) f8_norm_k
     const float eps = f == 1.f ? a.eps : a.eps * kDown * kDown;
     const float inv = rsqrtf(q / static_cast<float>(a.hidden) + eps);
 
+    // (piece after piece: two or four side by side cost registers, 8 x 1024 rows of 8192 70.7 and 71.8 us instead of 70.2)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int p = t + i * T;
-        float w[8], y[8];
         const bool in = live && p < pieces;
+        float w[8], y[1][8];
         if constexpr (kAhead) unpack8<BF16>(wv[i], w);
         else unpack8<BF16>(in ? load_uint4(a.weight + 8 * p) : make_uint4(0u, 0u, 0u, 0u), w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = in ? s[i][j] * f * inv * w[j] : 0.f;
-        uint2 codes;
-        const uint32_t byte = block_codes(y, codes);
+        for (int j = 0; j < 8; ++j) y[0][j] = in ? s[i][j] * f * inv * w[j] : 0.f;
+        uint32_t byte[1];
+        uint2 codes[1];
+        block_codes(y, byte, codes);
         if (in) {
-            *reinterpret_cast<uint2*>(a.codes[r] + base + 8 * p) = codes;
-            if ((t & 15) == 0) a.scale[r][row * ((pieces + 15) / 16) + p / 16] = static_cast<uint8_t>(byte);
+            *reinterpret_cast<uint2*>(a.codes[r] + base + 8 * p) = codes[0];
+            if ((t & 15) == 0) a.scale[r][row * ((pieces + 15) / 16) + p / 16] = static_cast<uint8_t>(byte[0]);
         }
     }
 }

@@ -319,20 +319,30 @@ struct Lists {
 int64_t f8_blocks(int64_t n) { return (n + 127) / 128; }
 
 // Codes (rows x cols) and scales of R ranks, given or new; both new ones are
-// one allocation, all ranks' codes and then all ranks' scales.
-bool code_outputs(PyObject* codes, PyObject* scales, int64_t R, int64_t rows, int64_t cols, const at::Device& dev, coc_stream_t stream, Lists& o) {
-    if (codes != Py_None || scales != Py_None)
+// one allocation, all ranks' codes and then all ranks' scales.  With `sums`
+// (not null: an output of the 16-bit type beside them, None where it is new) small new ones
+// of all three are one allocation; larger sums have their own, which does not
+// keep the codes' memory for as long as a residual lives.
+bool code_outputs(PyObject* codes, PyObject* scales, PyObject* sums, at::ScalarType dt, int64_t R, int64_t rows, int64_t cols,
+                  const at::Device& dev, coc_stream_t stream, Lists& o) {
+    constexpr int64_t kSmall = 1 << 20;
+    const int64_t n = R * rows * cols, scale_n = R * rows * f8_blocks(cols);
+    const bool fresh_codes = codes == Py_None && scales == Py_None;
+    const bool joint = sums == Py_None && fresh_codes && 3 * n + scale_n <= kSmall;
+    if (sums != nullptr && !joint && !outputs(sums, R, {rows, cols}, dt, dev, stream, &o.l[2], o.p[2])) return false;
+    if (!fresh_codes)
         return outputs(codes, R, {rows, cols}, at::kFloat8_e4m3fn, dev, stream, &o.l[0], o.p[0]) &&
                outputs(scales, R, {rows, f8_blocks(cols)}, at::kFloat8_e8m0fnu, dev, stream, &o.l[1], o.p[1]);
     const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream();
     const bool other = reinterpret_cast<cudaStream_t>(stream) != now.stream();
     c10::cuda::OptionalCUDAStreamGuard on;
     if (other) on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), dev.index()));
-    const int64_t code_bytes = R * rows * cols;
-    const at::Tensor all = fresh({code_bytes + R * rows * f8_blocks(cols)}, at::kByte);
+    const int64_t first = joint ? 2 * n : 0;        // codes behind the sums: whole 16 bytes where rows of codes are
+    const at::Tensor all = fresh({first + n + scale_n}, at::kByte);
     if (other) all.record_stream(now);
-    return parts(all, R, {rows, cols}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e4m3fn), 0, &o.l[0], o.p[0]) &&
-           parts(all, R, {rows, f8_blocks(cols)}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e8m0fnu), code_bytes, &o.l[1], o.p[1]);
+    return (!joint || parts(all, R, {rows, cols}, caffe2::TypeMeta::fromScalarType(dt), 0, &o.l[2], o.p[2])) &&
+           parts(all, R, {rows, cols}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e4m3fn), first, &o.l[0], o.p[0]) &&
+           parts(all, R, {rows, f8_blocks(cols)}, caffe2::TypeMeta::fromScalarType(at::kFloat8_e8m0fnu), first + n, &o.l[1], o.p[1]);
 }
 
 // (entry point, xs, outs, scales, stream) -> (status, codes, scales)
@@ -351,7 +361,7 @@ PyObject* quantize_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     coc_stream_t stream;
     if (!stream_of(a[4], &stream)) return nullptr;
     Lists o;
-    if (!code_outputs(a[2], a[3], R, rows, h, dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
+    if (!code_outputs(a[2], a[3], nullptr, at::kByte, R, rows, h, dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(R), rows, h, x.p, o.p[0], o.p[1], code_of(*x0), stream);
@@ -383,8 +393,7 @@ PyObject* norm_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     coc_stream_t stream;
     if (!stream_of(a[8], &stream)) return nullptr;
     Lists o;
-    if (!code_outputs(a[5], a[6], R, rows, h, dev, stream, o) || (add && !outputs(a[7], R, {rows, h}, dt, dev, stream, &o.l[2], o.p[2])))
-        return PyErr_Occurred() ? nullptr : none();
+    if (!code_outputs(a[5], a[6], add ? a[7] : nullptr, dt, R, rows, h, dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(R), rows, h, x.p, add ? res.p : nullptr, w->data_ptr(), static_cast<float>(eps), add ? o.p[2] : nullptr, o.p[0],
@@ -457,7 +466,7 @@ PyObject* gated_f8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!stream_of(a[7], &stream)) return nullptr;
     Lists o;
     const int64_t m = in.R * in.rows;
-    if (!code_outputs(a[5], a[6], in.R, m, in.n, *in.dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
+    if (!code_outputs(a[5], a[6], nullptr, at::kByte, in.R, m, in.n, *in.dev, stream, o)) return PyErr_Occurred() ? nullptr : none();
     coc_status_t st;
     Py_BEGIN_ALLOW_THREADS
     st = fn(static_cast<int>(in.R), in.rows, in.n, in.k, in.x.p, in.xs.p, in.w.p, in.ws.p, o.p[0], o.p[1], stream);

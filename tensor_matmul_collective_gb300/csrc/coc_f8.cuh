@@ -115,6 +115,22 @@ __device__ __forceinline__ void tma_load_3d_f8(uint32_t dst, const CUtensorMap* 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
         : "memory");
 }
+// The box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d_f8(const CUtensorMap* map, int c0, int c1) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d_f8(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 // Arrival at a barrier of the cluster that hands nothing over in memory: a
 // release at the cluster's scope waits for all that the thread has stored (1600
 // cycles of an epilogue).

@@ -38,6 +38,12 @@ namespace {
 constexpr int kWTile = 128 * 128;       // bytes of 128 weight rows' k-block
 constexpr int kSlabThreads = 256;
 constexpr int kMaxStages = 8;
+// Weights that all blocks together ask L2 for ahead of their turn, where there
+// are 40 MiB of them and one row tile: calls that follow each other, n 8192, k 8 x
+// 3584, m 64 39.4 to 37.6 us, gated 8 x 3584, k 8192, m 64 77.1 to 74.9, 11008, k 4096,
+// m 1 18.1 to 17.1 (16 MiB: 38.0, 75.7, 17.2; 64: 40.0, 76.9, 18.5); with less, n
+// 8192, k 4096, m 16 8.2 to 8.9.
+constexpr long long kAheadBytes = 32LL << 20;
 constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight, in shared and in tensor memory
 constexpr int kSfCols = 16;             // columns of a run's scale words in tensor memory
 
@@ -137,6 +143,28 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         named_sync(1, kSlabThreads);
     }
     if (splits > 1) cluster_arrive_relaxed();       // the cluster's barriers are there (waited for before they are used)
+    if (warp == 4) {
+        // Weights on their way into L2 while the kernel before this one ends.  L2 is
+        // where all writes meet: should that kernel write them, the loads behind the
+        // wait find what it wrote.
+        int left = p.ahead;
+        for (int i = b0; i < b1 && left > 0; ++i) {
+            const F8Run run = f8_run(i, per_shard, p.kblocks);
+            const CUtensorMap* wm = &p.tm_w[ag ? r : run.shard];
+            for (int j = 0; j < run.count && left > 0; j += KPS, left -= KPS) {
+                if (KPS == 2 && p.maps_3d) {
+                    tma_prefetch_3d_f8(wm, 0, nt * 128, run.kb + j);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < KPS; ++q) {
+                        if (j + q >= run.count) break;
+                        tma_prefetch_2d_f8(wm, (run.kb + j + q) * 128, nt * 128);
+                        if constexpr (GATED) tma_prefetch_2d_f8(wm, (run.kb + j + q) * 128, p.n + nt * 128);
+                    }
+                }
+            }
+        }
+    }
     grid_dependency_wait();
     // Tensor memory is asked for behind the wait, so that no kernel before this
     // one finds it taken by a block that waits for that kernel; and later kernels
@@ -439,6 +467,9 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     const bool alone = fit && (C::SHARED == 0 || C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
     a.stages = alone ? C::ALONE : C::SHARED;
     if (a.splits > 1 && a.stages * C::STAGE < C::SUMS + C::PARTS) return cudaErrorInvalidConfiguration;    // (never: see SlabCfg)
+    const long long blocks = static_cast<long long>(a.n_tiles) * (a.op == OP_AG ? a.R : 1) * a.shards * a.kblocks;      // of weights
+    const long long ahead = kAheadBytes / (C::WT * kWTile);
+    a.ahead = pdl_launch() && a.m_tiles == 1 && 4 * blocks >= 5 * ahead ? static_cast<int>(ahead / (tiles * a.splits)) : 0;
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * a.splits), 1, 1);
     cfg.dynamicSmemBytes = C::REST + a.stages * C::STAGE;
     attr[0].val.clusterDim.x = static_cast<unsigned>(a.splits);

@@ -286,7 +286,7 @@ struct F8Args {
     int maps_3d;                              // slabs of a k that is whole blocks
     int scale_words;                          // kblocks % 4 == 0 and all scales 4-byte aligned: read as words
     int inject_timeout;
-    int m_tiles, splits, stages, group_mt;    // set by the launch
+    int m_tiles, splits, stages, ahead, group_mt;     // set by the launch
 };
 // Which kernel takes m rows (sizes as in F8Args): tiles of CTA pairs, or slabs
 // of weight rows; and the rows of their X maps' boxes (tiles: 128).

@@ -8,11 +8,11 @@
 // which is one tile.
 //
 // What bounds it.  n k bytes of weights, read once: n 8192, k 8 x 3584, 64 rows
-// on 8 ranks take 39 to 41 us, 6.0 to 6.3 TB/s with the outputs; gated 8 x 3584, k
-// 8192, 64 rows 76 to 80 us, 6.1 TB/s; gated 11008, k 4096, one row 18.5 us, 4.9
-// TB/s; n 4096, k 4096, one row 5.5 to 5.9 us, of which the weights' bytes are 2.5.  A
-// tile is 128 weight rows by NT activation rows, so few rows cost the tensor cores
-// little (a product of 32 of k takes 40 cycles with 16 rows, 65 with 128).
+// on 8 ranks take 38 us, 6.4 TB/s with the outputs; gated 8 x 3584, k 8192, 64 rows
+// 75 to 77 us, 6.2 TB/s; gated 11008, k 4096, one row 17.1 to 17.6 us, 5.2 TB/s; n
+// 4096, k 4096, one row 5.5 us, of which the weights' bytes are 2.5.  A tile is 128
+// weight rows by NT activation rows, so few rows cost the tensor cores little (a
+// product of 32 of k takes 40 cycles with 16 rows, 65 with 128).
 //
 // Stages.  A k-block is 128 of k, one 128-byte swizzled row; two of them come
 // in one box where the ring has room (a block's SM took 600 cycles a k-block

@@ -849,7 +849,7 @@ def quantize_f8(xs, outs=None, scales=None, stream=None):
     xs[r]: rows x hidden (fp16/bf16), hidden a multiple of 16; codes[r]: rows x
     hidden float8_e4m3fn, scales[r]: rows x ceil(hidden/128) float8_e8m0fnu,
     the least power of two that keeps 128 values within e4m3 (at least 2**-100).
-    New ones are parts of one allocation."""
+    New ones are parts of common allocations."""
     native = _native or _marshal()
     if native:
         done = native[0].quantize_f8(native[4], xs, outs, scales, None if stream is None else _stream(stream))
@@ -872,7 +872,7 @@ def add_rms_norm_f8(xs, weight, residuals=None, eps: float = 1e-6, outs=None, sc
     rounded to the type of xs (None without residuals; residuals[r] itself may
     be given as sums[r]); codes[r], scales[r] = s / sqrt(mean(s**2) + eps) * weight
     as quantize_f8 gives them.  weight: hidden values in the type of xs, the
-    same for every rank; hidden up to 65536."""
+    same for every rank; hidden up to 65536.  New outputs are parts of common allocations."""
     native = _native or _marshal()
     if native:
         done = native[0].norm_f8(native[5], xs, weight, residuals, eps, outs, scales, sums, None if stream is None else _stream(stream))

@@ -122,6 +122,21 @@ def test_norm_in_place_and_given_outputs():
         assert u2[r] is rs[r] and c2[r] is outs[r] and not torch.equal(rs[r], keep[r])
         assert torch.equal(rs[r], sums[r])
         assert torch.equal(outs[r].view(torch.uint8), codes[r].view(torch.uint8)) and torch.equal(ss[r].view(torch.uint8), scales[r].view(torch.uint8))
+    # the sum over x itself
+    c3, s3, u3 = coc.add_rms_norm_f8(xs, w, residuals=keep, sums=xs)
+    for r in range(R):
+        assert u3[r] is xs[r] and torch.equal(xs[r], sums[r])
+        assert torch.equal(c3[r].view(torch.uint8), codes[r].view(torch.uint8)) and torch.equal(s3[r].view(torch.uint8), scales[r].view(torch.uint8))
+
+
+@pytest.mark.parametrize("R,n,h", [(1, 1, 4096), (8, 3, 144), (2, 700, 4096)])
+def test_new_outputs_do_not_overlap(R, n, h):
+    """Small new outputs are one allocation, large sums their own: codes, scales and sums of all ranks lie apart."""
+    xs, rs = [t.to(DEV) for t in rows(R, n, h, BF, 1)], [t.to(DEV) for t in rows(R, n, h, BF, 2)]
+    outs = coc.add_rms_norm_f8(xs, torch.ones(h, dtype=BF, device=DEV), residuals=rs)
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for ts in outs for t in ts)
+    assert len(spans) == 3 * R and all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+    assert all(t.data_ptr() % 16 == 0 for ts in (outs[0], outs[2]) for t in ts)
 
 
 def test_rows_empty():

@@ -1,5 +1,8 @@
 """The feed-forward block from the 8-bit operators, each stage against 64 bits from what the stage before it left; the
 block in captured graphs, on other streams and in threads; and the binding of its operators."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -270,6 +273,54 @@ def test_two_graphs_of_the_block(n):
         coc.sync_status()
         for (graph, xs, rs, run, outs, sums, ag, stream), want in zip(graphs, wants):
             assert all(torch.equal(a, b) for a, b in zip([*outs, *sums, *ag], want))
+
+
+FIRST_USE = """
+import torch
+from tensor_matmul_collective_gb300 import coc, decode_step as ds
+coc.quantize_f8([torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda")])      # the device's state
+mlp = ds.random_mlp(2, 256, 512)
+for n in (1, 40, 300):
+    xs = [torch.randn(n, 256, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs, sums = mlp(xs, residuals=xs)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in outs]
+    want, _ = mlp(xs, residuals=xs)
+    coc.sync_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)), n
+print("same")
+"""
+
+
+def test_kernels_used_first_in_a_capture():
+    """Sizes whose kernels no eager call has run yet are captured, in a process of their own."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=root, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0 and "same" in done.stdout, done.stdout + done.stderr
+
+
+@pytest.mark.parametrize("tile", ["0", "1"])
+def test_scales_at_odd_addresses(monkeypatch, tile):
+    """Scales have no alignment: the same values 0 to 3 bytes into a buffer, rows of whole words."""
+    monkeypatch.setenv("COC_F8_TILE", tile)
+    n, k, cols = 70, 1024, 264
+    c, s = coc.quantize_f8(rows(1, n, k, BF, 1))
+    w, ws = coc.f8_pack(torch.randn(cols, k, device=DEV) * 0.03)
+    want = coc.matmul_all_reduce_f8(c, s, [w], [ws])[0]
+
+    def moved(t, by):
+        buf = torch.zeros(t.numel() + 8, dtype=torch.uint8, device=DEV)
+        new = buf[by:by + t.numel()].view(f8.E8M0).view(t.shape)
+        new.view(torch.uint8).copy_(t.view(torch.uint8))
+        assert new.data_ptr() % 4 == by % 4
+        return new
+    for by in range(4):
+        assert torch.equal(coc.matmul_all_reduce_f8(c, [moved(s[0], by)], [w], [ws])[0], want)
+        assert torch.equal(coc.matmul_all_reduce_f8(c, s, [w], [moved(ws, by)])[0], want)
 
 
 def test_a_chain_of_layers_without_waits():

@@ -512,7 +512,8 @@ bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, in
     if (m <= slab_m) return false;
     const int64_t ranks = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R), n_tiles = (n + 127) / 128;
     const int64_t units = (m + 255) / 256 * (gated ? n_tiles : (n_tiles + 1) / 2) * ranks, slabs = (m + slab_m - 1) / slab_m * n_tiles * ranks;
-    const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>(8, sm_count / slabs));
+    const int64_t runs = ((k + 127) / 128 + 3) / 4 * (op == OP_AG ? 1 : R);
+    const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>({8, sm_count / slabs, runs}));
     const int64_t rounds = slabs <= sm_count ? 1 : (slabs + 2 * sm_count - 1) / (2 * sm_count);
     // rows that start between L2's sectors (16 bytes) or lines are fetched in more of them
     const double tile_rows = k % 32 ? 1.25 : k % 128 ? 1.03 : 1.0, slab_rows = k % 32 ? 1.6 : k % 128 ? 1.1 : 1.0;

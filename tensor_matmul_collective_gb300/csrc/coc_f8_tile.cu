@@ -285,6 +285,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                 }
                 __syncwarp();
             } else {
+                // where this lane's 8 rows lie in their rank's output (AllReduce: in rank 0's), once for the tile
+                uint16_t* at[8];
+                const int col0 = nt * 256 + piece * 8;
+                if (p.op == OP_RS) {
+                    int o = min(row0, p.m - 1) / p.rows_per_rank, begin = o * p.rows_per_rank;      // a rank and its first row
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = row0 + (lane >> 3) + 4 * i;
+                        while (row < p.m && row - begin >= p.rows_per_rank) {
+                            begin += p.rows_per_rank;
+                            ++o;
+                        }
+                        at[i] = row < p.m ? static_cast<uint16_t*>(p.out[o]) + static_cast<long long>(row - begin) * p.n + col0 : nullptr;
+                    }
+                } else {
+                    uint16_t* out = static_cast<uint16_t*>(p.out[ag ? r : 0]) + col0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = row0 + (lane >> 3) + 4 * i;
+                        at[i] = row < p.m ? out + static_cast<long long>(row) * p.n : nullptr;
+                    }
+                }
+                const int copies = p.op == OP_AR ? p.R : 1;
                 for (int s = 0; s < 4; ++s) {
                     const int sub = buf ? s : 3 - s;
                     uint32_t va[32], vb[32];
@@ -292,7 +315,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                     load(acc + 64 * sub + 32, vb);
                     tmem_wait_ld();
                     if (s == 0) release();
-                    const int col = nt * 256 + 64 * sub + piece * 8;
                     if (row0 >= p.m || nt * 256 + 64 * sub >= p.n) continue;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -307,25 +329,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                         const int rr = (lane >> 3) + 4 * i;
                         v[i] = *reinterpret_cast<const uint4*>(stage_buf + rr * 128 + ((piece ^ (rr & 7)) << 4));
                     }
-                    if (col < p.n) {
-                        if (p.op == OP_RS) {
+                    if (col0 + 64 * sub < p.n) {
+                        for (int c = 0; c < copies; ++c) {
+                            const long long to = reinterpret_cast<intptr_t>(p.out[c]) - reinterpret_cast<intptr_t>(p.out[0]);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int row = row0 + (lane >> 3) + 4 * i;
-                                if (row >= p.m) continue;
-                                const int o = row / p.rows_per_rank;
-                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[o]) + static_cast<long long>(row - o * p.rows_per_rank) * p.n + col) = v[i];
-                            }
-                        } else {
-                            const int o0 = ag ? r : 0, o1 = ag ? r + 1 : p.R;
-                            for (int o = o0; o < o1; ++o) {
-                                uint16_t* out = static_cast<uint16_t*>(p.out[o]) + col;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int row = row0 + (lane >> 3) + 4 * i;
-                                    if (row < p.m) *reinterpret_cast<uint4*>(out + static_cast<long long>(row) * p.n) = v[i];
-                                }
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (at[i] != nullptr)
+                                    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at[i] + 64 * sub) + (copies > 1 ? to : 0)) = v[i];
                         }
                     }
                     __syncwarp();

@@ -37,13 +37,17 @@ __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d
     return lo | (hi << 16);
 }
 
-// silu(g) u = g u / (1 + e^-g), e^-g = 2^(-g log2 e).  Where 2^x overflows
-// (g < -88) the quotient is -0; NaN comes through.
+// silu(g) u = g u / (1 + e^-g), e^-g = 2^(-g log2 e).  From g = -87 on e^-g or
+// its reciprocal would leave fp32's range, but g e^g u need not, u may be large: below
+// -69 numerator and denominator are taken 2^-120 times (above, the same factor
+// is 1, which changes no bit).  From g = -170 on the quotient is -0, where |h| is below
+// 2^-110, half of the least code, whatever u; NaN comes through.
 __device__ __forceinline__ float f8_gated(float g, float u) {
+    const float s = g < -69.f ? 0x1p-120f : 1.f;
     float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return g * r * u;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.4426950408889634f, g < -69.f ? -120.f : 0.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s + e));
+    return g * r * (u * s);
 }
 
 // ---- block-scaled products ----

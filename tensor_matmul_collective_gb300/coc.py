@@ -993,6 +993,7 @@ def f8_pack(w, parts: int = 1):
     parts: equal groups of rows (gate and up: 2) whose blocks of 128 rows begin anew."""
     if w.dim() != 2 or parts < 1 or w.shape[0] % parts:
         raise ValueError("w must be n x k, n a multiple of parts")
+    w = w.detach()                              # (a parameter's codes would keep its graph, and every temporary with it)
     n, k = w.shape[0] // parts, w.shape[1]
     codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
     scales = torch.empty((parts * _blocks(n), _blocks(k)), dtype=torch.uint8, device=w.device)

@@ -997,7 +997,7 @@ def f8_pack(w, parts: int = 1):
     n, k = w.shape[0] // parts, w.shape[1]
     codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
     scales = torch.empty((parts * _blocks(n), _blocks(k)), dtype=torch.uint8, device=w.device)
-    for p in range(parts):
+    for p in range(parts if k else 0):
         for b in range(_blocks(n)):
             rows = slice(p * n + b * F8_BLOCK, p * n + min(n, (b + 1) * F8_BLOCK))
             t = torch.nn.functional.pad(w[rows].float(), (0, _blocks(k) * F8_BLOCK - k)).view(-1, _blocks(k), F8_BLOCK)

@@ -11,3 +11,11 @@ def test_pack_of_a_parameter_keeps_no_graph():
     plain, plain_scales = coc.f8_pack(w.detach())
     assert torch.equal(codes.view(torch.uint8), plain.view(torch.uint8)) and torch.equal(scales.view(torch.uint8), plain_scales.view(torch.uint8))
     assert w.requires_grad and w.grad is None
+
+
+def test_pack_of_an_empty_inner_size():
+    """What the products take at k = 0, and no rows."""
+    for n, k, parts in ((24, 0, 1), (2 * 144, 0, 2), (0, 256, 1), (0, 0, 1)):
+        codes, scales = coc.f8_pack(torch.zeros(n, k), parts)
+        assert codes.shape == (n, k) and codes.dtype == torch.float8_e4m3fn
+        assert scales.shape == (parts * -(-n // parts // 128), -(-k // 128)) and scales.dtype == torch.float8_e8m0fnu

@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcoc.so")
 SOURCES = ["coc_api.cu", "coc_kernel.cu", "coc_slab.cu", "coc_w8_ts.cu", "coc_noalloc.cu", "coc_w8_prepass.cu", "coc_moe.cu",
            "coc_kv_append.cu", "coc_kv_attention.cu", "coc_w4.cu", "coc_f8_rows.cu", "coc_f8_slab.cu", "coc_f8_tile.cu"]
-HEADERS = ["coc_internal.h", "coc_dequant.cuh", "coc_ptx.cuh", "coc_kv.cuh", "coc_kv_units.h", "coc_f8.cuh", os.path.join("..", "..", "include", "coc.h")]
+HEADERS = ["coc_internal.h", "coc_dequant.cuh", "coc_ptx.cuh", "coc_kv.cuh", "coc_kv_units.h", "coc_f8.cuh", "coc_f8_plan.h", os.path.join("..", "..", "include", "coc.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]

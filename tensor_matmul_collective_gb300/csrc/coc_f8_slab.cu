@@ -27,10 +27,10 @@
 // memory, warps 2 and 3 gather scale words, alternating; then all eight warps
 // read the accumulators.
 #include <algorithm>
-#include <atomic>
 #include <cstdlib>
 
 #include "coc_f8.cuh"
+#include "coc_f8_plan.h"
 
 namespace coc {
 namespace {
@@ -426,7 +426,7 @@ template <int NT, bool GATED, bool BF16>
 cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     using C = SlabCfg<NT, GATED>;
     auto kern = f8_slab_kernel<NT, GATED, BF16>;
-    static std::atomic<int> known[64][9];   // clusters of k that run at once, a block on an SM each; 0: not asked yet
+    static KnownCount known[64][9];         // clusters of k that run at once, a block on an SM each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -441,7 +441,7 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     cfg.numAttrs = 1;
     // k == 1 raises the kernel's shared memory limit, once a device
     auto clusters = [&](int k, int* n) -> cudaError_t {
-        if (dev >= 0 && dev < 64 && (*n = known[dev][k].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+        if (dev >= 0 && dev < 64 && known[dev][k].get(n)) return cudaSuccess;
         cfg.dynamicSmemBytes = C::REST + C::ALONE * C::STAGE;
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(cfg.dynamicSmemBytes));
         if (err != cudaSuccess) return err;
@@ -451,7 +451,7 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
             attr[0].val.clusterDim.x = static_cast<unsigned>(k);
             if ((err = cudaOccupancyMaxActiveClusters(n, kern, &cfg)) != cudaSuccess) return err;
         }
-        if (dev >= 0 && dev < 64) known[dev][k].store(std::max(*n, 1), std::memory_order_release);
+        if (dev >= 0 && dev < 64) known[dev][k].set(*n);
         return cudaSuccess;
     };
     const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles * (a.op == OP_AG ? a.R : 1);
@@ -459,11 +459,7 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     int room = 0;
     if ((e = clusters(1, &room)) != cudaSuccess) return e;
     const bool fit = C::SHARED == 0 || tiles <= room;
-    a.splits = 1;
-    for (int k = 2; k <= 8 && k <= total && tiles * k <= sm_count; ++k) {
-        if ((e = clusters(k, &room)) != cudaSuccess) return e;
-        if (tiles <= room) a.splits = k;
-    }
+    if ((e = f8_ranges(tiles, total, sm_count, clusters, &a.splits)) != cudaSuccess) return e;
     const bool alone = fit && (C::SHARED == 0 || C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
     a.stages = alone ? C::ALONE : C::SHARED;
     if (a.splits > 1 && a.stages * C::STAGE < C::SUMS + C::PARTS) return cudaErrorInvalidConfiguration;    // (never: see SlabCfg)

@@ -58,13 +58,15 @@ struct SlabCfg {
     static constexpr int SUMS = WT * NT * 128 * 4;
     static constexpr int COLS = WT * NT + kSfStages * kSfCols;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    // stages of a ring that has an SM to itself, and of one that shares it with another block's (0: cannot)
+    // stages of a ring that has an SM to itself, and of one that shares it with another block's
     static constexpr int ALONE = (224 * 1024 - REST) / STAGE;
-    static constexpr int HALF = (112 * 1024 - REST) / STAGE;
-    static constexpr int SHARED = HALF >= 2 && TMEM <= 256 && SUMS <= HALF * STAGE ? HALF : 0;
+    static constexpr int SHARED = (112 * 1024 - REST) / STAGE;
     static constexpr int PARTS = WT * (NT + 7) * 512;           // the cluster's sums of a block's rows, rounded up for each block
     static_assert(ALONE >= 2 && ALONE <= kMaxStages && SUMS + PARTS <= ALONE * STAGE && ALONE * STAGE + REST <= kSlabSmemCap, "shared memory");
-    static_assert(SHARED == 0 || KPS == 1 || SUMS + PARTS <= SHARED * STAGE, "shared memory (split blocks that share an SM)");
+    static_assert(SHARED >= 2 && TMEM <= 256 && SUMS <= SHARED * STAGE, "shared memory, tensor memory (blocks that share an SM)");
+    // Blocks of a cluster share an SM only where a stage has two k-blocks (launch_t).
+    static_assert(KPS == 1 || SUMS + PARTS <= SHARED * STAGE, "shared memory (blocks of a cluster that share an SM)");
+    static_assert(KPS == 1 || !GATED, "a gated stage has one k-block: its boxes are 2-D");
 };
 
 // 32 lanes x 16 consecutive columns: thread t receives lane (base + t).
@@ -196,7 +198,6 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
                     // both k-blocks in one box (a last odd one: zeros behind it)
                     expect_tx_f8(fb, C::STAGE);
                     tma_load_3d_f8(dst, wm, 0, nt * 128, kb, fb, pol_w);
-                    if constexpr (GATED) tma_load_3d_f8(dst + KPS * kWTile, wm, 0, p.n + nt * 128, kb, fb, pol_w);
                     tma_load_3d_f8(dst + kXAt, xm, 0, row0, kb, fb, pol_x);
                 } else {
                     const int count = min(KPS, run.count - j);
@@ -458,11 +459,10 @@ cudaError_t launch_t(F8Args a, int sm_count, cudaStream_t stream) {
     const int total = a.shards * ((a.kblocks + 3) / 4);
     int room = 0;
     if ((e = clusters(1, &room)) != cudaSuccess) return e;
-    const bool fit = C::SHARED == 0 || tiles <= room;
     if ((e = f8_ranges(tiles, total, sm_count, clusters, &a.splits)) != cudaSuccess) return e;
-    const bool alone = fit && (C::SHARED == 0 || C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
+    // (room is every SM, and clusters have an SM for every block: with one k-block a stage a split tile is always alone)
+    const bool alone = tiles <= room && (C::KPS == 1 || (total + a.splits - 1) / a.splits > 2);
     a.stages = alone ? C::ALONE : C::SHARED;
-    if (a.splits > 1 && a.stages * C::STAGE < C::SUMS + C::PARTS) return cudaErrorInvalidConfiguration;    // (never: see SlabCfg)
     const long long blocks = static_cast<long long>(a.n_tiles) * (a.op == OP_AG ? a.R : 1) * a.shards * a.kblocks;      // of weights
     const long long ahead = kAheadBytes / (C::WT * kWTile);
     a.ahead = pdl_launch() && a.m_tiles == 1 && 4 * blocks >= 5 * ahead ? static_cast<int>(ahead / (tiles * a.splits)) : 0;

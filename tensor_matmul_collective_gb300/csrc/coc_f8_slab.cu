@@ -491,35 +491,9 @@ cudaError_t launch_n(const F8Args& a, int nt, int sm_count, cudaStream_t stream)
 
 }  // namespace
 
-// Tiles of CTA pairs or slabs of weight rows, by the time either takes for its
-// rounds of k-blocks (us, measured): a tile 6 and 0.31 a k-block (summed over
-// ranks 7, gated 8), a slab of 128 rows (gated: of 64) 5 and 0.28 (0.39) where it
-// has an SM to itself, 0.5 (0.83) where two share one, and 2.5 to join ranges.  Over
-// 700 random sizes that costs 0.5% against the better one of each.  Up to 128 rows
-// (gated: 64) the weights' bytes decide, and slabs stream them better.  Measured,
-// slab / tile: n 8192, k 8 x 3584, m 128 43 / 78 us, 256 68 / 80, 384 109 / 93, 4096
-// 816 / 574; n 1024, k 4096, m 512 9.6 / 15.1, 2048 13.8 / 15.2, 4096 22.6 / 17.1; n
-// 4096, k 1024, m 512 8.2 / 9.0, 1024 10.5 / 9.6; n 2 x 1384, m 666, k 4096 15.3 / 15.8,
-// 4112 21.7 / 18.5, 4128 17.0 / 16.4; gated, 8 x 3584, k 8192, m 64 81 / 88, 96 110 /
-// 90, 4096 1807 / 1049; 1376, k 4096, m 128 10.4 / 16.5, 512 17.8 / 17.2; 3584, k 8192,
-// m 128 19.3 / 27.4, 256 28.1 / 27.5.
 bool f8_use_tiles(int op, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
     if (const char* e = std::getenv("COC_F8_TILE")) return std::atoi(e) != 0;
-    const int64_t slab_m = gated ? 64 : 128;
-    if (m <= slab_m) return false;
-    const int64_t ranks = op == OP_AG ? R : 1, blocks = (k + 127) / 128 * (op == OP_AG ? 1 : R), n_tiles = (n + 127) / 128;
-    const int64_t units = (m + 255) / 256 * (gated ? n_tiles : (n_tiles + 1) / 2) * ranks, slabs = (m + slab_m - 1) / slab_m * n_tiles * ranks;
-    const int64_t runs = ((k + 127) / 128 + 3) / 4 * (op == OP_AG ? 1 : R);
-    const int64_t pairs = std::max(1, sm_count / 2), split = std::max<int64_t>(1, std::min<int64_t>({8, sm_count / slabs, runs}));
-    const int64_t rounds = slabs <= sm_count ? 1 : (slabs + 2 * sm_count - 1) / (2 * sm_count);
-    // rows that start between L2's sectors (16 bytes) or lines are fetched in more of them, which costs slabs the more the
-    // more SMs fetch
-    const double fill = std::min(1.0, static_cast<double>(slabs * split) / sm_count);
-    const double tile_rows = k % 32 ? 1.25 : k % 128 ? 1.03 : 1.0, slab_rows = 1.0 + (k % 32 ? 0.6 : k % 128 ? 0.1 : 0.0) * fill;
-    const double each = slabs <= sm_count ? (gated ? 0.39 : 0.28) : (gated ? 0.83 : 0.5);
-    const double tile = (gated ? 8.0 : op != OP_AG && R > 1 ? 7.0 : 6.0) + 0.31 * tile_rows * static_cast<double>((units + pairs - 1) / pairs * blocks);
-    const double slab = 5.0 + each * slab_rows * static_cast<double>(rounds * blocks) / static_cast<double>(split) + (split > 1 ? 2.5 : 0.0);
-    return tile < slab;
+    return f8_tiles_sooner(op == OP_AG, gated, R, m, n, k, sm_count);
 }
 
 // (gated slabs have two weight tiles: 128 rows of both would leave no ring)

@@ -5,6 +5,8 @@ import subprocess
 
 import pytest
 
+import __graft_entry__ as entry
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "tensor_matmul_collective_gb300", "csrc")
 SHIM = """
 #include "coc_f8_plan.h"
@@ -20,6 +22,7 @@ extern "C" int ranges(long long tiles, int total, int sms, const int* room, int*
         return 0;
     }, out);
 }
+extern "C" int tiles(int gathers, int gated, int R, long long m, long long n, long long k) { return coc::f8_tiles_sooner(gathers, gated, R, m, n, k, 152); }
 """
 
 
@@ -67,3 +70,12 @@ def test_an_error_is_handed_on_and_not_remembered(shim):
     asked = (ctypes.c_int * 9)()
     assert ranges(shim, 1, 2, [0, 152, -7] + [0] * 6, asked)[0] == 7
     assert ranges(shim, 1, 2, ROOM, asked) == (0, 2) and asked[2] == 2
+
+
+def test_smoke_runs_both_kernels(shim):
+    """The products of smoke()'s feed-forward block: slabs at its first number of rows, tiles of CTA pairs at its second, by the rule."""
+    R, hidden, f = entry.SMOKE_MLP["R"], entry.SMOKE_MLP["hidden"], entry.SMOKE_MLP["ffn"] // entry.SMOKE_MLP["R"]
+    for rows, want in zip(entry.SMOKE_MLP["rows"], (0, 1)):
+        m = ctypes.c_longlong(R * rows)
+        assert shim.tiles(1, 1, R, m, ctypes.c_longlong(f), ctypes.c_longlong(hidden)) == want
+        assert shim.tiles(0, 0, R, m, ctypes.c_longlong(hidden), ctypes.c_longlong(f)) == want

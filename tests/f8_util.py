@@ -105,3 +105,51 @@ def product(xs, x_scales, ws, w_scales):
 def sum_error(size, K, splits=8):
     """fp32 sums of exact products, 32 at a time and `splits` ranges joined: 2**-22 a step covers an addition that truncates."""
     return (K / 32 + splits + 8) * 2.0 ** -22 * size + 2.0 ** -140
+
+
+# ---- the same on the GPU, for sizes that take the CPU too long
+
+def _value_on(scale):
+    b = scale.view(torch.uint8).to(torch.int64)
+    return torch.where(b == 255, torch.full((), float("nan"), dtype=torch.float64, device=scale.device), pow2(b - 127))
+
+
+def real_on(codes, scale, rows=1):
+    """float64 values where they lie: of an activation, or (rows = 128) of a weight."""
+    return codes.double() * spread(_value_on(scale), codes.shape[1]).repeat_interleave(rows, 0)[:codes.shape[0]]
+
+
+def product_on(xs, x_scales, ws, w_scales):
+    """product() on the GPU."""
+    y = size = 0.0
+    for x, xs_, w, ws_ in zip(xs, x_scales, ws, w_scales):
+        a, b = real_on(x, xs_), real_on(w, ws_, 128)
+        y = y + a @ b.t()
+        size = size + a.abs() @ b.abs().t()
+    return y, size
+
+
+def course(xs, x_scales, ws, w_scales, each=16):
+    """(sums, largest partial sum, largest product's bound, steps of 32) of every output, on the GPU, in the order of the kernels'
+    one-range sums: rank after rank, k ascending."""
+    y, top, most, steps = 0.0, 0.0, 0.0, 0
+    for x, xs_, w, ws_ in zip(xs, x_scales, ws, w_scales):
+        a, b = real_on(x, xs_), real_on(w, ws_, 128)
+        pad = (0, -a.shape[1] % 32)
+        a = torch.nn.functional.pad(a, pad).view(a.shape[0], -1, 32).transpose(0, 1)
+        b = torch.nn.functional.pad(b, pad).view(b.shape[0], -1, 32).transpose(0, 1)
+        steps += a.shape[0]
+        for i in range(0, a.shape[0], each):
+            p, q = a[i:i + each], b[i:i + each]
+            part = torch.bmm(p, q.transpose(1, 2)).cumsum(0) + y
+            y = part[-1].clone()
+            top = torch.maximum(part.abs().amax(0), torch.as_tensor(top, dtype=torch.float64, device=y.device))
+            here = (p.abs().amax(2)[:, :, None] * q.abs().amax(2)[:, None, :]).amax(0)
+            most = torch.maximum(here, torch.as_tensor(most, dtype=torch.float64, device=y.device))
+    return y, top, most, steps
+
+
+def course_error(top, most, steps):
+    """A step adds 32 products to the sum: the addends are cut at 2**-25 of the largest of them, the sum to 24 bits (2**-23),
+    towards zero.  A range of the steps has partial sums of up to 2 top; 8 ranges are joined in 2**-24 each."""
+    return (steps * (33 * 2.0 ** -25 + 2.0 ** -23) + 8 * 2.0 ** -24) * (2 * top + most) + 2.0 ** -140

@@ -376,12 +376,17 @@ __global__ void __launch_bounds__(kSlabThreads) f8_slab_kernel(const __grid_cons
         const bool in = o < own && col < p.n;
         if constexpr (GATED) {
             // (all eight at once, whatever comes of them: with the test in front they took turns, 110 cycles each)
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[0][j] = f8_gated(y[0][j], y[1][j]);
+            float top = 0.f, h[8];
+            uint32_t g[8], u[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                y[0][j] = in ? y[0][j] : 0.f;
+                g[j] = __float_as_uint(y[0][j]);
+                u[j] = __float_as_uint(y[1][j]);
+            }
+            f8_gated(g, u, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                y[0][j] = in ? h[j] : 0.f;
                 top = fmaxf(top, f8_magnitude(y[0][j]));
             }
 #pragma unroll

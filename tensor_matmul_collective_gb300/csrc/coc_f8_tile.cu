@@ -251,11 +251,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) f8_tile_kernel(const __grid_c
                     load(acc + 128 + 32 * j, up);
                     tmem_wait_ld();
                     if (s == 0) release();
+                    f8_gated(g, up, h + 32 * s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float v = f8_gated(__uint_as_float(g[i]), __uint_as_float(up[i]));
-                        h[32 * s + i] = col0 + 32 * j + i < p.n ? v : 0.f;
-                    }
+                    for (int i = 0; i < 32; ++i) h[32 * s + i] = col0 + 32 * j + i < p.n ? h[32 * s + i] : 0.f;
                 }
                 float top = 0.f;
 #pragma unroll

@@ -37,3 +37,25 @@ def test_gate_over_the_whole_range(monkeypatch, tile, exp):
     # the result; 2^x, the reciprocal and the products 2**-20 more: less than 2**-15 in all.  From g = -170 on nothing is
     # left of 2^-246 and 2^7 for g: with u < 2^121, less than half of the least code, 2**-110
     f8.check_codes(got[0], got_scales[0], h, 2.0 ** -15 * h.abs() + (h.abs() < 2.0 ** -110) * 2.0 ** -110)
+
+
+@pytest.mark.parametrize("tile", ["0", "1"])
+def test_far_gates_leave_the_others_their_bits(monkeypatch, tile):
+    """One row whose gates are far out among ordinary rows, which share its warps."""
+    monkeypatch.setenv("COC_F8_TILE", tile)
+    g = torch.Generator().manual_seed(2)
+    k, f, rows = 256, 272, 70
+    w = torch.randn(2 * f, k, generator=g)
+    w[:f, 0], w[f:, 0] = -8.0, 1.0
+    x = torch.randn(rows, k, generator=g)
+    x[:, 0] = 0.0
+    wc, ws = coc.f8_pack(w, 2)
+    got = []
+    for first in (0.0, 32.0):                       # row 40: gates near -256
+        x[40, 0] = first
+        c, s = f8.quantize(x.double())
+        codes, scales = coc.all_gather_gated_matmul_f8([c.to(DEV)], [s.to(DEV)], [wc.to(DEV)], [ws.to(DEV)])
+        got.append(torch.cat([codes[0].cpu().view(torch.uint8), scales[0].cpu().view(torch.uint8)], 1))
+    coc.sync_status()
+    other = torch.arange(rows) != 40
+    assert torch.equal(got[0][other], got[1][other]) and not torch.equal(got[0][40], got[1][40])

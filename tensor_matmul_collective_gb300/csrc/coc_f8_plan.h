@@ -38,15 +38,17 @@ auto f8_ranges(long long tiles, int total, int sm_count, Room&& room, int* range
 // Tiles of CTA pairs or slabs of weight rows, by the time either takes for its
 // rounds of k-blocks (us, measured): a tile 6 and 0.31 a k-block (summed over
 // ranks 7, gated 8), a slab of 128 rows (gated: of 64) 5 and 0.28 (0.39) where it
-// has an SM to itself, 0.5 (0.83) where two share one, and 2.5 to join ranges.  Over
-// 700 random sizes that costs 0.5% against the better one of each.  Up to 128 rows
-// (gated: 64) the weights' bytes decide, and slabs stream them better.  Measured,
-// slab / tile: n 8192, k 8 x 3584, m 128 43 / 78 us, 256 68 / 80, 384 109 / 93, 4096
-// 816 / 574; n 1024, k 4096, m 512 9.6 / 15.1, 2048 13.8 / 15.2, 4096 22.6 / 17.1; n
-// 4096, k 1024, m 512 8.2 / 9.0, 1024 10.5 / 9.6; n 2 x 1384, m 666, k 4096 15.3 / 15.8,
-// 4112 21.7 / 18.5, 4128 17.0 / 16.4; gated, 8 x 3584, k 8192, m 64 81 / 88, 96 110 /
-// 90, 4096 1807 / 1049; 1376, k 4096, m 128 10.4 / 16.5, 512 17.8 / 17.2; 3584, k 8192,
-// m 128 19.3 / 27.4, 256 28.1 / 27.5.
+// has an SM to itself, 0.5 (0.83) where two share one, and 2.5 to join ranges.  Up
+// to 128 rows (gated: 64) the weights' bytes decide, and slabs stream them better.
+// Over 3253 random sizes above that the rule costs 0.7% against the better one of
+// each; 2.6% of them lose more than 7%, mostly under 10 us, the worst 31% (n 12960, k
+// 736, m 546: 17.2 / 13.1). Measured, slab / tile (us): n 8192, k 8 x 3584, m 64 38 /
+// 74, 128 42 / 79, 256 65 / 81, 384 106 / 88, 512 117 / 94, 1024 223 / 178, 4096 858 / 592;
+// n 1024, k 4096, m 512 9.6 / 15.1, 2048 13.0 / 15.7, 4096 21.9 / 17.7; n 4096, k 1024, m 512
+// 7.6 / 9.5, 1024 10.1 / 10.2; n 2 x 1384, m 666, k 4096 13.0 / 16.0, 4112 19.2 / 18.5,
+// 4128 14.6 / 16.4; gated, 8 x 3584, k 8192, m 64 76 / 83, 96 106 / 85, 256 151 / 92,
+// 4096 2075 / 1206; 1376, k 4096, m 64 9.6 / 17.1, 128 10.0 / 17.1, 512 15.8 / 17.8; 3584, k
+// 8192, m 128 18.4 / 27.6, 256 26.0 / 28.0 (tiles are taken there).
 inline bool f8_tiles_sooner(bool gathers, bool gated, int R, int64_t m, int64_t n, int64_t k, int sm_count) {
     const int64_t slab_m = gated ? 64 : 128;
     if (m <= slab_m) return false;

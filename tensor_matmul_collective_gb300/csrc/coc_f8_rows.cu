@@ -9,9 +9,12 @@
 // What bounds it.  Every value is read and written once: 7 bytes a value with
 // residual and sum, 3 without.  A row stays in registers between the sum of
 // squares and the scaling, so HBM is the bound: 8 x 1024 rows of 8192 with
-// residual take 70 us, 6.7 TB/s (a copy: 6.8); quantised alone, 2 x 4095 rows of
-// 3584 15.1 us, 5.8 TB/s (instructions: 100 for 24 bytes a lane); one row 2.8 us,
-// the launch and one chain of load, sum and store.
+// residual take 69.3 us, 6.8 TB/s (a copy: 6.8); quantised alone, 2 x 4095 rows of
+// 3584 15.0 us, 5.9 TB/s (instructions: 100 for 24 bytes a lane); one row 2.8 us,
+// the launch and one chain of load, sum and store.  Rows that do not fill whole
+// waves of blocks wait for the last (2 x 777 of 5008, fp16, 7.4 us, 3.2 TB/s). Rows
+// beyond 16384 have one block on an SM (4096 of 32768 178 us, 5.3 TB/s), beyond 32768 also
+// more than 128 registers a thread (560 bytes spilled; 2048 of 65536 338 us, 2.8 TB/s).
 //
 // Layout.  16 lanes hold a block of 128 (8 values, 16 bytes each), so its
 // largest magnitude is four shuffles away and codes go out 8 bytes a lane.

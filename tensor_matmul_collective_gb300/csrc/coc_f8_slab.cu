@@ -9,7 +9,7 @@
 //
 // What bounds it.  n k bytes of weights, read once: n 8192, k 8 x 3584, 64 rows
 // on 8 ranks take 38 us, 6.4 TB/s with the outputs; gated 8 x 3584, k 8192, 64 rows
-// 75 to 77 us, 6.2 TB/s; gated 11008, k 4096, one row 17.1 to 17.6 us, 5.2 TB/s; n
+// 74 to 79 us, 6.0 to 6.4 TB/s; gated 11008, k 4096, one row 16.9 to 17.8 us, 5.2 TB/s; n
 // 4096, k 4096, one row 5.5 us, of which the weights' bytes are 2.5.  A tile is 128
 // weight rows by NT activation rows, so few rows cost the tensor cores little (a
 // product of 32 of k takes 40 cycles with 16 rows, 65 with 128).
@@ -40,8 +40,8 @@ constexpr int kSlabThreads = 256;
 constexpr int kMaxStages = 8;
 // Weights that all blocks together ask L2 for ahead of their turn, where there
 // are 40 MiB of them and one row tile: calls that follow each other, n 8192, k 8 x
-// 3584, m 64 39.4 to 37.6 us, gated 8 x 3584, k 8192, m 64 77.1 to 74.9, 11008, k 4096,
-// m 1 18.1 to 17.1 (16 MiB: 38.0, 75.7, 17.2; 64: 40.0, 76.9, 18.5); with less, n
+// 3584, m 64 39.0 to 37.7 us, gated 8 x 3584, k 8192, m 64 78.6 to 74.9, 11008, k 4096,
+// m 1 18.2 to 17.1 (16 MiB: 37.8, 77.5, 17.2; 64: 39.5, 75.8, 18.5); with less, n
 // 8192, k 4096, m 16 8.2 to 8.9.
 constexpr long long kAheadBytes = 32LL << 20;
 constexpr int kSfStages = 4;            // scale words: runs of up to 4 k-blocks in flight, in shared and in tensor memory
@@ -515,16 +515,19 @@ int f8_slab_kblocks(int64_t m, bool gated) {
     }
 }
 
-// Blocks.  Where the tiles leave SMs free, a tile's contraction is cut into as
+// Where the tiles leave SMs free, a tile's contraction is cut into as
 // many ranges (2 to 8) as clusters of that size find an SM for every block: a
 // block alone on an SM has all its shared memory for the ring.  More tiles
 // than SMs go unsplit, two blocks on an SM, which overlaps one's beginning and end
 // with the other's middle.  So do blocks of up to 8 k-blocks: the next launch's
-// set themselves up beside them (n 4096, k 4096, m 1 6.8 to 6.2 us).  Measured,
-// ranges 1 / 2 / 4 / 8, alone: n 4096, k 4096, m 1 9.6 / 7.6 / 7.0 / 17.5 us; n 8192, k 8 x 3584, m 64 49 / 41 / 49 / 76 (shared 70 /
-// 47 / 44 / 55); n 14336, k 8 x 7168, m 16 120 / 128 / 144 / 162 (shared 148 / 127 /
-// 132 / 151); n 1024, k 2 x 8192, m 16 27 / 17 / 12 / 9.0.  Gated, 8 x 3584, k 8192, m
-// 64: shared 84 unsplit, 92 in two, alone 88.
+// set themselves up beside them.  Measured, ranges 1 / 2 / 4 / 8 (us, graphs of calls
+// in a row), alone on an SM and two to an SM:
+//   n 4096, k 4096, m 1          9.6 / 6.9 / 6.0 / 11.6    9.6 / 6.8 / 5.5 (taken) / 7.5
+//   n 4096, k 4096, m 64         10.3 / 8.2 / 7.3 / 16.4   10.8 / 8.4 / 7.0 (taken) / 8.9
+//   n 8192, k 8 x 3584, m 64     51 / 37.6 (taken) / 42 / 60   71 / 45 / 38.4 / 43
+//   n 14336, k 8 x 7168, m 16    117 (taken) / 125 / 131 / 144   147 / 121 / 126 / 136
+//   n 1024, k 2 x 8192, m 16     29 / 16.5 / 10.9 / 8.2 (taken)   38 / 22 / 13.0 / 9.1
+//   gated, 8 x 3584, k 8192, m 64   77 / 81   75 to 77 (taken), not split
 cudaError_t launch_f8_slab(const F8Args& args, bool gated, bool bf16, int sm_count, cudaStream_t stream) {
     F8Args a = args;
     const int nt = f8_slab_rows(a.m, gated);

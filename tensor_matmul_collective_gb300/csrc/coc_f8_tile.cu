@@ -6,10 +6,10 @@
 //
 // What bounds it.  The tensor cores: a k-block of a pair is four products of
 // 256 x 256 x 32, 512 cycles, and 32 KiB of copies a CTA, 64 bytes a cycle.  Gated, 8
-// x 3584, k 8192, 4096 rows: 1049 us for a short while (3.67 PFLOP/s; tensor
-// pipes 83% active under the profiler at 1.68 GHz, 13.9 TB/s out of L2), 1220 to
+// x 3584, k 8192, 4096 rows: 1054 to 1069 us for a short while (3.6 PFLOP/s; tensor
+// pipes 82% active under the profiler at 1.69 GHz, 13.9 TB/s out of L2), 1190 to
 // 1250 in a long loop, where the GPU's power holds the clock at 1.4 GHz; n 8192, k 8
-// x 3584, 4096 rows scattered: 537 and 640 us.  With a quarter of the copies
+// x 3584, 4096 rows scattered: 548 and 620 to 643 us.  With a quarter of the copies
 // left out (wrong results) the loops take 1179 and 563 us: what moves between L2
 // and the SMs costs both time and power.
 //

@@ -41,7 +41,7 @@ auto f8_ranges(long long tiles, int total, int sm_count, Room&& room, int* range
 // has an SM to itself, 0.5 (0.83) where two share one, and 2.5 to join ranges.  Up
 // to 128 rows (gated: 64) the weights' bytes decide, and slabs stream them better.
 // Over 3253 random sizes above that the rule costs 0.7% against the better one of
-// each; 2.6% of them lose more than 7%, mostly under 10 us, the worst 31% (n 12960, k
+// each; 2.6% of them lose more than 7%, most in 7 to 11 us, the worst 31% (n 12960, k
 // 736, m 546: 17.2 / 13.1). Measured, slab / tile (us): n 8192, k 8 x 3584, m 64 38 /
 // 74, 128 42 / 79, 256 65 / 81, 384 106 / 88, 512 117 / 94, 1024 223 / 178, 4096 858 / 592;
 // n 1024, k 4096, m 512 9.6 / 15.1, 2048 13.0 / 15.7, 4096 21.9 / 17.7; n 4096, k 1024, m 512
